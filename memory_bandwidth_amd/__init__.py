@@ -33,6 +33,13 @@ EXPORTS = ("gemv_q4", "gemv_q4_ws", "gemv_q4_workspace_size", "gemv_q4_static", 
            "block_geometry", "gemv_block", "dequant_block", "gemv_block_set_config",
            "gemv_block_config", "scan2", "scan2_set_config", "scan2_config")
 
+# Exported C symbols, in the order include/q4i8.h declares them.
+EXPORTS_I8 = ("quant_i8", "gemm_i8", "gemm_i8_swiglu", "gemm_i8_grouped", "gemm_i8_grouped_swiglu")
+
+# Element types of include/q4i8.h.
+I8_F32, I8_F16, I8_BF16 = 0, 1, 2
+I8_TYPES = {torch.float32: I8_F32, torch.float16: I8_F16, torch.bfloat16: I8_BF16}
+
 # Block formats of include/q4blocks.h.
 BLK_Q4_0, BLK_Q8_0, BLK_Q4_K, BLK_Q5_K, BLK_Q6_K = 1, 2, 3, 4, 5
 BLOCK_FORMATS = {"q4_0": BLK_Q4_0, "q8_0": BLK_Q8_0, "q4_k": BLK_Q4_K, "q5_k": BLK_Q5_K,
@@ -83,6 +90,13 @@ def lib() -> ctypes.CDLL:
     L.scan2.argtypes = [P, P, P, I, I, I, P]
     L.scan2_set_config.argtypes = [I, I, I, I]
     L.scan2_config.argtypes = [IP, IP, IP, IP]
+    L.quant_i8.argtypes = [P, I, P, P, I, I, P]
+    L.gemm_i8.argtypes = [P, P, P, P, P, P, I, I, I, I, P]
+    L.gemm_i8_swiglu.argtypes = [P, P, P, P, P, P, P, I, I, I, I, P]
+    L.gemm_i8_grouped.argtypes = [P, P, P, P, P, P, I, I, I, I, I, P]
+    L.gemm_i8_grouped_swiglu.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, I, P]
+    for f in EXPORTS_I8:
+        getattr(L, f).restype = ctypes.c_int
     L.q4_strerror.argtypes = [I]
     L.q4_strerror.restype = ctypes.c_char_p
     L.q4_abi_version.argtypes = []
@@ -416,3 +430,153 @@ def scan2_config() -> tuple[int, int, int, int]:
     v = [ctypes.c_int() for _ in range(4)]
     _check("scan2_config", lib().scan2_config(*[ctypes.byref(t) for t in v]))
     return tuple(t.value for t in v)
+
+
+# ---------------------------------------------------------------- 8-bit activations and weights
+
+def _i8_type(dtype, name: str) -> int:
+    if dtype not in I8_TYPES:
+        raise TypeError(f"{name} must be float32, float16 or bfloat16, got {dtype}")
+    return I8_TYPES[dtype]
+
+
+def _i8_call(fn: str, dev: torch.device, *args) -> None:
+    """Calls the entry point on dev's current stream, with dev current."""
+    if dev.index == torch.cuda.current_device():
+        _check(fn, getattr(lib(), fn)(*args, torch.cuda.current_stream(dev).cuda_stream))
+        return
+    with torch.cuda.device(dev):
+        _check(fn, getattr(lib(), fn)(*args, torch.cuda.current_stream(dev).cuda_stream))
+
+
+def _i8_rows(a: torch.Tensor, a_scales: torch.Tensor) -> tuple[int, int]:
+    _need(a, "a", (torch.int8,))
+    _need(a_scales, "a_scales", (torch.float32,), a.device)
+    if a.dim() != 2 or tuple(a_scales.shape) != (a.shape[0],):
+        raise ValueError(f"a must be [M, K] and a_scales [M]: got {tuple(a.shape)}, {tuple(a_scales.shape)}")
+    return a.shape[0], a.shape[1]
+
+
+def _i8_matrix(w: torch.Tensor, w_scales: torch.Tensor, shape, name: str) -> None:
+    """w int8 [..., N, K] and w_scales float32 [..., N]; shape is w's, None where any size will do."""
+    _need(w, name, (torch.int8,))
+    _need(w_scales, f"{name}'s scales", (torch.float32,), w.device)
+    if (w.dim() != len(shape) or any(s is not None and s != n for s, n in zip(shape, w.shape))
+            or w_scales.shape != w.shape[:-1]):
+        want = "[" + ", ".join("*" if s is None else str(s) for s in shape) + "]"
+        raise ValueError(f"{name} must be {want} with a scale for each row: got {tuple(w.shape)}, "
+                         f"{tuple(w_scales.shape)}")
+
+
+def _i8_out(out: torch.Tensor | None, M: int, N: int, dtype, dev: torch.device) -> torch.Tensor:
+    if out is None:
+        return torch.empty((M, N), dtype=dtype, device=dev)
+    _need(out, "out", (dtype,), dev)
+    if tuple(out.shape) != (M, N):
+        raise ValueError("out must be [M, N]")
+    return out
+
+
+def quant_i8(x: torch.Tensor, out: tuple | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+    """(codes int8 [M, K], scales float32 [M]) of x [M, K], float32, float16 or
+    bfloat16: scales[m] = max|x[m]| / 127 and codes = x / scales to the nearest
+    integer.  K is a multiple of 16.  A row with an Inf or a NaN gets the scale
+    NaN and zero codes."""
+    _need(x, "x", tuple(I8_TYPES))
+    if x.dim() != 2:
+        raise ValueError("x must be [M, K]")
+    M, K = x.shape
+    if out is None:
+        codes = torch.empty((M, K), dtype=torch.int8, device=x.device)
+        scales = torch.empty(M, dtype=torch.float32, device=x.device)
+    else:
+        codes, scales = out
+        _need(codes, "codes", (torch.int8,), x.device)
+        _need(scales, "scales", (torch.float32,), x.device)
+        if tuple(codes.shape) != (M, K) or tuple(scales.shape) != (M,):
+            raise ValueError("out must be codes [M, K] and scales [M]")
+    _i8_call("quant_i8", x.device, _ptr(x), I8_TYPES[x.dtype], _ptr(codes), _ptr(scales), M, K)
+    return codes, scales
+
+
+def gemm_i8(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
+            bias: torch.Tensor | None = None, dtype=torch.float32,
+            out: torch.Tensor | None = None) -> torch.Tensor:
+    """y[M, N] = (a[M, K] . w[N, K]^T) * a_scales[M] * w_scales[N] (+ bias[N]), the sums exact."""
+    M, K = _i8_rows(a, a_scales)
+    dev = a.device
+    _i8_matrix(w, w_scales, (None, K), "w")
+    N = w.shape[0]
+    if w.device != dev:
+        raise ValueError(f"w is on {w.device}, expected {dev}")
+    if bias is not None:
+        _need(bias, "bias", (torch.float32,), dev)
+        if tuple(bias.shape) != (N,):
+            raise ValueError("bias must be [N]")
+    t = _i8_type(dtype, "dtype")
+    out = _i8_out(out, M, N, dtype, dev)
+    _i8_call("gemm_i8", dev, _ptr(a), _ptr(a_scales), _ptr(w), _ptr(w_scales), _ptr(bias), _ptr(out), t, M, N, K)
+    return out
+
+
+def _i8_pair(a: torch.Tensor, gate: tuple, up: tuple, shape) -> int:
+    (wg, sg), (wu, su) = gate, up
+    _i8_matrix(wg, sg, shape, "gate")
+    _i8_matrix(wu, su, tuple(wg.shape), "up")
+    if wg.device != a.device or wu.device != a.device:
+        raise ValueError(f"gate and up must be on {a.device}")
+    return wg.shape[-2]
+
+
+def gemm_i8_swiglu(a: torch.Tensor, a_scales: torch.Tensor, gate: tuple, up: tuple,
+                   dtype=torch.float32, out: torch.Tensor | None = None) -> torch.Tensor:
+    """y = silu(g) * u with g, u the gemm_i8 of a with gate and up, each (w, w_scales)."""
+    M, K = _i8_rows(a, a_scales)
+    N = _i8_pair(a, gate, up, (None, K))
+    t = _i8_type(dtype, "dtype")
+    out = _i8_out(out, M, N, dtype, a.device)
+    (wg, sg), (wu, su) = gate, up
+    _i8_call("gemm_i8_swiglu", a.device, _ptr(a), _ptr(a_scales), _ptr(wg), _ptr(sg), _ptr(wu), _ptr(su), _ptr(out),
+             t, M, N, K)
+    return out
+
+
+def _i8_offsets(offsets: torch.Tensor, dev: torch.device) -> int:
+    _need(offsets, "offsets", (torch.int32,), dev)
+    if offsets.dim() != 1 or offsets.numel() < 2:
+        raise ValueError("offsets must be [E + 1] with E >= 1")
+    return offsets.numel() - 1
+
+
+def gemm_i8_grouped(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
+                    offsets: torch.Tensor, dtype=torch.float32,
+                    out: torch.Tensor | None = None) -> torch.Tensor:
+    """The gemm_i8 of rows offsets[e] .. offsets[e + 1] of a with matrix e of w
+    [E, N, K], w_scales [E, N].  offsets is int32 [E + 1] on the GPU.  Rows
+    outside every group are not written."""
+    M, K = _i8_rows(a, a_scales)
+    E = _i8_offsets(offsets, a.device)
+    _i8_matrix(w, w_scales, (E, None, K), "w")
+    if w.device != a.device:
+        raise ValueError(f"w is on {w.device}, expected {a.device}")
+    N = w.shape[1]
+    t = _i8_type(dtype, "dtype")
+    out = _i8_out(out, M, N, dtype, a.device)
+    _i8_call("gemm_i8_grouped", a.device, _ptr(a), _ptr(a_scales), _ptr(w), _ptr(w_scales), _ptr(offsets), _ptr(out),
+             t, M, E, N, K)
+    return out
+
+
+def gemm_i8_grouped_swiglu(a: torch.Tensor, a_scales: torch.Tensor, gate: tuple, up: tuple,
+                           offsets: torch.Tensor, dtype=torch.float32,
+                           out: torch.Tensor | None = None) -> torch.Tensor:
+    """gemm_i8_swiglu of rows offsets[e] .. offsets[e + 1] with matrices e of gate and up."""
+    M, K = _i8_rows(a, a_scales)
+    E = _i8_offsets(offsets, a.device)
+    N = _i8_pair(a, gate, up, (E, None, K))
+    t = _i8_type(dtype, "dtype")
+    out = _i8_out(out, M, N, dtype, a.device)
+    (wg, sg), (wu, su) = gate, up
+    _i8_call("gemm_i8_grouped_swiglu", a.device, _ptr(a), _ptr(a_scales), _ptr(wg), _ptr(sg), _ptr(wu), _ptr(su),
+             _ptr(offsets), _ptr(out), t, M, E, N, K)
+    return out

@@ -1,0 +1,395 @@
+"""GPU parity of the 8-bit operators against the 64-bit oracle, through the
+Python binding.
+
+Codes and token scales are compared exactly.  Products are held to the
+oracle's bound (the fp32 roundings that include/q4i8.h allows) plus half a
+step of the output's type.  Sizes cover one row to many, rows and columns that
+end inside a tile, K that ends inside a step, and groups that are empty, of
+one row, or cross tiles.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import memory_bandwidth_amd as q4
+from oracle import i8
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+TYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+
+
+def dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).to(DEV)
+
+
+def codes(seed, *shape):
+    """Every int8 value, -128 among them."""
+    return np.random.default_rng(seed).integers(-128, 128, shape, dtype=np.int8)
+
+
+def scales(seed, *shape):
+    return np.random.default_rng(seed).uniform(0.0005, 0.02, shape).astype(np.float32)
+
+
+def small_scales(seed, K, *shape):
+    """Scales that bring products of random codes near 1, whatever K."""
+    return (np.random.default_rng(seed).uniform(0.5, 2, shape) / (74 * K ** 0.25)).astype(np.float32)
+
+
+def check(y, want, bound, t, label):
+    got = y.float().cpu().numpy().astype(np.float64)
+    tol = i8.tolerance(want, bound, t)
+    bad = ~(np.abs(got - want) <= tol)
+    assert not bad.any(), (f"{label}: {int(bad.sum())} of {bad.size} outside, first at {np.argwhere(bad)[0]}, worst "
+                           f"{np.nanmax(np.abs(got - want) / tol):.3g} of the tolerance")
+
+
+# ---------------------------------------------------------------- quant_i8
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("M,K", [(1, 16), (3, 48), (65, 128), (7, 896), (33, 1040), (2, 4096), (5, 14336), (3, 32784),
+                                 (1, 131056), (1030, 272)])
+def test_quant(t, M, K):
+    x = torch.from_numpy(np.random.default_rng(M * K).standard_normal((M, K)).astype(np.float32)).to(TYPES[t])
+    x[:, 5] *= 11
+    c, s = q4.quant_i8(x.to(DEV))
+    cw, sw = i8.quant(x.double().numpy())
+    assert np.array_equal(s.cpu().numpy(), sw)
+    assert np.array_equal(c.cpu().numpy(), cw)
+
+
+@pytest.mark.parametrize("t", TYPES)
+def test_quant_ties_and_special_rows(t):
+    K = 528
+    rng = np.random.default_rng(9)
+    x = np.zeros((12, K), dtype=np.float32)
+    x[0] = rng.integers(-254, 255, K) / 2                  # scale 1: half of the values are ties
+    x[0, 3] = 127
+    x[1] = rng.integers(-254, 255, K) * 0.375              # scale 0.75
+    x[1, 3] = -127 * 0.75
+    x[3] = rng.standard_normal(K)
+    x[3, 100] = np.inf
+    x[4] = rng.standard_normal(K)
+    x[4, K - 1] = np.nan
+    x[5, 0] = -np.inf
+    x[6] = rng.standard_normal(K) * 1e-6
+    x[7] = rng.standard_normal(K) * 100
+    x[8, 17] = 2.0 ** -24                                  # alone in its row
+    x[9] = 1.0
+    x[10, K - 1] = -3.0
+    x[11] = rng.standard_normal(K)
+    if t == "f32":
+        x[6] = rng.integers(-9, 10, K) * 2.0 ** -149       # subnormal
+        x[7] = rng.standard_normal(K) * 8e37
+        x[8] = rng.integers(-254, 255, K) * 2.0 ** -127    # scale 2^-126, ties
+        x[8, 1] = 127 * 2.0 ** -126
+    xt = torch.from_numpy(x).to(TYPES[t])
+    c, s = q4.quant_i8(xt.to(DEV))
+    cw, sw = i8.quant(xt.double().numpy())
+    assert np.array_equal(s.cpu().numpy(), sw, equal_nan=True)
+    assert np.array_equal(c.cpu().numpy(), cw)
+
+
+def test_quant_near_ties():
+    """Quotients within a few ulp of n + 1/2, on both sides and on it."""
+    K = 4096
+    rng = np.random.default_rng(4)
+    s = np.float32(0.0123456789)
+    x = ((rng.integers(-126, 126, K) + 0.5) * np.float64(s)).astype(np.float32)
+    x = (x.view(np.int32) + rng.integers(-2, 3, K).astype(np.int32)).view(np.float32)
+    x[0] = np.float32(127) * s
+    c, got = q4.quant_i8(dev(x[None]))
+    cw, sw = i8.quant(x[None].astype(np.float64))
+    assert np.array_equal(got.cpu().numpy(), sw) and np.array_equal(c.cpu().numpy(), cw)
+
+
+# ---------------------------------------------------------------- gemm_i8
+
+GEMM = [(1, 1, 16), (1, 17, 48), (1, 896, 896), (1, 300, 4096), (2, 64, 128), (3, 129, 144), (8, 1000, 1040),
+        (15, 33, 4096), (16, 16, 64), (17, 257, 272), (31, 130, 14336), (32, 512, 2816), (48, 100, 912),
+        (64, 64, 128), (65, 127, 256), (100, 896, 4864), (128, 256, 1024), (129, 300, 1040), (200, 333, 2064),
+        (256, 256, 256), (257, 511, 528), (300, 1024, 896), (511, 520, 4112), (700, 777, 1296), (1025, 1030, 400),
+        (2049, 260, 144), (260, 4100, 208)]
+
+
+@pytest.mark.parametrize("M,N,K", GEMM)
+@pytest.mark.parametrize("t", TYPES)
+def test_gemm(M, N, K, t):
+    a, w, sa, sw = codes(1, M, K), codes(2, N, K), small_scales(3, K, M), small_scales(4, K, N)
+    y = q4.gemm_i8(dev(a), dev(sa), dev(w), dev(sw), dtype=TYPES[t])
+    assert y.dtype == TYPES[t]
+    check(y, *i8.gemm(a, sa, w, sw), t, f"{M} {N} {K}")
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 77, 256), (40, 520, 144), (130, 64, 1024), (600, 515, 400)])
+@pytest.mark.parametrize("t", TYPES)
+def test_gemm_bias(M, N, K, t):
+    a, w, sa, sw = codes(1, M, K), codes(2, N, K), small_scales(3, K, M), small_scales(4, K, N)
+    b = np.random.default_rng(5).standard_normal(N).astype(np.float32) * 3
+    y = q4.gemm_i8(dev(a), dev(sa), dev(w), dev(sw), bias=dev(b), dtype=TYPES[t])
+    check(y, *i8.gemm(a, sa, w, sw, b), t, f"{M} {N} {K}")
+
+
+@pytest.mark.parametrize("M,N", [(1, 5), (20, 18), (70, 70), (300, 260)])
+def test_gemm_largest_sums(M, N):
+    """-128 x -128 at the longest K, and its negative: the sums reach 2147221504."""
+    K = 131056
+    a, w = np.full((M, K), -128, dtype=np.int8), np.full((N, K), -128, dtype=np.int8)
+    w[1::2] = 127
+    one = np.ones(max(M, N), dtype=np.float32)
+    y = q4.gemm_i8(dev(a), dev(one[:M]), dev(w), dev(one[:N])).cpu().numpy()
+    want = np.where(np.arange(N) % 2 == 0, 16384.0 * K, -128.0 * 127 * K).astype(np.float32)
+    assert np.array_equal(y, np.broadcast_to(want, (M, N)))
+
+
+@pytest.mark.parametrize("M", [1, 9, 40, 100, 600])
+def test_gemm_rows_do_not_mix(M):
+    """A NaN scale, a zero row and huge scales stay in their rows and columns."""
+    N, K = 150, 400
+    a, w, sa, sw = codes(1, M, K), codes(2, N, K), scales(3, M), scales(4, N)
+    a[M // 2] = 0
+    sa[M - 1] = np.nan
+    sw[3] = np.inf
+    want = i8.product(a, sa, w, sw)
+    y = q4.gemm_i8(dev(a), dev(sa), dev(w), dev(sw)).cpu().numpy()
+    assert np.array_equal(np.isnan(y), np.isnan(want)) and np.isnan(y[M - 1]).all()
+    fine = np.isfinite(want)
+    assert np.array_equal(fine, np.isfinite(y))
+    assert (np.abs(y[fine] - want[fine]) <= 4.1 * i8.U * np.abs(want[fine])).all()
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("M,N", [(1, 40), (5, 64), (70, 72), (300, 264)])
+@pytest.mark.parametrize("skew", [0, 1])
+def test_gemm_out_in_a_larger_buffer(t, M, N, skew):
+    """Outputs that start off a 16-byte border, with guards on both sides."""
+    K = 160
+    a, w, sa, sw = codes(1, M, K), codes(2, N, K), small_scales(3, K, M), small_scales(4, K, N)
+    buf = torch.full((M * N + 32,), 7.0, dtype=TYPES[t], device=DEV)
+    out = buf[8 + skew:8 + skew + M * N].view(M, N)
+    y = q4.gemm_i8(dev(a), dev(sa), dev(w), dev(sw), dtype=TYPES[t], out=out)
+    assert y.data_ptr() == out.data_ptr()
+    check(y, *i8.gemm(a, sa, w, sw), t, f"{M} {N}")
+    assert (buf[:8 + skew] == 7).all() and (buf[8 + skew + M * N:] == 7).all()
+
+
+def test_gemm_empty():
+    z = torch.zeros
+    y = q4.gemm_i8(z(0, 64, dtype=torch.int8, device=DEV), z(0, device=DEV), z(5, 64, dtype=torch.int8, device=DEV),
+                   z(5, device=DEV))
+    assert tuple(y.shape) == (0, 5)
+    c, s = q4.quant_i8(z(0, 64, device=DEV))
+    assert tuple(c.shape) == (0, 64) and tuple(s.shape) == (0,)
+
+
+# ---------------------------------------------------------------- swiglu
+
+@pytest.mark.parametrize("M,N,K", [(1, 1, 16), (1, 896, 896), (4, 300, 4096), (16, 65, 144), (30, 1000, 1040),
+                                   (64, 32, 128), (100, 130, 2816), (257, 200, 528), (520, 515, 1296)])
+@pytest.mark.parametrize("t", TYPES)
+def test_swiglu(M, N, K, t):
+    a, sa = codes(1, M, K), small_scales(3, K, M)
+    gate, up = (codes(2, N, K), small_scales(4, K, N) * 3), (codes(5, N, K), small_scales(6, K, N))
+    y = q4.gemm_i8_swiglu(dev(a), dev(sa), tuple(map(dev, gate)), tuple(map(dev, up)), dtype=TYPES[t])
+    check(y, *i8.swiglu(a, sa, gate, up), t, f"{M} {N} {K}")
+
+
+def test_swiglu_far_gates():
+    """Gates far to both sides: silu(g) -> g and -> 0, no NaN."""
+    M, N, K = 3, 40, 64
+    a, sa = codes(1, M, K), scales(3, M)
+    gate, up = (codes(2, N, K), scales(4, N) * 5000), (codes(5, N, K), scales(6, N))
+    y = q4.gemm_i8_swiglu(dev(a), dev(sa), tuple(map(dev, gate)), tuple(map(dev, up)))
+    check(y, *i8.swiglu(a, sa, gate, up), "f32", "far")
+
+
+# ---------------------------------------------------------------- grouped
+
+GROUPS = {
+    "one": [0, 37],
+    "empty ends": [0, 0, 5, 5, 21, 21],
+    "all in the last": [0, 0, 0, 90],
+    "single rows": list(range(0, 18)),
+    "tile borders": [0, 16, 48, 112, 240, 496, 497, 1009],
+    "rows outside": [3, 20, 20, 85],
+    "none": [0, 0, 0],
+    "none, in the middle": [4, 4, 4, 4],
+    "many": np.concatenate([[0], np.cumsum(np.random.default_rng(8).integers(0, 9, 150))]).tolist(),
+    "uneven": [0, 1, 400, 402, 402, 700, 701],
+}
+
+
+@pytest.mark.parametrize("name", GROUPS)
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("t,N,K", [("f32", 70, 144), ("bf16", 136, 400)])
+def test_grouped(name, swiglu, t, N, K):
+    off = GROUPS[name]
+    E, M = len(off) - 1, off[-1] + 6                       # rows behind the last group
+    a, sa = codes(1, M, K), small_scales(3, K, M)
+    gate, up = (codes(2, E, N, K), small_scales(4, K, E, N)), (codes(5, E, N, K), small_scales(6, K, E, N))
+    out = torch.full((M, N), 7.0, dtype=TYPES[t], device=DEV)
+    o = torch.tensor(off, dtype=torch.int32, device=DEV)
+    if swiglu:
+        y = q4.gemm_i8_grouped_swiglu(dev(a), dev(sa), tuple(map(dev, gate)), tuple(map(dev, up)), o, dtype=TYPES[t],
+                                      out=out)
+    else:
+        y = q4.gemm_i8_grouped(dev(a), dev(sa), dev(gate[0]), dev(gate[1]), o, dtype=TYPES[t], out=out)
+    inside = np.zeros(M, dtype=bool)
+    for e, lo, hi in i8.groups(off):
+        inside[lo:hi] = True
+        g, u = (gate[0][e], gate[1][e]), (up[0][e], up[1][e])
+        want = i8.swiglu(a[lo:hi], sa[lo:hi], g, u) if swiglu else i8.gemm(a[lo:hi], sa[lo:hi], *g)
+        check(y[lo:hi], *want, t, f"{name} expert {e}")
+    assert (y[torch.from_numpy(~inside).to(DEV)] == 7).all()
+
+
+@pytest.mark.parametrize("off", [[0, 50, 30, 80], [-5, 10, 900, 40], [70, 60, 50, 40], [2**31 - 1, -2**31, 5, 9]])
+@pytest.mark.parametrize("M", [40, 300])
+def test_grouped_bad_offsets_stay_inside(off, M):
+    """Offsets out of order and range: nothing outside y is written."""
+    N, K, E = 40, 160, 3
+    a, sa = codes(1, M, K), scales(3, M)
+    w, sw = codes(2, E, N, K), scales(4, E, N)
+    buf = torch.full((M * N + 64,), 7.0, device=DEV)
+    out = buf[32:32 + M * N].view(M, N)
+    q4.gemm_i8_grouped(dev(a), dev(sa), dev(w), dev(sw), torch.tensor(off, dtype=torch.int32, device=DEV), out=out)
+    torch.cuda.synchronize()
+    assert (buf[:32] == 7).all() and (buf[32 + M * N:] == 7).all() and torch.isfinite(out).all()
+
+
+# ---------------------------------------------------------------- streams, graphs, whole layers
+
+def layer(x, gate, up, down):
+    """A feed-forward layer: quantise, gate and up, quantise, down."""
+    c, s = q4.quant_i8(x)
+    h = q4.gemm_i8_swiglu(c, s, gate, up, dtype=torch.bfloat16)
+    c2, s2 = q4.quant_i8(h)
+    return c, s, h, c2, s2, q4.gemm_i8(c2, s2, *down, dtype=torch.bfloat16)
+
+
+def layer_problem(M, D, F, seed=1):
+    rng = np.random.default_rng(seed)
+    x = torch.from_numpy(rng.standard_normal((M, D)).astype(np.float32)).bfloat16()
+    gate = (codes(2, F, D), small_scales(4, D, F) * 10)
+    up = (codes(5, F, D), small_scales(6, D, F) * 10)
+    down = (codes(7, D, F), small_scales(8, F, D))
+    return x, gate, up, down
+
+
+@pytest.mark.parametrize("M", [1, 5, 33, 150, 300])
+def test_layer(M):
+    x, gate, up, down = layer_problem(M, 896, 1200)
+    c, s, h, c2, s2, y = layer(x.to(DEV), *(tuple(map(dev, m)) for m in (gate, up, down)))
+    cw, sw = i8.quant(x.double().numpy())
+    assert np.array_equal(c.cpu().numpy(), cw) and np.array_equal(s.cpu().numpy(), sw)
+    check(h, *i8.swiglu(cw, sw, gate, up), "bf16", "h")
+    cw, sw = i8.quant(h.double().cpu().numpy())
+    assert np.array_equal(c2.cpu().numpy(), cw) and np.array_equal(s2.cpu().numpy(), sw)
+    check(y, *i8.gemm(cw, sw, *down), "bf16", "y")
+
+
+@pytest.mark.parametrize("T", [3, 64, 400])
+def test_expert_layer(T):
+    """Routed rows: quantise, grouped gate and up, quantise, grouped down."""
+    E, D, F = 6, 512, 720
+    rng = np.random.default_rng(T)
+    x = torch.from_numpy(rng.standard_normal((T, D)).astype(np.float32)).bfloat16()
+    gate = (codes(2, E, F, D), small_scales(4, D, E, F) * 10)
+    up = (codes(5, E, F, D), small_scales(6, D, E, F) * 10)
+    down = (codes(7, E, D, F), small_scales(8, F, E, D))
+    chosen = np.sort(rng.choice(E, T, p=[0.5, 0.3, 0.1, 0.1, 0, 0]))
+    off = np.concatenate([[0], np.cumsum(np.bincount(chosen, minlength=E))])
+    o = torch.tensor(off, dtype=torch.int32, device=DEV)
+    c, s = q4.quant_i8(x.to(DEV))
+    h = q4.gemm_i8_grouped_swiglu(c, s, tuple(map(dev, gate)), tuple(map(dev, up)), o, dtype=torch.bfloat16)
+    c2, s2 = q4.quant_i8(h)
+    y = q4.gemm_i8_grouped(c2, s2, *map(dev, down), o)
+    cw, sw = i8.quant(x.double().numpy())
+    cw2, sw2 = i8.quant(h.double().cpu().numpy())
+    assert np.array_equal(c2.cpu().numpy(), cw2) and np.array_equal(s2.cpu().numpy(), sw2)
+    for e, lo, hi in i8.groups(off):
+        check(h[lo:hi], *i8.swiglu(cw[lo:hi], sw[lo:hi], (gate[0][e], gate[1][e]), (up[0][e], up[1][e])), "bf16",
+              f"h {e}")
+        check(y[lo:hi], *i8.gemm(cw2[lo:hi], sw2[lo:hi], down[0][e], down[1][e]), "f32", f"y {e}")
+
+
+@pytest.mark.parametrize("M", [1, 24, 90, 300])
+def test_a_row_does_not_depend_on_the_batch(M):
+    """The sums are exact, so a row's products are the same bits at any batch."""
+    N, K = 200, 2064
+    a, w, sa, sw = dev(codes(1, 300, K)), dev(codes(2, N, K)), dev(scales(3, 300)), dev(scales(4, N))
+    whole = q4.gemm_i8(a, sa, w, sw)
+    assert torch.equal(q4.gemm_i8(a[:M], sa[:M], w, sw), whole[:M])
+    o = torch.tensor([0, M], dtype=torch.int32, device=DEV)
+    assert torch.equal(q4.gemm_i8_grouped(a[:M], sa[:M], w[None], sw[None], o), whole[:M])
+
+
+@pytest.mark.parametrize("M", [2, 40, 300])
+def test_graph_replays(M):
+    x, *mats = layer_problem(M, 512, 640)
+    mats = [tuple(map(dev, m)) for m in mats]
+    xs = x.to(DEV)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        layer(xs, *mats)
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = layer(xs, *mats)
+    for k in range(4):
+        xs.copy_(torch.randn(x.shape, generator=torch.Generator().manual_seed(k)).bfloat16())
+        want = layer(xs, *mats)
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), k
+
+
+@pytest.mark.parametrize("M", [3, 300])
+def test_two_streams(M):
+    """Calls on two streams at once, each with its own outputs."""
+    x, *mats = layer_problem(M, 512, 640)
+    mats = [tuple(map(dev, m)) for m in mats]
+    xs = [x.to(DEV), (x * 3 + 1).to(DEV)]
+    want = [layer(v, *mats) for v in xs]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [None, None]
+    for _ in range(5):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i] = layer(xs[i], *mats)
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(a, b) for a, b in zip(got[i], want[i]))
+
+
+def test_refusals():
+    a, w, sa, sw = dev(codes(1, 4, 64)), dev(codes(2, 8, 64)), dev(scales(3, 4)), dev(scales(4, 8))
+    with pytest.raises(ValueError):
+        q4.gemm_i8(a, sa, w[:, :32], sw)                   # another K, not contiguous
+    with pytest.raises(ValueError):
+        q4.gemm_i8(a, sa[:3], w, sw)
+    with pytest.raises(ValueError):
+        q4.gemm_i8(a, sa, w, sw, bias=sw[:7])
+    with pytest.raises(TypeError):
+        q4.gemm_i8(a, sa, w, sw, dtype=torch.float64)
+    with pytest.raises(TypeError):
+        q4.gemm_i8(a, sa, w, sw, dtype=torch.float16, out=torch.empty(4, 8, device=DEV))
+    with pytest.raises(ValueError):
+        q4.gemm_i8(a, sa, w, sw, out=torch.empty(8, 4, device=DEV))
+    with pytest.raises(q4.Q4Error):
+        q4.gemm_i8(dev(codes(1, 4, 24)), sa, dev(codes(2, 8, 24)), sw)
+    with pytest.raises(ValueError):
+        q4.gemm_i8_swiglu(a, sa, (w, sw), (w[:7], sw[:7]))
+    o = torch.tensor([0, 4], dtype=torch.int32, device=DEV)
+    with pytest.raises(TypeError):
+        q4.gemm_i8_grouped(a, sa, w[None], sw[None], o.long())
+    with pytest.raises(ValueError):
+        q4.gemm_i8_grouped(a, sa, w[None], sw[None], torch.tensor([0, 2, 4], dtype=torch.int32, device=DEV))
+    with pytest.raises(ValueError):
+        q4.gemm_i8_grouped(a, sa, w, sw, o)
+    with pytest.raises(ValueError):
+        q4.gemm_i8_grouped(a, sa, w[None].cpu(), sw[None], o)

@@ -1,0 +1,147 @@
+"""8-bit operators: what can be checked without a GPU.  The library exports
+what include/q4i8.h declares, refuses bad arguments before it touches the
+device, and the oracle agrees with integer arithmetic and worked values."""
+
+import os
+import re
+import subprocess
+
+import numpy as np
+import pytest
+import torch
+
+import memory_bandwidth_amd as q4
+from oracle import i8
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+A = 0x10000          # fake, aligned, never dereferenced device address
+
+
+@pytest.fixture(scope="module")
+def L():
+    if not os.path.exists(q4.LIB_PATH):
+        from memory_bandwidth_amd import build
+        build.build()
+    return q4.lib()
+
+
+def declared():
+    text = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include", "q4i8.h")).read(), flags=re.S)
+    return re.findall(r"^int\s+([a-z_0-9]+)\s*\(", text, flags=re.M)
+
+
+def test_header_and_exports_agree(L):
+    assert tuple(declared()) == q4.EXPORTS_I8
+    out = subprocess.run(["nm", "-D", "--defined-only", q4.LIB_PATH], capture_output=True, text=True,
+                         check=True).stdout
+    exported = {ln.split()[-1] for ln in out.splitlines() if " T " in ln}
+    assert set(declared()) <= exported
+
+
+def call(L, fn, M, N, K, t=q4.I8_F32, E=2, p=None, at=()):
+    """Calls fn with fake pointers; `at` overrides pointers by position."""
+    n = {"quant_i8": 3, "gemm_i8": 6, "gemm_i8_swiglu": 7, "gemm_i8_grouped": 6, "gemm_i8_grouped_swiglu": 8}[fn]
+    ptr = [A] * n
+    for i, v in at:
+        ptr[i] = v
+    if fn == "quant_i8":
+        return L.quant_i8(ptr[0], t, ptr[1], ptr[2], M, K, None)
+    sizes = [M, E, N, K] if "grouped" in fn else [M, N, K]
+    return getattr(L, fn)(*ptr, t, *sizes, None)
+
+
+GEMMS = [f for f in q4.EXPORTS_I8 if f != "quant_i8"]
+
+
+@pytest.mark.parametrize("fn", GEMMS)
+@pytest.mark.parametrize("M,N,K,want", [
+    (-1, 8, 64, q4.Q4_EINVAL), (1, -1, 64, q4.Q4_EINVAL), (1, 8, 0, q4.Q4_EINVAL), (1, 8, 24, q4.Q4_EINVAL),
+    (1, 8, 8, q4.Q4_EINVAL), (1, 8, 131072, q4.Q4_EINVAL), (2**24 + 1, 8, 64, q4.Q4_EINVAL),
+    (1, 2**24 + 1, 64, q4.Q4_EINVAL), (2**24, 2**24, 64, q4.Q4_EINVAL),
+    (0, 8, 64, q4.Q4_OK), (4, 0, 64, q4.Q4_OK), (0, 8, 131056, q4.Q4_OK),
+])
+def test_gemm_sizes(L, fn, M, N, K, want):
+    assert call(L, fn, M, N, K) == want
+
+
+@pytest.mark.parametrize("fn", q4.EXPORTS_I8)
+@pytest.mark.parametrize("t", [-1, 3])
+def test_types(L, fn, t):
+    assert call(L, fn, 4, 8, 64, t=t) == q4.Q4_EINVAL
+
+
+@pytest.mark.parametrize("fn", [f for f in GEMMS if "grouped" in f])
+def test_group_counts(L, fn):
+    assert call(L, fn, 4, 8, 64, E=0) == q4.Q4_EINVAL
+    assert call(L, fn, 4, 8, 64, E=65537) == q4.Q4_EINVAL
+    assert call(L, fn, 4, 2**24, 64, E=256) == q4.Q4_EINVAL
+
+
+@pytest.mark.parametrize("fn", q4.EXPORTS_I8)
+def test_pointers(L, fn):
+    n = {"quant_i8": 3, "gemm_i8": 6, "gemm_i8_swiglu": 7, "gemm_i8_grouped": 6, "gemm_i8_grouped_swiglu": 8}[fn]
+    for i in range(n):
+        if fn == "gemm_i8" and i == 4:                 # bias may be NULL
+            continue
+        assert call(L, fn, 4, 8, 64, at=[(i, None)]) == q4.Q4_ENULL, i
+        assert call(L, fn, 4, 8, 64, at=[(i, A + 1)]) == q4.Q4_EALIGN, i
+    for i in {"quant_i8": (0, 1), "gemm_i8": (0, 2), "gemm_i8_swiglu": (0, 2, 4), "gemm_i8_grouped": (0, 2),
+              "gemm_i8_grouped_swiglu": (0, 2, 4)}[fn]:
+        assert call(L, fn, 4, 8, 64, at=[(i, A + 8)]) == q4.Q4_EALIGN, i
+
+
+@pytest.mark.parametrize("M,K,want", [(-1, 64, q4.Q4_EINVAL), (1, 0, q4.Q4_EINVAL), (1, 40, q4.Q4_EINVAL),
+                                      (1, 131072, q4.Q4_EINVAL), (0, 64, q4.Q4_OK)])
+def test_quant_sizes(L, M, K, want):
+    assert call(L, "quant_i8", M, 8, K) == want
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="a GPU would be given fake addresses")
+@pytest.mark.parametrize("fn", q4.EXPORTS_I8)
+def test_no_device(L, fn):
+    assert call(L, fn, 4, 8, 64) == q4.Q4_EDEVICE
+
+
+def test_binding_refuses_host_tensors_and_wrong_types():
+    a, s = torch.zeros(2, 32, dtype=torch.int8), torch.ones(2)
+    w, sw = torch.zeros(4, 32, dtype=torch.int8), torch.ones(4)
+    with pytest.raises(ValueError):
+        q4.gemm_i8(a, s, w, sw)
+    with pytest.raises(TypeError):
+        q4.gemm_i8(a.float(), s, w, sw)
+    with pytest.raises(TypeError):
+        q4.quant_i8(a)
+    with pytest.raises(ValueError):
+        q4.quant_i8(a.float())
+
+
+# ---------------------------------------------------------------- the oracle
+
+def test_oracle_quant_worked_values():
+    # Row 0: scale exactly 1, ties at .5 go to the even integer.  Row 1: zeros.  Row 2: an infinity.
+    x = np.array([[127, 0.5, 1.5, 2.5, -0.5, -1.5, -2.5, 126.5], [0] * 8, [1, np.inf, 0, 0, 0, 0, 0, 0]])
+    c, s = i8.quant(x)
+    assert c[0].tolist() == [127, 0, 2, 2, 0, -2, -2, 126]
+    assert s[0] == 1 and s[1] == np.float32(2.0 ** -126) and not c[1].any()
+    assert np.isnan(s[2]) and not c[2].any()
+
+
+def test_oracle_product_is_integer_arithmetic():
+    rng = np.random.default_rng(3)
+    a = rng.integers(-128, 128, (5, 4096), dtype=np.int8)
+    w = rng.integers(-128, 128, (7, 4096), dtype=np.int8)
+    a[0], w[0] = -128, -128
+    one = np.ones(7, dtype=np.float32)
+    assert np.array_equal(i8.product(a, one[:5], w, one), a.astype(np.int64) @ w.astype(np.int64).T)
+
+
+def test_oracle_swiglu_and_bias_worked_values():
+    a = np.array([[2, 0]], dtype=np.int8)
+    g = (np.array([[3, 9]], dtype=np.int8), np.array([0.5], dtype=np.float32))
+    u = (np.array([[-4, 9]], dtype=np.int8), np.array([0.25], dtype=np.float32))
+    sa = np.array([1.0], dtype=np.float32)
+    y, _ = i8.swiglu(a, sa, g, u)                  # g = 3, u = -2
+    assert y[0, 0] == pytest.approx(-2 * 3 / (1 + np.exp(-3.0)), rel=1e-15)
+    y, _ = i8.gemm(a, sa, *g, bias=np.array([10], dtype=np.float32))
+    assert y[0, 0] == 13
+    assert i8.groups([0, 2, 2, 5]) == [(0, 0, 2), (2, 2, 5)]
