@@ -30,7 +30,7 @@ struct Args {
     const int32_t *offsets;    // groups, or NULL
     void *y;
     int y_type, M, N, K, E;
-    int tiles_n;
+    int tiles_m, tiles_n;
     bool vec;                  // rows of y may be written in 16-byte stores
 };
 
@@ -116,18 +116,64 @@ __device__ __forceinline__ Tile find_tile(const Args &p, int t) {
             const int o = __shfl_up(upto, d);
             if (lane >= d) upto += o;
         }
-        const int all = __shfl(upto, 63);
+        const int all = __builtin_amdgcn_readlane(upto, 63);
         if (t < all) {
             const int owner = __ffsll((unsigned long long)__ballot(upto > t)) - 1;
-            const int first = __builtin_amdgcn_readfirstlane(__shfl(upto - mine, owner));
-            const int l = __builtin_amdgcn_readfirstlane(__shfl(lo, owner));
-            const int h = __builtin_amdgcn_readfirstlane(__shfl(hi, owner));
-            const int m0 = l + (t - first) * BM;
-            return {m0, min(BM, h - m0), e0 + __builtin_amdgcn_readfirstlane(owner)};
+            const int m0 = __builtin_amdgcn_readlane(lo, owner) +
+                           (t - __builtin_amdgcn_readlane(upto - mine, owner)) * BM;
+            return {m0, min(BM, __builtin_amdgcn_readlane(hi, owner) - m0), e0 + owner};
         }
         t -= all;
     }
     return {0, 0, 0};
+}
+
+// Scales a wavefront's sums and writes them.  acc[i][..]: rows row0 + 16 i +
+// lane % 16 of the tile; over its fragments a lane holds the C columns from n
+// on (with SWI: C of gate in the first half of the fragments, C of up in the
+// second).
+template <int FM, int C, bool SWI>
+__device__ __forceinline__ void finish(const Args &p, const i32x4_t (&acc)[FM][SWI ? C / 2 : C / 4], const Tile &tl,
+                                       size_t mat, int row0, int n, int lane) {
+    float sw[SWI ? 2 : 1][C], bias[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const bool in = n + c < p.N;
+        sw[0][c] = in ? p.sw[0][mat + n + c] : 0.f;
+        if constexpr (SWI) sw[SWI][c] = in ? p.sw[1][mat + n + c] : 0.f;
+        bias[c] = !SWI && p.bias && in ? p.bias[n + c] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+        const int r = row0 + i * 16 + (lane & 15);
+        if (r >= tl.rows) continue;
+        const float sa = p.sa[tl.m0 + r];
+        float v[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            if constexpr (SWI) {
+                const float g = (float)acc[i][c >> 2][c & 3] * sa * sw[0][c];
+                const float u = (float)acc[i][(C + c) >> 2][c & 3] * sa * sw[SWI][c];
+                v[c] = silu(g) * u;
+            } else {
+                v[c] = (float)acc[i][c >> 2][c & 3] * sa * sw[0][c] + bias[c];
+            }
+        }
+        store_run<C>(p, tl.m0 + r, n, v);
+    }
+}
+
+// The tile of this workgroup.  Workgroups are dealt to the eight XCDs in
+// turn, each with its own L2: XCD x takes the x-th eighth of the tiles, and
+// tiles are ordered in bands of eight tile rows, column by column, so that
+// the tiles an XCD runs at one time share rows of a and of w.
+__device__ __forceinline__ void tile_of(const Args &p, int &tm, int &tn) {
+    const int all = gridDim.x, b = blockIdx.x, x = b & 7, per = all >> 3, more = all & 7;
+    const int t = x * per + min(x, more) + (b >> 3);
+    const int band = t / (8 * p.tiles_n), first = band * 8, rows = min(8, p.tiles_m - first);
+    const int in = t - band * 8 * p.tiles_n;
+    tm = first + in % rows;
+    tn = in / rows;
 }
 
 // LDS tiles: rows of 128 bytes in eight 16-byte chunks; chunk c of row r
@@ -144,9 +190,11 @@ __global__ __launch_bounds__(256) void gemm_i8_tile(Args p) {
     __shared__ __align__(16) char lds[(BM + BW) * BK];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int wm = wave >> 1, wn = wave & 1;
-    const int n0 = (int)(blockIdx.x % p.tiles_n) * BN;
-    const Tile tl = find_tile<BM>(p, (int)(blockIdx.x / p.tiles_n));
+    int tm, tn;
+    tile_of(p, tm, tn);
+    const Tile tl = find_tile<BM>(p, tm);
     if (tl.rows <= 0) return;
+    const int n0 = tn * BN;
     const size_t mat = (size_t)tl.e * p.N;
 
     i32x4_t acc[2][2] = {};
@@ -193,34 +241,152 @@ __global__ __launch_bounds__(256) void gemm_i8_tile(Args p) {
     }
 
     constexpr int C = SWI ? 4 : 8;       // consecutive columns of a lane
-    const int n = n0 + (SWI ? wn * 16 : wn * 32) + (lane >> 4) * C;
-    float sw[2][C] = {}, bias[C] = {};
+    finish<2, C, SWI>(p, acc, tl, mat, wm * 32, n0 + (SWI ? wn * 16 : wn * 32) + (lane >> 4) * C, lane);
+}
+
+// ---------------------------------------------------------------- large tiles
+//
+// A 256 x 256 tile (with SWI: 128 columns of each matrix), eight wavefronts
+// of 128 x 64.  Steps of 128 bytes of K pass through two LDS buffers, loaded
+// straight from memory (buffer loads to LDS, 1 KiB an instruction: eight rows
+// of 128 bytes, the lanes' chunk order making the swizzle).  A step has two
+// halves of 64 bytes; the fragments of each half are read into registers
+// while the other half's products run:
+//
+//     first half:   read (t, second half),  products of (t, first half)
+//                   wait for step t + 1 in LDS and for this step's reads
+//     second half:  load step t + 2 over step t,  read (t + 1, first half),
+//                   products of (t, second half)
+//
+// so there is one barrier a step, and a step's loads have a whole step to
+// arrive.  A last step that K does not fill is taken as the last 128 bytes
+// of the rows, with the activations already used set to zero; every address
+// stays inside the rows.  Rows past the tile's end repeat its last row, and
+// their results are not stored.
+typedef __attribute__((address_space(3))) void *lds_ptr_t;
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const int8_t *base, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t *>(base), 0, (int)bytes, 0x00020000);
+}
+
+template <bool SWI>
+__global__ __launch_bounds__(512, 2) void gemm_i8_large(Args p) {
+    constexpr int BM = 256, BW = 256, BN = SWI ? 128 : 256;
+    constexpr int STAGE = (BM + BW) * BK;
+    extern __shared__ __align__(16) char lds[];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave >> 2, wn = wave & 3;
+    int tm, tn;
+    tile_of(p, tm, tn);
+    const Tile tl = find_tile<BM>(p, tm);
+    if (tl.rows <= 0) return;
+    const int n0 = tn * BN, cols = min(BN, p.N - n0);
+    const size_t mat = (size_t)tl.e * p.N;
+
+    // Loads: this wavefront brings rows 32 wave .. 32 wave + 31 of both
+    // halves of a stage, eight rows an instruction.
+    const __amdgpu_buffer_rsrc_t ra = rsrc_of(p.a + (size_t)tl.m0 * p.K, (uint32_t)tl.rows * p.K);
+    // SWI: the 32 weight rows of one wavefront's loads are all gate or all up.
+    const int8_t *wbase = SWI && (wave & 1) ? p.w[1] : p.w[0];
+    const __amdgpu_buffer_rsrc_t rw = rsrc_of(wbase + (mat + n0) * p.K, (uint32_t)cols * p.K);
+    uint32_t va[4], vw[4];
+    const int chunk = ((lane & 7) ^ (lane >> 3)) << 4;
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-        if (n + c < p.N) {
-            sw[0][c] = p.sw[0][mat + n + c];
-            if (SWI) sw[1][c] = p.sw[1][mat + n + c];
-            else if (p.bias) bias[c] = p.bias[n + c];
-        }
+    for (int i = 0; i < 4; ++i) {
+        const int r = wave * 32 + i * 8 + (lane >> 3);
+        va[i] = (uint32_t)min(r, tl.rows - 1) * p.K + chunk;
+        // Row r of the weight half belongs to wavefront column r / 64, its
+        // fragment (r / 16) % 4, row r % 16 of it.
+        const int c = r >> 6, j = (r >> 4) & 3, q = r & 15;
+        const int n = SWI ? c * 32 + frag_row<2>(j & 1, q) : c * 64 + frag_row<4>(j, q);
+        vw[i] = (uint32_t)min(n, cols - 1) * p.K + chunk;
     }
+    auto load = [&](int buf, int koff) {
+        char *at = lds + buf * STAGE + wave * 32 * BK;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int r = wm * 32 + i * 16 + (lane & 15);
-        if (r >= tl.rows) continue;
-        const float sa = p.sa[tl.m0 + r];
-        float v[C];
+        for (int i = 0; i < 4; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr_t)(at + i * 8 * BK), 16, va[i], koff, 0, 0);
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-            if (SWI) {
-                const float g = (float)acc[i][0][c] * sa * sw[0][c];
-                const float u = (float)acc[i][1][c] * sa * sw[1][c];
-                v[c] = silu(g) * u;
-            } else {
-                v[c] = (float)acc[i][c >> 2][c & 3] * sa * sw[0][c] + bias[c];
-            }
+        for (int i = 0; i < 4; ++i)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_ptr_t)(at + BM * BK + i * 8 * BK), 16, vw[i], koff, 0,
+                                                     0);
+    };
+
+    // Fragment reads: lane l takes row l % 16, chunk l / 16 (+ 4 in the
+    // second half, which flips bit 6 of the swizzled address).
+    const int fr = (lane & 15) * BK + (((lane >> 4) ^ (lane & 7)) << 4);
+    const char *xa = lds + wm * 128 * BK + fr, *wa = lds + (BM + wn * 64) * BK + fr;
+    const char *xb = lds + wm * 128 * BK + (fr ^ 64), *wb = lds + (BM + wn * 64) * BK + (fr ^ 64);
+    i32x4_t acc[8][4] = {};
+    i32x4_t x0[8], w0[4], x1[8], w1[4];
+    auto read = [&](i32x4_t (&x)[8], i32x4_t (&w)[4], const char *px, const char *pw) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const i32x4_t *>(pw + j * 16 * BK);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = *reinterpret_cast<const i32x4_t *>(px + i * 16 * BK);
+    };
+    auto products = [&](const i32x4_t (&x)[8], const i32x4_t (&w)[4]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[j], x[i], acc[i][j], 0, 0, 0);
+    };
+    const int steps = (p.K + BK - 1) / BK;
+    auto koff = [&](int t) { return min(t * BK, p.K - BK); };
+    // Chunks of the last step that earlier steps have used.
+    const int used = steps * 8 - (p.K >> 4);
+    auto drop = [&](i32x4_t (&x)[8], int c) {
+        if (c < used) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = i32x4_t{0, 0, 0, 0};
         }
-        store_run<C>(p, tl.m0 + r, n, v);
+    };
+
+    load(0, koff(0));
+    if (steps > 1) load(1, koff(1));
+    if (steps > 1) asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
+    else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    asm volatile("s_barrier" ::: "memory");
+    read(x0, w0, xa, wa);
+    if (steps == 1 && used) drop(x0, lane >> 4);
+    auto wait = [&]() {
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    int t = 0;
+    auto whole = [&](int buf) {          // a step with two full ones behind it
+        const int cur = buf * STAGE, nxt = STAGE - cur;
+        read(x1, w1, xb + cur, wb + cur);
+        products(x0, w0);
+        wait();
+        load(buf, (t + 2) * BK);
+        read(x0, w0, xa + nxt, wa + nxt);
+        products(x1, w1);
+        __builtin_amdgcn_sched_barrier(0);
+        ++t;
+    };
+    while (t + 4 < steps) {
+        whole(0);
+        whole(1);
     }
+    for (; t < steps; ++t) {
+        const int cur = (t & 1) * STAGE, nxt = STAGE - cur;
+        read(x1, w1, xb + cur, wb + cur);
+        if (t + 1 == steps && used) drop(x1, 4 + (lane >> 4));
+        products(x0, w0);
+        wait();
+        if (t + 2 < steps) load(t & 1, koff(t + 2));
+        if (t + 1 < steps) {
+            read(x0, w0, xa + nxt, wa + nxt);
+            if (t + 2 == steps && used) drop(x0, lane >> 4);
+        }
+        products(x1, w1);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+
+    constexpr int C = SWI ? 8 : 16;      // consecutive columns of a lane
+    finish<8, C, SWI>(p, acc, tl, mat, wm * 128, n0 + (SWI ? wn * 32 : wn * 64) + (lane >> 4) * C, lane);
 }
 
 constexpr int kMaxRows = 1 << 24;
@@ -242,14 +408,25 @@ int run(Args p, int mats, hipStream_t stream) {
     if (mats == 2 && (!q4::aligned(p.w[1], 16) || !q4::aligned(p.sw[1], 4))) return Q4_EALIGN;
     if (int st = q4::check_device()) return st;
     p.vec = q4::aligned(p.y, 16) && (size_t)p.N * (p.y_type == I8_F32 ? 4 : 2) % 16 == 0;
-    const int bn = mats == 2 ? 32 : 64;
+    const bool large = p.K >= BK && p.M > 128;
+    const int bm = large ? 256 : 64, bn = bm / mats;
     p.tiles_n = (p.N + bn - 1) / bn;
     // Groups: every group may end inside a tile.
-    const int64_t tiles_m = p.offsets ? p.M / 64 + std::min(p.E, p.M) : (p.M + 63) / 64;
+    const int64_t tiles_m = p.offsets ? p.M / bm + std::min(p.E, p.M) : (p.M + bm - 1) / bm;
     const int64_t grid = tiles_m * p.tiles_n;
     if (grid > 0x7FFFFFFFll) return Q4_EINVAL;
-    if (mats == 2) gemm_i8_tile<true><<<(unsigned)grid, 256, 0, stream>>>(p);
-    else gemm_i8_tile<false><<<(unsigned)grid, 256, 0, stream>>>(p);
+    p.tiles_m = (int)tiles_m;
+    if (large) {
+        constexpr int lds = 2 * 512 * BK;
+        const void *f = mats == 2 ? (const void *)gemm_i8_large<true> : (const void *)gemm_i8_large<false>;
+        if (hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, lds) != hipSuccess) return Q4_ELAUNCH;
+        if (mats == 2) gemm_i8_large<true><<<(unsigned)grid, 512, lds, stream>>>(p);
+        else gemm_i8_large<false><<<(unsigned)grid, 512, lds, stream>>>(p);
+    } else if (mats == 2) {
+        gemm_i8_tile<true><<<(unsigned)grid, 256, 0, stream>>>(p);
+    } else {
+        gemm_i8_tile<false><<<(unsigned)grid, 256, 0, stream>>>(p);
+    }
     return q4::launch_status();
 }
 
@@ -257,14 +434,14 @@ int run(Args p, int mats, hipStream_t stream) {
 
 extern "C" int gemm_i8(const int8_t *a, const float *a_scales, const int8_t *w, const float *w_scales,
                        const float *bias, void *y, int y_type, int M, int N, int K, void *stream) {
-    return run({a, a_scales, {w, nullptr}, {w_scales, nullptr}, bias, nullptr, y, y_type, M, N, K, 1, 0, false}, 1,
+    return run({a, a_scales, {w, nullptr}, {w_scales, nullptr}, bias, nullptr, y, y_type, M, N, K, 1, 0, 0, false}, 1,
                static_cast<hipStream_t>(stream));
 }
 
 extern "C" int gemm_i8_swiglu(const int8_t *a, const float *a_scales, const int8_t *w_gate,
                               const float *scales_gate, const int8_t *w_up, const float *scales_up, void *y,
                               int y_type, int M, int N, int K, void *stream) {
-    return run({a, a_scales, {w_gate, w_up}, {scales_gate, scales_up}, nullptr, nullptr, y, y_type, M, N, K, 1, 0,
+    return run({a, a_scales, {w_gate, w_up}, {scales_gate, scales_up}, nullptr, nullptr, y, y_type, M, N, K, 1, 0, 0,
                 false},
                2, static_cast<hipStream_t>(stream));
 }
@@ -273,7 +450,7 @@ extern "C" int gemm_i8_grouped(const int8_t *a, const float *a_scales, const int
                                const int32_t *offsets, void *y, int y_type, int M, int E, int N, int K,
                                void *stream) {
     if (!offsets && M > 0 && N > 0) return Q4_ENULL;
-    return run({a, a_scales, {w, nullptr}, {w_scales, nullptr}, nullptr, offsets, y, y_type, M, N, K, E, 0, false}, 1,
+    return run({a, a_scales, {w, nullptr}, {w_scales, nullptr}, nullptr, offsets, y, y_type, M, N, K, E, 0, 0, false}, 1,
                static_cast<hipStream_t>(stream));
 }
 
@@ -282,7 +459,7 @@ extern "C" int gemm_i8_grouped_swiglu(const int8_t *a, const float *a_scales, co
                                       const int32_t *offsets, void *y, int y_type, int M, int E, int N, int K,
                                       void *stream) {
     if (!offsets && M > 0 && N > 0) return Q4_ENULL;
-    return run({a, a_scales, {w_gate, w_up}, {scales_gate, scales_up}, nullptr, offsets, y, y_type, M, N, K, E, 0,
+    return run({a, a_scales, {w_gate, w_up}, {scales_gate, scales_up}, nullptr, offsets, y, y_type, M, N, K, E, 0, 0,
                 false},
                2, static_cast<hipStream_t>(stream));
 }
