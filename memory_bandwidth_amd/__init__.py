@@ -433,48 +433,47 @@ def scan2_config() -> tuple[int, int, int, int]:
 
 
 # ---------------------------------------------------------------- 8-bit activations and weights
+#
+# A call of these at one row takes as long on the host as on the GPU, so each
+# entry point tests its arguments in one expression; only when that fails do
+# the checks below run one by one, to raise what is wrong.
 
-def _i8_type(dtype, name: str) -> int:
-    if dtype not in I8_TYPES:
-        raise TypeError(f"{name} must be float32, float16 or bfloat16, got {dtype}")
-    return I8_TYPES[dtype]
-
-
-def _i8_call(fn: str, dev: torch.device, *args) -> None:
-    """Calls the entry point on dev's current stream, with dev current."""
-    if dev.index == torch.cuda.current_device():
-        _check(fn, getattr(lib(), fn)(*args, torch.cuda.current_stream(dev).cuda_stream))
-        return
-    with torch.cuda.device(dev):
-        _check(fn, getattr(lib(), fn)(*args, torch.cuda.current_stream(dev).cuda_stream))
-
-
-def _i8_rows(a: torch.Tensor, a_scales: torch.Tensor) -> tuple[int, int]:
-    _need(a, "a", (torch.int8,))
-    _need(a_scales, "a_scales", (torch.float32,), a.device)
-    if a.dim() != 2 or tuple(a_scales.shape) != (a.shape[0],):
-        raise ValueError(f"a must be [M, K] and a_scales [M]: got {tuple(a.shape)}, {tuple(a_scales.shape)}")
-    return a.shape[0], a.shape[1]
+def _i8_call(fn: str, dev: int, *args) -> None:
+    """Calls the entry point on the device's current stream, with that device current."""
+    f = getattr(_lib or lib(), fn)
+    if dev == torch._C._cuda_getDevice():
+        status = f(*args, torch._C._cuda_getCurrentRawStream(dev))
+    else:
+        with torch.cuda.device(dev):
+            status = f(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if status:
+        raise Q4Error(fn, status)
 
 
-def _i8_matrix(w: torch.Tensor, w_scales: torch.Tensor, shape, name: str) -> None:
-    """w int8 [..., N, K] and w_scales float32 [..., N]; shape is w's, None where any size will do."""
-    _need(w, name, (torch.int8,))
-    _need(w_scales, f"{name}'s scales", (torch.float32,), w.device)
-    if (w.dim() != len(shape) or any(s is not None and s != n for s, n in zip(shape, w.shape))
-            or w_scales.shape != w.shape[:-1]):
-        want = "[" + ", ".join("*" if s is None else str(s) for s in shape) + "]"
-        raise ValueError(f"{name} must be {want} with a scale for each row: got {tuple(w.shape)}, "
-                         f"{tuple(w_scales.shape)}")
+def _i8_refuse(tensors: dict, shapes: dict, dtype=None) -> None:
+    """Raises for the first tensor of the wrong type, place or layout, then for
+    the first of the wrong shape.  tensors: name -> (tensor, dtypes); shapes:
+    name -> (tensor, shape), None in a shape where any size will do."""
+    if dtype is not None and dtype not in I8_TYPES:
+        raise TypeError(f"dtype must be float32, float16 or bfloat16, got {dtype}")
+    dev = None
+    for name, (t, dtypes) in tensors.items():
+        if t is not None:
+            _need(t, name, dtypes, dev)
+            dev = t.device
+    for name, (t, shape) in shapes.items():
+        if t is not None and (t.dim() != len(shape) or any(s is not None and s != n for s, n in zip(shape, t.shape))):
+            want = ", ".join("*" if s is None else str(s) for s in shape)
+            raise ValueError(f"{name} must be [{want}], got {list(t.shape)}")
+    raise ValueError("unsupported arguments")
 
 
-def _i8_out(out: torch.Tensor | None, M: int, N: int, dtype, dev: torch.device) -> torch.Tensor:
-    if out is None:
-        return torch.empty((M, N), dtype=dtype, device=dev)
-    _need(out, "out", (dtype,), dev)
-    if tuple(out.shape) != (M, N):
-        raise ValueError("out must be [M, N]")
-    return out
+_I8, _F32, _I32 = torch.int8, torch.float32, torch.int32
+
+
+def _size(t, d: int):
+    """t.shape[d], None where t has none such: for messages only."""
+    return t.shape[d] if isinstance(t, torch.Tensor) and -t.dim() <= d < t.dim() else None
 
 
 def quant_i8(x: torch.Tensor, out: tuple | None = None) -> tuple[torch.Tensor, torch.Tensor]:
@@ -486,84 +485,128 @@ def quant_i8(x: torch.Tensor, out: tuple | None = None) -> tuple[torch.Tensor, t
     if x.dim() != 2:
         raise ValueError("x must be [M, K]")
     M, K = x.shape
+    dev = x.get_device()
     if out is None:
-        codes = torch.empty((M, K), dtype=torch.int8, device=x.device)
-        scales = torch.empty(M, dtype=torch.float32, device=x.device)
+        codes = torch.empty((M, K), dtype=_I8, device=x.device)
+        scales = torch.empty((M,), dtype=_F32, device=x.device)
     else:
         codes, scales = out
-        _need(codes, "codes", (torch.int8,), x.device)
-        _need(scales, "scales", (torch.float32,), x.device)
+        _need(codes, "codes", (_I8,), x.device)
+        _need(scales, "scales", (_F32,), x.device)
         if tuple(codes.shape) != (M, K) or tuple(scales.shape) != (M,):
             raise ValueError("out must be codes [M, K] and scales [M]")
-    _i8_call("quant_i8", x.device, _ptr(x), I8_TYPES[x.dtype], _ptr(codes), _ptr(scales), M, K)
+    _i8_call("quant_i8", dev, x.data_ptr(), I8_TYPES[x.dtype], codes.data_ptr(), scales.data_ptr(), M, K)
     return codes, scales
 
 
 def gemm_i8(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
             bias: torch.Tensor | None = None, dtype=torch.float32,
             out: torch.Tensor | None = None) -> torch.Tensor:
-    """y[M, N] = (a[M, K] . w[N, K]^T) * a_scales[M] * w_scales[N] (+ bias[N]), the sums exact."""
-    M, K = _i8_rows(a, a_scales)
-    dev = a.device
-    _i8_matrix(w, w_scales, (None, K), "w")
-    N = w.shape[0]
-    if w.device != dev:
-        raise ValueError(f"w is on {w.device}, expected {dev}")
-    if bias is not None:
-        _need(bias, "bias", (torch.float32,), dev)
-        if tuple(bias.shape) != (N,):
-            raise ValueError("bias must be [N]")
-    t = _i8_type(dtype, "dtype")
-    out = _i8_out(out, M, N, dtype, dev)
-    _i8_call("gemm_i8", dev, _ptr(a), _ptr(a_scales), _ptr(w), _ptr(w_scales), _ptr(bias), _ptr(out), t, M, N, K)
+    """y[M, N] = (a[M, K] . w[N, K]^T) * a_scales[M] * w_scales[N] (+ bias[N]), the sums exact.
+
+    a and w int8, scales and bias float32; y is of `dtype` (float32, float16
+    or bfloat16).  K is a multiple of 16."""
+    t = I8_TYPES.get(dtype)
+    try:
+        dev, (M, K), (N, Kw) = a.get_device(), a.shape, w.shape
+        fine = (a.dtype is _I8 and w.dtype is _I8 and a_scales.dtype is _F32 and w_scales.dtype is _F32
+                and dev >= 0 and w.get_device() == dev and a_scales.get_device() == dev
+                and w_scales.get_device() == dev and K == Kw and a_scales.shape == (M,) and w_scales.shape == (N,)
+                and a.is_contiguous() and w.is_contiguous() and a_scales.is_contiguous()
+                and w_scales.is_contiguous() and t is not None
+                and (bias is None or (bias.dtype is _F32 and bias.get_device() == dev and bias.shape == (N,)
+                                      and bias.is_contiguous()))
+                and (out is None or (out.dtype is dtype and out.get_device() == dev and out.shape == (M, N)
+                                     and out.is_contiguous())))
+    except (AttributeError, ValueError):
+        fine = False
+    if not fine:
+        _i8_refuse({"a": (a, (_I8,)), "a_scales": (a_scales, (_F32,)), "w": (w, (_I8,)), "w_scales": (w_scales, (_F32,)),
+                    "bias": (bias, (_F32,)), "out": (out, (dtype,))},
+                   {"a": (a, (None, None)), "a_scales": (a_scales, (_size(a, 0),)), "w": (w, (None, _size(a, 1))),
+                    "w_scales": (w_scales, (_size(w, 0),)), "bias": (bias, (_size(w, 0),)),
+                    "out": (out, (_size(a, 0), _size(w, 0)))}, dtype)
+    if out is None:
+        out = torch.empty((M, N), dtype=dtype, device=a.device)
+    _i8_call("gemm_i8", dev, a.data_ptr(), a_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(),
+             None if bias is None else bias.data_ptr(), out.data_ptr(), t, M, N, K)
     return out
 
 
-def _i8_pair(a: torch.Tensor, gate: tuple, up: tuple, shape) -> int:
+def _i8_pair_fine(dev, K, lead, wg, sg, wu, su) -> bool:
+    """Gate and up: one shape [..lead, N, K], a scale for each row."""
+    return (wg.dtype is _I8 and wu.dtype is _I8 and sg.dtype is _F32 and su.dtype is _F32
+            and wg.get_device() == dev and wu.get_device() == dev and sg.get_device() == dev
+            and su.get_device() == dev and wg.shape[:-2] == lead and wg.shape[-1] == K and wu.shape == wg.shape
+            and sg.shape == wg.shape[:-1] and su.shape == sg.shape and wg.is_contiguous() and wu.is_contiguous()
+            and sg.is_contiguous() and su.is_contiguous())
+
+
+def _i8_refuse_pair(a, a_scales, gate, up, offsets, out, dtype) -> None:
     (wg, sg), (wu, su) = gate, up
-    _i8_matrix(wg, sg, shape, "gate")
-    _i8_matrix(wu, su, tuple(wg.shape), "up")
-    if wg.device != a.device or wu.device != a.device:
-        raise ValueError(f"gate and up must be on {a.device}")
-    return wg.shape[-2]
+    lead = () if offsets is None else (offsets.numel() - 1 if isinstance(offsets, torch.Tensor) else None,)
+    shape = (*lead, _size(wg, -2), _size(a, 1))
+    _i8_refuse({"a": (a, (_I8,)), "a_scales": (a_scales, (_F32,)), "gate": (wg, (_I8,)), "gate's scales": (sg, (_F32,)),
+                "up": (wu, (_I8,)), "up's scales": (su, (_F32,)), "offsets": (offsets, (_I32,)), "out": (out, (dtype,))},
+               {"a": (a, (None, None)), "a_scales": (a_scales, (_size(a, 0),)), "offsets": (offsets, (None,)),
+                "gate": (wg, shape), "gate's scales": (sg, shape[:-1]), "up": (wu, shape), "up's scales": (su, shape[:-1]),
+                "out": (out, (_size(a, 0), shape[-2]))}, dtype)
 
 
 def gemm_i8_swiglu(a: torch.Tensor, a_scales: torch.Tensor, gate: tuple, up: tuple,
                    dtype=torch.float32, out: torch.Tensor | None = None) -> torch.Tensor:
     """y = silu(g) * u with g, u the gemm_i8 of a with gate and up, each (w, w_scales)."""
-    M, K = _i8_rows(a, a_scales)
-    N = _i8_pair(a, gate, up, (None, K))
-    t = _i8_type(dtype, "dtype")
-    out = _i8_out(out, M, N, dtype, a.device)
+    t = I8_TYPES.get(dtype)
     (wg, sg), (wu, su) = gate, up
-    _i8_call("gemm_i8_swiglu", a.device, _ptr(a), _ptr(a_scales), _ptr(wg), _ptr(sg), _ptr(wu), _ptr(su), _ptr(out),
-             t, M, N, K)
+    try:
+        dev, (M, K) = a.get_device(), a.shape
+        fine = (a.dtype is _I8 and a_scales.dtype is _F32 and dev >= 0 and a_scales.get_device() == dev
+                and a_scales.shape == (M,) and a.is_contiguous() and a_scales.is_contiguous() and t is not None
+                and wg.dim() == 2 and _i8_pair_fine(dev, K, (), wg, sg, wu, su)
+                and (out is None or (out.dtype is dtype and out.get_device() == dev
+                                     and out.shape == (M, wg.shape[0]) and out.is_contiguous())))
+    except (AttributeError, ValueError):
+        fine = False
+    if not fine:
+        _i8_refuse_pair(a, a_scales, gate, up, None, out, dtype)
+    N = wg.shape[0]
+    if out is None:
+        out = torch.empty((M, N), dtype=dtype, device=a.device)
+    _i8_call("gemm_i8_swiglu", dev, a.data_ptr(), a_scales.data_ptr(), wg.data_ptr(), sg.data_ptr(), wu.data_ptr(),
+             su.data_ptr(), out.data_ptr(), t, M, N, K)
     return out
-
-
-def _i8_offsets(offsets: torch.Tensor, dev: torch.device) -> int:
-    _need(offsets, "offsets", (torch.int32,), dev)
-    if offsets.dim() != 1 or offsets.numel() < 2:
-        raise ValueError("offsets must be [E + 1] with E >= 1")
-    return offsets.numel() - 1
 
 
 def gemm_i8_grouped(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
                     offsets: torch.Tensor, dtype=torch.float32,
                     out: torch.Tensor | None = None) -> torch.Tensor:
     """The gemm_i8 of rows offsets[e] .. offsets[e + 1] of a with matrix e of w
-    [E, N, K], w_scales [E, N].  offsets is int32 [E + 1] on the GPU.  Rows
-    outside every group are not written."""
-    M, K = _i8_rows(a, a_scales)
-    E = _i8_offsets(offsets, a.device)
-    _i8_matrix(w, w_scales, (E, None, K), "w")
-    if w.device != a.device:
-        raise ValueError(f"w is on {w.device}, expected {a.device}")
-    N = w.shape[1]
-    t = _i8_type(dtype, "dtype")
-    out = _i8_out(out, M, N, dtype, a.device)
-    _i8_call("gemm_i8_grouped", a.device, _ptr(a), _ptr(a_scales), _ptr(w), _ptr(w_scales), _ptr(offsets), _ptr(out),
-             t, M, E, N, K)
+    [E, N, K], w_scales [E, N].  offsets is int32 [E + 1] on the GPU, and is
+    read there.  Rows outside every group are not written."""
+    t = I8_TYPES.get(dtype)
+    try:
+        dev, (M, K), (E, N, Kw) = a.get_device(), a.shape, w.shape
+        fine = (a.dtype is _I8 and w.dtype is _I8 and a_scales.dtype is _F32 and w_scales.dtype is _F32
+                and offsets.dtype is _I32 and dev >= 0 and w.get_device() == dev and a_scales.get_device() == dev
+                and w_scales.get_device() == dev and offsets.get_device() == dev and K == Kw
+                and a_scales.shape == (M,) and w_scales.shape == (E, N) and offsets.shape == (E + 1,)
+                and a.is_contiguous() and w.is_contiguous() and a_scales.is_contiguous()
+                and w_scales.is_contiguous() and offsets.is_contiguous() and t is not None
+                and (out is None or (out.dtype is dtype and out.get_device() == dev and out.shape == (M, N)
+                                     and out.is_contiguous())))
+    except (AttributeError, ValueError):
+        fine = False
+    if not fine:
+        E = None if _size(offsets, 0) is None else _size(offsets, 0) - 1
+        _i8_refuse({"a": (a, (_I8,)), "a_scales": (a_scales, (_F32,)), "w": (w, (_I8,)), "w_scales": (w_scales, (_F32,)),
+                    "offsets": (offsets, (_I32,)), "out": (out, (dtype,))},
+                   {"a": (a, (None, None)), "a_scales": (a_scales, (_size(a, 0),)), "offsets": (offsets, (None,)),
+                    "w": (w, (E, None, _size(a, 1))), "w_scales": (w_scales, (E, _size(w, 1))),
+                    "out": (out, (_size(a, 0), _size(w, 1)))}, dtype)
+    if out is None:
+        out = torch.empty((M, N), dtype=dtype, device=a.device)
+    _i8_call("gemm_i8_grouped", dev, a.data_ptr(), a_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(),
+             offsets.data_ptr(), out.data_ptr(), t, M, E, N, K)
     return out
 
 
@@ -571,12 +614,22 @@ def gemm_i8_grouped_swiglu(a: torch.Tensor, a_scales: torch.Tensor, gate: tuple,
                            offsets: torch.Tensor, dtype=torch.float32,
                            out: torch.Tensor | None = None) -> torch.Tensor:
     """gemm_i8_swiglu of rows offsets[e] .. offsets[e + 1] with matrices e of gate and up."""
-    M, K = _i8_rows(a, a_scales)
-    E = _i8_offsets(offsets, a.device)
-    N = _i8_pair(a, gate, up, (E, None, K))
-    t = _i8_type(dtype, "dtype")
-    out = _i8_out(out, M, N, dtype, a.device)
+    t = I8_TYPES.get(dtype)
     (wg, sg), (wu, su) = gate, up
-    _i8_call("gemm_i8_grouped_swiglu", a.device, _ptr(a), _ptr(a_scales), _ptr(wg), _ptr(sg), _ptr(wu), _ptr(su),
-             _ptr(offsets), _ptr(out), t, M, E, N, K)
+    try:
+        dev, (M, K), (E, N, _) = a.get_device(), a.shape, wg.shape
+        fine = (a.dtype is _I8 and a_scales.dtype is _F32 and offsets.dtype is _I32 and dev >= 0
+                and a_scales.get_device() == dev and offsets.get_device() == dev and a_scales.shape == (M,)
+                and offsets.shape == (E + 1,) and a.is_contiguous() and a_scales.is_contiguous()
+                and offsets.is_contiguous() and t is not None and _i8_pair_fine(dev, K, (E,), wg, sg, wu, su)
+                and (out is None or (out.dtype is dtype and out.get_device() == dev and out.shape == (M, N)
+                                     and out.is_contiguous())))
+    except (AttributeError, ValueError):
+        fine = False
+    if not fine:
+        _i8_refuse_pair(a, a_scales, gate, up, offsets, out, dtype)
+    if out is None:
+        out = torch.empty((M, N), dtype=dtype, device=a.device)
+    _i8_call("gemm_i8_grouped_swiglu", dev, a.data_ptr(), a_scales.data_ptr(), wg.data_ptr(), sg.data_ptr(),
+             wu.data_ptr(), su.data_ptr(), offsets.data_ptr(), out.data_ptr(), t, M, E, N, K)
     return out

@@ -31,7 +31,6 @@ struct Args {
     void *y;
     int y_type, M, N, K, E;
     int tiles_m, tiles_n;
-    bool vec;                  // rows of y may be written in 16-byte stores
 };
 
 // The fragment of 16 weight rows j (of F that share a run of 16 F rows) takes
@@ -47,8 +46,14 @@ __device__ __forceinline__ uint32_t bits16(float v, int type) {
     return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)v);
 }
 
+// Stores of 16 and 8 bytes that need no more than their elements' alignment
+// (the hardware takes any address; rows of odd N start anywhere).
+typedef u32x4_t u32x4_at4_t __attribute__((aligned(4)));
+typedef u32x4_t u32x4_at2_t __attribute__((aligned(2)));
+typedef u32x2_t u32x2_at2_t __attribute__((aligned(2)));
+
 // Writes the run v[0 .. C) of row m from column n on, its columns past N
-// left out.  16-byte stores where the rows allow them.
+// left out.
 template <int C>
 __device__ __forceinline__ void store_run(const Args &p, int m, int n, const float (&v)[C]) {
     if (n >= p.N) return;
@@ -56,10 +61,10 @@ __device__ __forceinline__ void store_run(const Args &p, int m, int n, const flo
     const bool whole = n + C <= p.N;
     if (p.y_type == I8_F32) {
         float *y = static_cast<float *>(p.y) + at;
-        if (p.vec && whole) {
+        if (whole) {
 #pragma unroll
             for (int c = 0; c < C; c += 4)
-                *reinterpret_cast<u32x4_t *>(y + c) =
+                *reinterpret_cast<u32x4_at4_t *>(y + c) =
                     u32x4_t{__builtin_bit_cast(uint32_t, v[c]), __builtin_bit_cast(uint32_t, v[c + 1]),
                             __builtin_bit_cast(uint32_t, v[c + 2]), __builtin_bit_cast(uint32_t, v[c + 3])};
         } else {
@@ -70,25 +75,22 @@ __device__ __forceinline__ void store_run(const Args &p, int m, int n, const flo
         return;
     }
     uint16_t *y = static_cast<uint16_t *>(p.y) + at;
-    uint32_t b[C];
+    uint32_t b[C / 2];
 #pragma unroll
-    for (int c = 0; c < C; ++c) b[c] = bits16(v[c], p.y_type);
-    if (p.vec && whole) {
+    for (int c = 0; c < C / 2; ++c) b[c] = bits16(v[2 * c], p.y_type) | bits16(v[2 * c + 1], p.y_type) << 16;
+    if (whole) {
         if constexpr (C % 8 == 0) {
 #pragma unroll
-            for (int c = 0; c < C; c += 8)
-                *reinterpret_cast<u32x4_t *>(y + c) =
-                    u32x4_t{b[c] | b[c + 1] << 16, b[c + 2] | b[c + 3] << 16, b[c + 4] | b[c + 5] << 16,
-                            b[c + 6] | b[c + 7] << 16};
+            for (int c = 0; c < C / 2; c += 4)
+                *reinterpret_cast<u32x4_at2_t *>(y + 2 * c) = u32x4_t{b[c], b[c + 1], b[c + 2], b[c + 3]};
         } else {
 #pragma unroll
-            for (int c = 0; c < C; c += 4)
-                *reinterpret_cast<u32x2_t *>(y + c) = u32x2_t{b[c] | b[c + 1] << 16, b[c + 2] | b[c + 3] << 16};
+            for (int c = 0; c < C / 2; c += 2) *reinterpret_cast<u32x2_at2_t *>(y + 2 * c) = u32x2_t{b[c], b[c + 1]};
         }
     } else {
 #pragma unroll
         for (int c = 0; c < C; ++c)
-            if (n + c < p.N) y[c] = (uint16_t)b[c];
+            if (n + c < p.N) y[c] = (uint16_t)(b[c / 2] >> (16 * (c & 1)));
     }
 }
 
@@ -182,83 +184,21 @@ __device__ __forceinline__ void tile_of(const Args &p, int &tm, int &tn) {
 constexpr int BK = 128;
 __device__ __forceinline__ int slot(int r, int c) { return r * BK + ((c ^ (r & 7)) << 4); }
 
-// One 64 x 64 tile (with SWI: 32 columns of each matrix), four wavefronts of
-// 32 x 32 each.  Tiles pass through registers into one LDS buffer.
-template <bool SWI>
-__global__ __launch_bounds__(256) void gemm_i8_tile(Args p) {
-    constexpr int BM = 64, BW = 64, BN = SWI ? 32 : 64;
-    __shared__ __align__(16) char lds[(BM + BW) * BK];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int wm = wave >> 1, wn = wave & 1;
-    int tm, tn;
-    tile_of(p, tm, tn);
-    const Tile tl = find_tile<BM>(p, tm);
-    if (tl.rows <= 0) return;
-    const int n0 = tn * BN;
-    const size_t mat = (size_t)tl.e * p.N;
-
-    i32x4_t acc[2][2] = {};
-    const int kc = p.K >> 4;       // 16-byte chunks of a row
-    for (int k0 = 0; k0 < kc; k0 += 8) {
-#pragma unroll
-        for (int i = 0; i < (BM + BW) * 8 / 256; ++i) {
-            const int q = i * 256 + tid, r = q >> 3, c = q & 7;
-            i32x4_t v = {0, 0, 0, 0};
-            if (k0 + c < kc) {
-                if (r < BM) {
-                    if (r < tl.rows)
-                        v = *reinterpret_cast<const i32x4_t *>(p.a + (size_t)(tl.m0 + r) * p.K + (size_t)(k0 + c) * 16);
-                } else {
-                    // SWI: each wavefront's 32 weight rows are 16 of gate, then 16 of up.
-                    const int b = r - BM, s = SWI ? (b >> 4) & 1 : 0;
-                    const int n = n0 + (SWI ? (b >> 5) * 16 + (b & 15) : b);
-                    if (n < p.N)
-                        v = *reinterpret_cast<const i32x4_t *>(p.w[s] + (mat + n) * p.K + (size_t)(k0 + c) * 16);
-                }
-            }
-            *reinterpret_cast<i32x4_t *>(lds + slot(r, c)) = v;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-            const int c = kk * 4 + (lane >> 4);
-            i32x4_t x[2], w[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                x[i] = *reinterpret_cast<const i32x4_t *>(lds + slot(wm * 32 + i * 16 + (lane & 15), c));
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int r = SWI ? j * 16 + (lane & 15) : frag_row<2>(j, lane & 15);
-                w[j] = *reinterpret_cast<const i32x4_t *>(lds + slot(BM + wn * 32 + r, c));
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[j], x[i], acc[i][j], 0, 0, 0);
-        }
-        __syncthreads();
-    }
-
-    constexpr int C = SWI ? 4 : 8;       // consecutive columns of a lane
-    finish<2, C, SWI>(p, acc, tl, mat, wm * 32, n0 + (SWI ? wn * 16 : wn * 32) + (lane >> 4) * C, lane);
-}
-
-// ---------------------------------------------------------------- large tiles
+// ---------------------------------------------------------------- tiles
 //
-// A 256 x 256 tile (with SWI: 128 columns of each matrix), eight wavefronts
-// of 128 x 64.  Steps of 128 bytes of K pass through two LDS buffers, loaded
-// straight from memory (buffer loads to LDS, 1 KiB an instruction: eight rows
-// of 128 bytes, the lanes' chunk order making the swizzle).  A step has two
-// halves of 64 bytes; the fragments of each half are read into registers
-// while the other half's products run:
+// A tile of BM rows and BW weight rows (with SWI: BW / 2 of each matrix) by
+// eight wavefronts, WM x WN of them.  Steps of 128 bytes of K pass through a
+// ring of D stages in LDS, loaded straight from memory (buffer loads to LDS,
+// 1 KiB an instruction: eight rows of 128 bytes, the lanes' chunk order
+// making the swizzle).  A step has two halves of 64 bytes; the fragments of
+// each half are read into registers while the other half's products run:
 //
 //     first half:   read (t, second half),  products of (t, first half)
 //                   wait for step t + 1 in LDS and for this step's reads
-//     second half:  load step t + 2 over step t,  read (t + 1, first half),
+//     second half:  load step t + D over step t,  read (t + 1, first half),
 //                   products of (t, second half)
 //
-// so there is one barrier a step, and a step's loads have a whole step to
+// so there is one barrier a step, and a step's loads have D - 1 steps to
 // arrive.  A last step that K does not fill is taken as the last 128 bytes
 // of the rows, with the activations already used set to zero; every address
 // stays inside the rows.  Rows past the tile's end repeat its last row, and
@@ -269,13 +209,50 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const int8_t *base, ui
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t *>(base), 0, (int)bytes, 0x00020000);
 }
 
-template <bool SWI>
-__global__ __launch_bounds__(512, 2) void gemm_i8_large(Args p) {
-    constexpr int BM = 256, BW = 256, BN = SWI ? 128 : 256;
+// 16 bytes a lane from memory to LDS, lane l's at `to` + 16 l.
+__device__ __forceinline__ void load16(__amdgpu_buffer_rsrc_t r, char *to, uint32_t voff, int soff) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t)to, 16, voff, soff, 0, 0);
+}
+
+template <int N>
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
+
+// Waits until at most `n` (0 .. MOST) batches of L loads are on their way.
+template <int L, int MOST>
+__device__ __forceinline__ void wait_batches(int n) {
+    if constexpr (MOST == 0) wait_loads<0>();
+    else if (n >= MOST) wait_loads<L * MOST>();
+    else wait_batches<L, MOST - 1>(n);
+}
+
+// Orders the instructions of one half step: a product first, then the loads,
+// then the LDS reads, each behind a product, then the products left.
+template <int LOADS, int READS, int PRODUCTS>
+__device__ __forceinline__ void interleave() {
+    if constexpr (LOADS + READS <= PRODUCTS) {
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < READS; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x008, PRODUCTS - LOADS - READS, 0);
+    }
+}
+
+template <int BM, int BW, int WM, int WN, int D, bool SWI>
+__global__ __launch_bounds__(512, 2) void gemm_i8_block(Args p) {
+    static_assert(WM * WN == 8, "eight wavefronts");
+    constexpr int FM = BM / WM / 16, FW = BW / WN / 16, BN = SWI ? BW / 2 : BW;
+    constexpr int LX = BM / 64, LW = BW / 64, LOADS = LX + LW;       // load instructions of a wavefront and step
     constexpr int STAGE = (BM + BW) * BK;
     extern __shared__ __align__(16) char lds[];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wm = wave >> 2, wn = wave & 3;
+    const int wm = wave / WN, wn = wave % WN;
     int tm, tn;
     tile_of(p, tm, tn);
     const Tile tl = find_tile<BM>(p, tm);
@@ -283,110 +260,235 @@ __global__ __launch_bounds__(512, 2) void gemm_i8_large(Args p) {
     const int n0 = tn * BN, cols = min(BN, p.N - n0);
     const size_t mat = (size_t)tl.e * p.N;
 
-    // Loads: this wavefront brings rows 32 wave .. 32 wave + 31 of both
-    // halves of a stage, eight rows an instruction.
+    // Loads: this wavefront brings an eighth of the rows of a and of w.
     const __amdgpu_buffer_rsrc_t ra = rsrc_of(p.a + (size_t)tl.m0 * p.K, (uint32_t)tl.rows * p.K);
-    // SWI: the 32 weight rows of one wavefront's loads are all gate or all up.
-    const int8_t *wbase = SWI && (wave & 1) ? p.w[1] : p.w[0];
+    // SWI: the weight rows that one wavefront loads are all gate or all up.
+    const int8_t *wbase = SWI && wave * LW / 2 % FW >= FW / 2 ? p.w[1] : p.w[0];
     const __amdgpu_buffer_rsrc_t rw = rsrc_of(wbase + (mat + n0) * p.K, (uint32_t)cols * p.K);
-    uint32_t va[4], vw[4];
+    uint32_t va[LX], vw[LW];
     const int chunk = ((lane & 7) ^ (lane >> 3)) << 4;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = wave * 32 + i * 8 + (lane >> 3);
-        va[i] = (uint32_t)min(r, tl.rows - 1) * p.K + chunk;
-        // Row r of the weight half belongs to wavefront column r / 64, its
-        // fragment (r / 16) % 4, row r % 16 of it.
-        const int c = r >> 6, j = (r >> 4) & 3, q = r & 15;
-        const int n = SWI ? c * 32 + frag_row<2>(j & 1, q) : c * 64 + frag_row<4>(j, q);
+    for (int i = 0; i < LX; ++i)
+        va[i] = (uint32_t)min((wave * LX + i) * 8 + (lane >> 3), tl.rows - 1) * p.K + chunk;
+#pragma unroll
+    for (int i = 0; i < LW; ++i) {
+        // Row r belongs to wavefront column c, its fragment j, row q of it.
+        const int r = (wave * LW + i) * 8 + (lane >> 3), c = r / (16 * FW), j = r / 16 % FW, q = r & 15;
+        const int n = SWI ? c * (8 * FW) + frag_row<FW / 2>(j % (FW / 2), q) : c * (16 * FW) + frag_row<FW>(j, q);
         vw[i] = (uint32_t)min(n, cols - 1) * p.K + chunk;
     }
-    auto load = [&](int buf, int koff) {
-        char *at = lds + buf * STAGE + wave * 32 * BK;
+    auto load = [&](int slot, int koff) {
+        char *at = lds + slot * STAGE + wave * 1024;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_ptr_t)(at + i * 8 * BK), 16, va[i], koff, 0, 0);
+        for (int i = 0; i < LX; ++i) load16(ra, at + (wave * (LX - 1) + i) * 1024, va[i], koff);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_ptr_t)(at + BM * BK + i * 8 * BK), 16, vw[i], koff, 0,
-                                                     0);
+        for (int i = 0; i < LW; ++i) load16(rw, at + (BM / 8 + wave * (LW - 1) + i) * 1024, vw[i], koff);
     };
 
     // Fragment reads: lane l takes row l % 16, chunk l / 16 (+ 4 in the
     // second half, which flips bit 6 of the swizzled address).
     const int fr = (lane & 15) * BK + (((lane >> 4) ^ (lane & 7)) << 4);
-    const char *xa = lds + wm * 128 * BK + fr, *wa = lds + (BM + wn * 64) * BK + fr;
-    const char *xb = lds + wm * 128 * BK + (fr ^ 64), *wb = lds + (BM + wn * 64) * BK + (fr ^ 64);
-    i32x4_t acc[8][4] = {};
-    i32x4_t x0[8], w0[4], x1[8], w1[4];
-    auto read = [&](i32x4_t (&x)[8], i32x4_t (&w)[4], const char *px, const char *pw) {
+    const int xat = wm * (16 * FM) * BK, wat = (BM + wn * (16 * FW)) * BK;
+    i32x4_t acc[FM][FW] = {};
+    i32x4_t x0[FM], w0[FW], x1[FM], w1[FW];
+    auto read = [&](i32x4_t (&x)[FM], i32x4_t (&w)[FW], int slot, int f) {
+        const char *at = lds + slot * STAGE + f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const i32x4_t *>(pw + j * 16 * BK);
+        for (int j = 0; j < FW; ++j) w[j] = *reinterpret_cast<const i32x4_t *>(at + wat + j * 16 * BK);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = *reinterpret_cast<const i32x4_t *>(px + i * 16 * BK);
+        for (int i = 0; i < FM; ++i) x[i] = *reinterpret_cast<const i32x4_t *>(at + xat + i * 16 * BK);
     };
-    auto products = [&](const i32x4_t (&x)[8], const i32x4_t (&w)[4]) {
+    auto products = [&](const i32x4_t (&x)[FM], const i32x4_t (&w)[FW]) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < FM; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[j], x[i], acc[i][j], 0, 0, 0);
+            for (int q = 0; q < FW; ++q) {
+                const int j = i & 1 ? FW - 1 - q : q;
+                acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[j], x[i], acc[i][j], 0, 0, 0);
+            }
     };
     const int steps = (p.K + BK - 1) / BK;
     auto koff = [&](int t) { return min(t * BK, p.K - BK); };
     // Chunks of the last step that earlier steps have used.
     const int used = steps * 8 - (p.K >> 4);
-    auto drop = [&](i32x4_t (&x)[8], int c) {
+    auto drop = [&](i32x4_t (&x)[FM], int c) {
         if (c < used) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = i32x4_t{0, 0, 0, 0};
+            for (int i = 0; i < FM; ++i) x[i] = i32x4_t{0, 0, 0, 0};
         }
     };
-
-    load(0, koff(0));
-    if (steps > 1) load(1, koff(1));
-    if (steps > 1) asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
-    else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    asm volatile("s_barrier" ::: "memory");
-    read(x0, w0, xa, wa);
-    if (steps == 1 && used) drop(x0, lane >> 4);
-    auto wait = [&]() {
+    auto barrier = [&]() {       // and this wavefront's LDS reads are done
         __builtin_amdgcn_sched_barrier(0);
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
     };
+
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+        if (d < steps) load(d, koff(d));
+    wait_batches<LOADS, D - 1>(steps - 1);
+    barrier();
+    read(x0, w0, 0, fr);
+    if (steps == 1 && used) drop(x0, lane >> 4);
     int t = 0;
-    auto whole = [&](int buf) {          // a step with two full ones behind it
-        const int cur = buf * STAGE, nxt = STAGE - cur;
-        read(x1, w1, xb + cur, wb + cur);
+    auto whole = [&](int slot, int next) {          // a step with D full ones behind it
+        read(x1, w1, slot, fr ^ 64);
         products(x0, w0);
-        wait();
-        load(buf, (t + 2) * BK);
-        read(x0, w0, xa + nxt, wa + nxt);
+        interleave<0, FM + FW, FM * FW>();
+        __builtin_amdgcn_sched_barrier(0);
+        wait_loads<(D - 2) * LOADS>();
+        barrier();
+        load(slot, (t + D) * BK);
+        read(x0, w0, next, fr);
         products(x1, w1);
+        interleave<LOADS, FM + FW, FM * FW>();
         __builtin_amdgcn_sched_barrier(0);
         ++t;
     };
-    while (t + 4 < steps) {
-        whole(0);
-        whole(1);
+    while (t + 2 * D < steps) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) whole(d, (d + 1) % D);
     }
-    for (; t < steps; ++t) {
-        const int cur = (t & 1) * STAGE, nxt = STAGE - cur;
-        read(x1, w1, xb + cur, wb + cur);
+    for (int slot = 0; t < steps; ++t) {
+        const int next = slot + 1 == D ? 0 : slot + 1;
+        read(x1, w1, slot, fr ^ 64);
         if (t + 1 == steps && used) drop(x1, 4 + (lane >> 4));
         products(x0, w0);
-        wait();
-        if (t + 2 < steps) load(t & 1, koff(t + 2));
+        __builtin_amdgcn_sched_barrier(0);
+        wait_batches<LOADS, D - 2>(steps - t - 2);       // step t + 1 has come
+        barrier();
+        if (t + D < steps) load(slot, koff(t + D));
         if (t + 1 < steps) {
-            read(x0, w0, xa + nxt, wa + nxt);
+            read(x0, w0, next, fr);
             if (t + 2 == steps && used) drop(x0, lane >> 4);
         }
         products(x1, w1);
         __builtin_amdgcn_sched_barrier(0);
+        slot = next;
     }
 
-    constexpr int C = SWI ? 8 : 16;      // consecutive columns of a lane
-    finish<8, C, SWI>(p, acc, tl, mat, wm * 128, n0 + (SWI ? wn * 32 : wn * 64) + (lane >> 4) * C, lane);
+    constexpr int C = SWI ? 2 * FW : 4 * FW;      // consecutive columns of a lane
+    finish<FM, C, SWI>(p, acc, tl, mat, wm * (16 * FM), n0 + wn * (4 * C) + (lane >> 4) * C, lane);
+}
+
+// ---------------------------------------------------------------- few rows
+//
+// Up to 8 NX rows: the weights are streamed once, and what counts is the
+// bytes in flight.  A wavefront takes FN strips of 16 weight rows (of each
+// matrix) and every KS-th unit of 128 bytes of K; KS wavefronts of a
+// workgroup meet in LDS at the end.  Its units pass through a ring of D
+// slots of its own in LDS, loaded straight from memory eight rows of 128
+// bytes an instruction (a fragment's own order, 16 rows of 64 bytes, loads
+// the same bytes at 3/4 of the rate or less), the next unit issued as soon
+// as a slot has been read: no barrier, and D - 1 units in flight while one
+// is multiplied.  Units past K repeat the row's last 16 bytes against
+// activations of zero.
+template <int NX, int FN, bool SWI, int W, int D>
+__global__ __launch_bounds__(W * 64) void gemm_i8_few(Args p, int ks_log2) {
+    constexpr int FM = (NX + 1) / 2, BM = 8 * NX, MATS = SWI ? 2 : 1, FW = FN * MATS;
+    constexpr int LOADS = 2 * FW + NX;             // load instructions of a unit
+    constexpr int SLOT = (2 * FW + 2 * FM) * 1024; // whole fragments, the last may be half loaded
+    extern __shared__ __align__(16) char lds[];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int KS = 1 << ks_log2, ks = wave & (KS - 1);
+    const int tn = (int)(blockIdx.x % p.tiles_n);
+    const Tile tl = find_tile<BM>(p, (int)(blockIdx.x / p.tiles_n));
+    if (tl.rows <= 0) return;
+    const int n0 = (tn * (W >> ks_log2) + (wave >> ks_log2)) * (16 * FN);
+    const size_t mat = (size_t)tl.e * p.N;
+    const int kc = p.K >> 4, units = (kc + 7) >> 3;
+    const int g = lane >> 4, r = lane & 15;
+    i32x4_t acc[FM][FW] = {};
+
+    if (n0 < p.N) {
+        char *ring = lds + wave * (D * SLOT);
+        const int cols = min(16 * FN, p.N - n0);
+        const __amdgpu_buffer_rsrc_t rx = rsrc_of(p.a + (size_t)tl.m0 * p.K, (uint32_t)tl.rows * p.K);
+        __amdgpu_buffer_rsrc_t rw[MATS];
+#pragma unroll
+        for (int s = 0; s < MATS; ++s) rw[s] = rsrc_of(p.w[s] + (mat + n0) * p.K, (uint32_t)cols * p.K);
+        uint32_t vx[NX], vw[2 * FN];
+#pragma unroll
+        for (int i = 0; i < NX; ++i) vx[i] = (uint32_t)min(i * 8 + (lane >> 3), tl.rows - 1) * p.K;
+#pragma unroll
+        for (int i = 0; i < 2 * FN; ++i) {
+            const int q = (i & 1) * 8 + (lane >> 3);               // row of fragment i / 2
+            vw[i] = (uint32_t)min(frag_row<FN>(i >> 1, q), cols - 1) * p.K;
+        }
+        const int chunk = (lane & 7) ^ (lane >> 3);
+        auto load = [&](int slot, int u) {
+            char *at = ring + slot * SLOT;
+            const uint32_t k = (uint32_t)min(u * 8 + chunk, kc - 1) << 4;
+#pragma unroll
+            for (int s = 0; s < MATS; ++s)
+#pragma unroll
+                for (int i = 0; i < 2 * FN; ++i)
+                    load16(rw[s], at + (s * 2 * FN + i) * 1024, vw[i] + k, 0);
+#pragma unroll
+            for (int i = 0; i < NX; ++i)
+                load16(rx, at + (2 * FW + i) * 1024, vx[i] + k, 0);
+        };
+        const int fr = r * BK + ((g ^ (r & 7)) << 4);
+        auto products = [&](int slot, int u) {
+            const char *at = ring + slot * SLOT;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const char *f = at + (h ? fr ^ 64 : fr);
+                i32x4_t w[FW], x[FM];
+#pragma unroll
+                for (int j = 0; j < FW; ++j) w[j] = *reinterpret_cast<const i32x4_t *>(f + j * 2048);
+#pragma unroll
+                for (int i = 0; i < FM; ++i) x[i] = *reinterpret_cast<const i32x4_t *>(f + (FW + i) * 2048);
+                if (u * 8 + 8 > kc && u * 8 + h * 4 + g >= kc) {
+#pragma unroll
+                    for (int i = 0; i < FM; ++i) x[i] = i32x4_t{0, 0, 0, 0};
+                }
+#pragma unroll
+                for (int i = 0; i < FM; ++i)
+#pragma unroll
+                    for (int j = 0; j < FW; ++j)
+                        acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[j], x[i], acc[i][j], 0, 0, 0);
+            }
+        };
+        int left = (units - ks + KS - 1) >> ks_log2, u = ks, slot = 0;      // this wavefront's units
+#pragma unroll
+        for (int d = 0; d < D; ++d)
+            if (d < left) load(d, ks + d * KS);
+        for (; left > D; --left, u += KS) {
+            wait_loads<(D - 1) * LOADS>();
+            products(slot, u);
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");      // the slot has been read
+            load(slot, u + D * KS);
+            if (++slot == D) slot = 0;
+        }
+        for (; left > 0; --left, u += KS) {
+            if (D > 3 && left == 4) wait_loads<3 * LOADS>();
+            else if (D > 2 && left == 3) wait_loads<2 * LOADS>();
+            else if (left == 2) wait_loads<LOADS>();
+            else wait_loads<0>();
+            products(slot, u);
+            if (++slot == D) slot = 0;
+        }
+    }
+    if (KS > 1) {
+        // Every wavefront has read its ring: the partial sums take its place.
+        __syncthreads();
+        i32x4_t *part = reinterpret_cast<i32x4_t *>(lds) + lane;
+        if (ks > 0) {
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int j = 0; j < FW; ++j) part[(wave * FM * FW + i * FW + j) * 64] = acc[i][j];
+        }
+        __syncthreads();
+        if (ks > 0) return;
+        for (int k = 1; k < KS; ++k)
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int j = 0; j < FW; ++j) acc[i][j] += part[((wave + k) * FM * FW + i * FW + j) * 64];
+    }
+    finish<FM, 4 * FN, SWI>(p, acc, tl, mat, 0, n0 + g * (4 * FN), lane);
 }
 
 constexpr int kMaxRows = 1 << 24;
@@ -394,11 +496,98 @@ constexpr int kMaxK = 131056;      // 16384 * 131056 < 2^31: the sum fits whatev
 
 bool elem_aligned(const void *y, int type) { return q4::aligned(y, type == I8_F32 ? 4 : 2); }
 
-int run(Args p, int mats, hipStream_t stream) {
+constexpr int64_t kMaxThreads = 0xFFFFFFFFll;      // of one launch
+
+int64_t tiles_of(int64_t n, int tile) { return (n + tile - 1) / tile; }
+
+// Tiles of bm rows that a call may need: every group may end inside one.
+int64_t row_tiles(const Args &p, int bm) {
+    return p.offsets ? p.M / bm + std::min(p.E, p.M) : tiles_of(p.M, bm);
+}
+
+template <int NX, int FN, bool SWI, int W>
+int launch_few(Args p, hipStream_t stream) {
+    constexpr int FM = (NX + 1) / 2, FW = FN * (SWI ? 2 : 1), D = 2;
+    const int64_t tiles_m = row_tiles(p, 8 * NX), strips = tiles_of(p.N, 16 * FN), units = tiles_of(p.K, BK);
+    // Wavefronts on one strip's K: as many as it takes for 1536 wavefronts,
+    // 6 for each CU, while each has a unit.  At 8 rows, 4096 -> 14336, 2 of
+    // them take 11.8 us and 8 take 13.6; at 24 rows, 14336 -> 4096, 8 take
+    // 12.0 and 2 take 26.1.
+    int log2 = 0;
+    while ((2 << log2) <= W && (units >> log2) > 1 && (tiles_m * strips) << log2 < 1536) ++log2;
+    p.tiles_m = (int)tiles_m;
+    p.tiles_n = (int)tiles_of(strips, W >> log2);
+    const int64_t grid = tiles_m * p.tiles_n;
+    if (grid * (W * 64) > kMaxThreads) return Q4_EINVAL;
+    gemm_i8_few<NX, FN, SWI, W, D><<<(unsigned)grid, W * 64, W * D * (2 * FW + 2 * FM) * 1024, stream>>>(p, log2);
+    return q4::launch_status();
+}
+
+template <int BM, int BW, int D, bool SWI>
+int launch_block(Args p, hipStream_t stream) {
+    p.tiles_m = (int)row_tiles(p, BM);
+    p.tiles_n = (int)tiles_of(p.N, SWI ? BW / 2 : BW);
+    const int64_t grid = (int64_t)p.tiles_m * p.tiles_n;
+    if (grid * 512 > kMaxThreads) return Q4_EINVAL;
+    gemm_i8_block<BM, BW, 2, 4, D, SWI><<<(unsigned)grid, 512, D * (BM + BW) * BK, stream>>>(p);
+    return q4::launch_status();
+}
+
+enum Kernel { kFew8, kFew16, kFew32, kFew64, kTile64, kTile128, kTile256 };
+
+// The kernel for a call's sizes.  Up to 32 rows the weights' stream decides.
+// Above that, each kernel's time is estimated from its tiles and steps, with
+// constants fitted to 370 measured shapes (33 to 8192 rows, N 64 to 14336, K
+// 256 to 14336; the choice is on average 0.7% behind the best of the five
+// measured): fixed us a tile, us a step, and how far more tiles than CUs
+// stretch it.  The 256-row tile has a CU to itself, so its rounds are whole.
+// Groups go by their average rows, their sizes being known to the GPU alone.
+Kernel choose(const Args &p, int mats) {
+    const int64_t steps = tiles_of(p.K, BK);
+    if (p.offsets) {
+        const int64_t rows = tiles_of(p.M, p.E);
+        if (p.K < BK) return rows <= 2 ? kFew8 : rows <= 6 ? kFew16 : kFew64;
+        return rows <= 2 ? kFew8 : rows <= 6 ? kFew16 : rows <= 96 ? kTile64 : rows <= 192 ? kTile128 : kTile256;
+    }
+    if (p.M <= 32) return p.M <= 8 ? kFew8 : p.M <= 16 ? kFew16 : kFew32;
+    if (p.K < BK) return kFew64;
+    auto tiles = [&](int bm, int bw) { return tiles_of(p.M, bm) * tiles_of(p.N, bw / mats); };
+    const double few = tiles(64, 32), t64 = tiles(64, 128), t128 = tiles(128, 128), t256 = tiles(256, 256);
+    const int ks = few < 384 ? 4 : few < 768 ? 2 : 1;            // as launch_few's rule
+    double cost[7];
+    cost[kFew64] = std::max(1.0, few * ks / 1024 * 1.65) * (1.3 + (double)tiles_of(steps, ks) * 0.88);
+    cost[kTile64] = std::max(1.0, t64 / 256 * 1.38) * (0.7 + steps * 0.40);
+    cost[kTile128] = t128 <= 256 ? 2.9 + steps * 0.54 : t128 / 256 * 0.92 * (0.95 + steps * 0.72);
+    cost[kTile256] = (double)tiles_of((int64_t)t256, 256) * (7.0 + steps * 1.3);
+    Kernel best = kFew64;
+    for (Kernel k : {kTile64, kTile128, kTile256})
+        if (cost[k] < cost[best]) best = k;
+    return best;
+}
+
+template <bool SWI>
+int launch(const Args &p, Kernel k, hipStream_t stream) {
+    switch (k) {
+    case kFew8: return launch_few<1, 1, SWI, 8>(p, stream);
+    case kFew16: return launch_few<2, 1, SWI, 8>(p, stream);
+    case kFew32: return launch_few<4, 1, SWI, 8>(p, stream);
+    case kFew64: return launch_few<8, SWI ? 1 : 2, SWI, 4>(p, stream);
+    case kTile64: return launch_block<64, 128, 3, SWI>(p, stream);
+    case kTile128:
+        // Two workgroups share a CU with a ring of two stages; where there is
+        // only one for each CU, it takes four: 1024 x 4096 x 4096 in 19.0
+        // against 24.1 us, but 1999 x 14336 x 4096 in 128 against 112.
+        if (row_tiles(p, 128) * tiles_of(p.N, SWI ? 64 : 128) <= 256) return launch_block<128, 128, 4, SWI>(p, stream);
+        return launch_block<128, 128, 2, SWI>(p, stream);
+    default: return launch_block<256, 256, 2, SWI>(p, stream);
+    }
+}
+
+int run(const Args &p, int mats, hipStream_t stream) {
     if (p.M < 0 || p.M > kMaxRows || p.N < 0 || p.N > kMaxRows || p.K < 16 || p.K % 16 || p.K > kMaxK)
         return Q4_EINVAL;
     if (p.y_type != I8_F32 && p.y_type != I8_F16 && p.y_type != I8_BF16) return Q4_EINVAL;
-    if ((int64_t)((p.M + 15) / 16) * ((p.N + 15) / 16) > 0x7FFFFFFFll) return Q4_EINVAL;
+    if (tiles_of(p.M, 16) * tiles_of(p.N, 16) > 0x7FFFFFFFll) return Q4_EINVAL;
     if (p.E < 1 || p.E > 65536 || (int64_t)p.E * p.N > 0x7FFFFFFFll) return Q4_EINVAL;
     if (p.M == 0 || p.N == 0) return Q4_OK;
     if (!p.a || !p.sa || !p.w[0] || !p.sw[0] || !p.y || (mats == 2 && (!p.w[1] || !p.sw[1]))) return Q4_ENULL;
@@ -407,42 +596,22 @@ int run(Args p, int mats, hipStream_t stream) {
         return Q4_EALIGN;
     if (mats == 2 && (!q4::aligned(p.w[1], 16) || !q4::aligned(p.sw[1], 4))) return Q4_EALIGN;
     if (int st = q4::check_device()) return st;
-    p.vec = q4::aligned(p.y, 16) && (size_t)p.N * (p.y_type == I8_F32 ? 4 : 2) % 16 == 0;
-    const bool large = p.K >= BK && p.M > 128;
-    const int bm = large ? 256 : 64, bn = bm / mats;
-    p.tiles_n = (p.N + bn - 1) / bn;
-    // Groups: every group may end inside a tile.
-    const int64_t tiles_m = p.offsets ? p.M / bm + std::min(p.E, p.M) : (p.M + bm - 1) / bm;
-    const int64_t grid = tiles_m * p.tiles_n;
-    if (grid > 0x7FFFFFFFll) return Q4_EINVAL;
-    p.tiles_m = (int)tiles_m;
-    if (large) {
-        constexpr int lds = 2 * 512 * BK;
-        const void *f = mats == 2 ? (const void *)gemm_i8_large<true> : (const void *)gemm_i8_large<false>;
-        if (hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, lds) != hipSuccess) return Q4_ELAUNCH;
-        if (mats == 2) gemm_i8_large<true><<<(unsigned)grid, 512, lds, stream>>>(p);
-        else gemm_i8_large<false><<<(unsigned)grid, 512, lds, stream>>>(p);
-    } else if (mats == 2) {
-        gemm_i8_tile<true><<<(unsigned)grid, 256, 0, stream>>>(p);
-    } else {
-        gemm_i8_tile<false><<<(unsigned)grid, 256, 0, stream>>>(p);
-    }
-    return q4::launch_status();
+    const Kernel k = choose(p, mats);
+    return mats == 2 ? launch<true>(p, k, stream) : launch<false>(p, k, stream);
 }
 
 }  // namespace
 
 extern "C" int gemm_i8(const int8_t *a, const float *a_scales, const int8_t *w, const float *w_scales,
                        const float *bias, void *y, int y_type, int M, int N, int K, void *stream) {
-    return run({a, a_scales, {w, nullptr}, {w_scales, nullptr}, bias, nullptr, y, y_type, M, N, K, 1, 0, 0, false}, 1,
+    return run({a, a_scales, {w, nullptr}, {w_scales, nullptr}, bias, nullptr, y, y_type, M, N, K, 1, 0, 0}, 1,
                static_cast<hipStream_t>(stream));
 }
 
 extern "C" int gemm_i8_swiglu(const int8_t *a, const float *a_scales, const int8_t *w_gate,
                               const float *scales_gate, const int8_t *w_up, const float *scales_up, void *y,
                               int y_type, int M, int N, int K, void *stream) {
-    return run({a, a_scales, {w_gate, w_up}, {scales_gate, scales_up}, nullptr, nullptr, y, y_type, M, N, K, 1, 0, 0,
-                false},
+    return run({a, a_scales, {w_gate, w_up}, {scales_gate, scales_up}, nullptr, nullptr, y, y_type, M, N, K, 1, 0, 0},
                2, static_cast<hipStream_t>(stream));
 }
 
@@ -450,7 +619,7 @@ extern "C" int gemm_i8_grouped(const int8_t *a, const float *a_scales, const int
                                const int32_t *offsets, void *y, int y_type, int M, int E, int N, int K,
                                void *stream) {
     if (!offsets && M > 0 && N > 0) return Q4_ENULL;
-    return run({a, a_scales, {w, nullptr}, {w_scales, nullptr}, nullptr, offsets, y, y_type, M, N, K, E, 0, 0, false}, 1,
+    return run({a, a_scales, {w, nullptr}, {w_scales, nullptr}, nullptr, offsets, y, y_type, M, N, K, E, 0, 0}, 1,
                static_cast<hipStream_t>(stream));
 }
 
@@ -459,7 +628,6 @@ extern "C" int gemm_i8_grouped_swiglu(const int8_t *a, const float *a_scales, co
                                       const int32_t *offsets, void *y, int y_type, int M, int E, int N, int K,
                                       void *stream) {
     if (!offsets && M > 0 && N > 0) return Q4_ENULL;
-    return run({a, a_scales, {w_gate, w_up}, {scales_gate, scales_up}, nullptr, offsets, y, y_type, M, N, K, E, 0, 0,
-                false},
+    return run({a, a_scales, {w_gate, w_up}, {scales_gate, scales_up}, nullptr, offsets, y, y_type, M, N, K, E, 0, 0},
                2, static_cast<hipStream_t>(stream));
 }
