@@ -26,10 +26,10 @@
  * Sizes: K a multiple of 16 with 16 <= K <= 131056 (the exact sum then fits
  * int32 whatever the codes); 0 <= M, N <= 2^24 with at most 2^31 - 1 tiles of
  * 16 x 16 (and no launch of 2^32 threads or more, which M N beyond about
- * 10^10 would need: Q4_EINVAL); M == 0 or N == 0 returns Q4_OK with nothing launched, before any
- * pointer check.  a and w 16-byte aligned, scales, bias and offsets 4-byte
- * aligned, outputs aligned to their element.  Outputs must not overlap any
- * input.
+ * 10^10 would need: Q4_EINVAL); M == 0 or N == 0 returns Q4_OK with nothing
+ * launched, before any pointer check.  a and w 16-byte aligned, scales, bias
+ * and offsets 4-byte aligned, outputs aligned to their element.  Outputs must
+ * not overlap any input.
  */
 #ifndef Q4I8_H
 #define Q4I8_H
@@ -53,7 +53,7 @@ enum i8_type { I8_F32 = 0, I8_F16 = 1, I8_BF16 = 2 };
  * that of the real quotient, so codes lie in -127..127 and a zero row gets
  * zero codes.  A row holding an Inf or a NaN gets zero codes and the scale
  * NaN, so that every product of the row is NaN.
- *   x  [M, K] of x_type, 16-byte aligned; codes 16-byte aligned. */
+ *   x  [M, K] of x_type, 16-byte aligned; codes 16-byte aligned; M < 2^22. */
 int quant_i8(const void *x, int x_type, int8_t *codes, float *scales, int M, int K, void *stream);
 
 /* y[m, n] = P[m, n] + bias[n]; bias float32 [N] or NULL.  y [M, N] of y_type. */
