@@ -98,32 +98,52 @@ __device__ __forceinline__ void store_run(const Args &p, int m, int n, const flo
 // rows == 0: no such tile.
 struct Tile { int m0, rows, e; };
 
+// A group's rows (0 past the last group), and its tiles of BM rows.  Offsets
+// are held to 0 .. M.
+struct Group { int lo, hi; };
+__device__ __forceinline__ Group group_of(const Args &p, int e) {
+    if (e >= p.E) return {0, 0};
+    const int lo = min(max(p.offsets[e], 0), p.M);
+    return {lo, min(max(p.offsets[e + 1], lo), p.M)};
+}
+
+// Sums over the lanes up to and with each lane.
+__device__ __forceinline__ int scan_lanes(int v) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(v, d);
+        if (lane >= d) v += o;
+    }
+    return v;
+}
+
+// The tiles of BM rows that all groups have.
+template <int BM>
+__device__ __forceinline__ int count_tiles(const Args &p) {
+    if (!p.offsets) return p.tiles_m;
+    int all = 0;
+    for (int e0 = 0; e0 < p.E; e0 += 64) {
+        const Group g = group_of(p, e0 + (threadIdx.x & 63));
+        all += __builtin_amdgcn_readlane(scan_lanes((g.hi - g.lo + BM - 1) / BM), 63);
+    }
+    return all;
+}
+
 // Finds tile t of BM rows among the groups: 64 groups at a time, one a lane,
-// the lanes' tile counts summed by a scan.  Offsets are held to 0 .. M.
+// the lanes' tile counts summed by a scan.
 template <int BM>
 __device__ __forceinline__ Tile find_tile(const Args &p, int t) {
     if (!p.offsets) return {t * BM, min(BM, p.M - t * BM), 0};
-    const int lane = threadIdx.x & 63;
     for (int e0 = 0; e0 < p.E; e0 += 64) {
-        const int e = e0 + lane;
-        int lo = 0, hi = 0;
-        if (e < p.E) {
-            lo = min(max(p.offsets[e], 0), p.M);
-            hi = min(max(p.offsets[e + 1], lo), p.M);
-        }
-        const int mine = (hi - lo + BM - 1) / BM;
-        int upto = mine;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int o = __shfl_up(upto, d);
-            if (lane >= d) upto += o;
-        }
+        const Group g = group_of(p, e0 + (threadIdx.x & 63));
+        const int mine = (g.hi - g.lo + BM - 1) / BM, upto = scan_lanes(mine);
         const int all = __builtin_amdgcn_readlane(upto, 63);
         if (t < all) {
             const int owner = __ffsll((unsigned long long)__ballot(upto > t)) - 1;
-            const int m0 = __builtin_amdgcn_readlane(lo, owner) +
+            const int m0 = __builtin_amdgcn_readlane(g.lo, owner) +
                            (t - __builtin_amdgcn_readlane(upto - mine, owner)) * BM;
-            return {m0, min(BM, __builtin_amdgcn_readlane(hi, owner) - m0), e0 + owner};
+            return {m0, min(BM, __builtin_amdgcn_readlane(g.hi, owner) - m0), e0 + owner};
         }
         t -= all;
     }
@@ -165,17 +185,21 @@ __device__ __forceinline__ void finish(const Args &p, const i32x4_t (&acc)[FM][S
     }
 }
 
-// The tile of this workgroup.  Workgroups are dealt to the eight XCDs in
-// turn, each with its own L2: XCD x takes the x-th eighth of the tiles, and
-// tiles are ordered in bands of eight tile rows, column by column, so that
-// the tiles an XCD runs at one time share rows of a and of w.
-__device__ __forceinline__ void tile_of(const Args &p, int &tm, int &tn) {
-    const int all = gridDim.x, b = blockIdx.x, x = b & 7, per = all >> 3, more = all & 7;
+// The tile (tm, tn) that a workgroup takes, of tiles_m rows of them; false:
+// none.  Workgroups are dealt to the eight XCDs in turn, each with its own L2:
+// XCD x takes the x-th eighth of the tiles (of those that the groups have, not
+// of those that they might have needed), and tiles are ordered in bands of
+// eight tile rows, column by column, so that the tiles an XCD runs at one
+// time share rows of a and of w.
+__device__ __forceinline__ bool tile_of(int b, int tiles_m, int tiles_n, int &tm, int &tn) {
+    const int all = tiles_m * tiles_n, x = b & 7, per = all >> 3, more = all & 7;
+    if ((b >> 3) >= per + (x < more ? 1 : 0)) return false;
     const int t = x * per + min(x, more) + (b >> 3);
-    const int band = t / (8 * p.tiles_n), first = band * 8, rows = min(8, p.tiles_m - first);
-    const int in = t - band * 8 * p.tiles_n;
+    const int band = t / (8 * tiles_n), first = band * 8, rows = min(8, tiles_m - first);
+    const int in = t - band * 8 * tiles_n;
     tm = first + in % rows;
     tn = in / rows;
+    return true;
 }
 
 // LDS tiles: rows of 128 bytes in eight 16-byte chunks; chunk c of row r
@@ -254,9 +278,8 @@ __global__ __launch_bounds__(512, 2) void gemm_i8_block(Args p) {
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WN, wn = wave % WN;
     int tm, tn;
-    tile_of(p, tm, tn);
+    if (!tile_of(blockIdx.x, count_tiles<BM>(p), p.tiles_n, tm, tn)) return;
     const Tile tl = find_tile<BM>(p, tm);
-    if (tl.rows <= 0) return;
     const int n0 = tn * BN, cols = min(BN, p.N - n0);
     const size_t mat = (size_t)tl.e * p.N;
 
