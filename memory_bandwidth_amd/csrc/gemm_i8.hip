@@ -153,32 +153,32 @@ __device__ __forceinline__ Tile find_tile(const Args &p, int t) {
 // Scales a wavefront's sums and writes them.  acc[i][..]: rows row0 + 16 i +
 // lane % 16 of the tile; over its fragments a lane holds the C columns from n
 // on (with SWI: C of gate in the first half of the fragments, C of up in the
-// second).
+// second).  sa, sw0, sw1: the scales of the tile's rows and of the lane's
+// columns (sw1: of up), anything past N.
 template <int FM, int C, bool SWI>
 __device__ __forceinline__ void finish(const Args &p, const i32x4_t (&acc)[FM][SWI ? C / 2 : C / 4], const Tile &tl,
-                                       size_t mat, int row0, int n, int lane) {
-    float sw[SWI ? 2 : 1][C], bias[C];
+                                       const float *sa, const float *sw0, const float *sw1, int row0, int n, int lane) {
+    float w[SWI ? 2 : 1][C], bias[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-        const bool in = n + c < p.N;
-        sw[0][c] = in ? p.sw[0][mat + n + c] : 0.f;
-        if constexpr (SWI) sw[SWI][c] = in ? p.sw[1][mat + n + c] : 0.f;
-        bias[c] = !SWI && p.bias && in ? p.bias[n + c] : 0.f;
+        w[0][c] = sw0[c];
+        if constexpr (SWI) w[SWI][c] = sw1[c];
+        bias[c] = !SWI && p.bias && n + c < p.N ? p.bias[n + c] : 0.f;
     }
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
         const int r = row0 + i * 16 + (lane & 15);
         if (r >= tl.rows) continue;
-        const float sa = p.sa[tl.m0 + r];
+        const float s = sa[r];
         float v[C];
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             if constexpr (SWI) {
-                const float g = (float)acc[i][c >> 2][c & 3] * sa * sw[0][c];
-                const float u = (float)acc[i][(C + c) >> 2][c & 3] * sa * sw[SWI][c];
+                const float g = (float)acc[i][c >> 2][c & 3] * s * w[0][c];
+                const float u = (float)acc[i][(C + c) >> 2][c & 3] * s * w[SWI][c];
                 v[c] = silu(g) * u;
             } else {
-                v[c] = (float)acc[i][c >> 2][c & 3] * sa * sw[0][c] + bias[c];
+                v[c] = (float)acc[i][c >> 2][c & 3] * s * w[0][c] + bias[c];
             }
         }
         store_run<C>(p, tl.m0 + r, n, v);
@@ -229,13 +229,18 @@ __device__ __forceinline__ int slot(int r, int c) { return r * BK + ((c ^ (r & 7
 // their results are not stored.
 typedef __attribute__((address_space(3))) void *lds_ptr_t;
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const int8_t *base, uint32_t bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t *>(base), 0, (int)bytes, 0x00020000);
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void *base, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, (int)bytes, 0x00020000);
 }
 
 // 16 bytes a lane from memory to LDS, lane l's at `to` + 16 l.
 __device__ __forceinline__ void load16(__amdgpu_buffer_rsrc_t r, char *to, uint32_t voff, int soff) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t)to, 16, voff, soff, 0, 0);
+}
+
+// 4 bytes a lane, lane l's at `to` + l.
+__device__ __forceinline__ void load4(__amdgpu_buffer_rsrc_t r, float *to, uint32_t voff) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t)to, 4, voff, 0, 0, 0);
 }
 
 template <int N>
@@ -346,6 +351,15 @@ __global__ __launch_bounds__(512, 2) void gemm_i8_block(Args p) {
         __builtin_amdgcn_sched_barrier(0);
     };
 
+    // The scales of the tile's rows and columns go behind the ring, 64 of them
+    // a wavefront: fetched at the end, they would cost a trip to memory there.
+    float *sa = reinterpret_cast<float *>(lds + D * STAGE), *sw0 = sa + BM, *sw1 = SWI ? sw0 + BN : sw0;
+    if (wave * 64 < BM + BW) {
+        const int at = wave * 64 - BM, col = (at & (BN - 1)) + lane;
+        const float *from = at < 0 ? p.sa + tl.m0 : (SWI && at >= BN ? p.sw[1] : p.sw[0]) + mat + n0;
+        const int i = at < 0 ? min(wave * 64 + lane, tl.rows - 1) : min(col, cols - 1);
+        load4(rsrc_of(from, (uint32_t)(at < 0 ? tl.rows : cols) * 4), sa + wave * 64, i * 4);
+    }
 #pragma unroll
     for (int d = 0; d < D; ++d)
         if (d < steps) load(d, koff(d));
@@ -391,7 +405,8 @@ __global__ __launch_bounds__(512, 2) void gemm_i8_block(Args p) {
     }
 
     constexpr int C = SWI ? 2 * FW : 4 * FW;      // consecutive columns of a lane
-    finish<FM, C, SWI>(p, acc, tl, mat, wm * (16 * FM), n0 + wn * (4 * C) + (lane >> 4) * C, lane);
+    const int col = wn * (4 * C) + (lane >> 4) * C;
+    finish<FM, C, SWI>(p, acc, tl, sa, sw0 + col, sw1 + col, wm * (16 * FM), n0 + col, lane);
 }
 
 // ---------------------------------------------------------------- few rows
@@ -511,7 +526,14 @@ __global__ __launch_bounds__(W * 64) void gemm_i8_few(Args p, int ks_log2) {
 #pragma unroll
                 for (int j = 0; j < FW; ++j) acc[i][j] += part[((wave + k) * FM * FW + i * FW + j) * 64];
     }
-    finish<FM, 4 * FN, SWI>(p, acc, tl, mat, 0, n0 + g * (4 * FN), lane);
+    constexpr int C = 4 * FN;
+    const int n = n0 + g * C;
+    float sw[MATS][C];
+#pragma unroll
+    for (int s = 0; s < MATS; ++s)
+#pragma unroll
+        for (int c = 0; c < C; ++c) sw[s][c] = n + c < p.N ? p.sw[s][mat + n + c] : 0.f;
+    finish<FM, C, SWI>(p, acc, tl, p.sa + tl.m0, sw[0], sw[MATS - 1], 0, n, lane);
 }
 
 constexpr int kMaxRows = 1 << 24;
@@ -552,7 +574,7 @@ int launch_block(Args p, hipStream_t stream) {
     p.tiles_n = (int)tiles_of(p.N, SWI ? BW / 2 : BW);
     const int64_t grid = (int64_t)p.tiles_m * p.tiles_n;
     if (grid * 512 > kMaxThreads) return Q4_EINVAL;
-    gemm_i8_block<BM, BW, 2, 4, D, SWI><<<(unsigned)grid, 512, D * (BM + BW) * BK, stream>>>(p);
+    gemm_i8_block<BM, BW, 2, 4, D, SWI><<<(unsigned)grid, 512, D * (BM + BW) * BK + (BM + BW) * 4, stream>>>(p);
     return q4::launch_status();
 }
 
