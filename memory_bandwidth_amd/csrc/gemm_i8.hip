@@ -223,7 +223,9 @@ __device__ __forceinline__ int slot(int r, int c) { return r * BK + ((c ^ (r & 7
 //                   products of (t, second half)
 //
 // so there is one barrier a step, and a step's loads have D - 1 steps to
-// arrive.  A last step that K does not fill is taken as the last 128 bytes
+// arrive.  The last D steps of a tile load the first D of the workgroup's
+// next tile (one gridDim.x further), which arrive while this one is scaled and
+// stored.  A last step that K does not fill is taken as the last 128 bytes
 // of the rows, with the activations already used set to zero; every address
 // stays inside the rows.  Rows past the tile's end repeat its last row, and
 // their results are not stored.
@@ -282,31 +284,43 @@ __global__ __launch_bounds__(512, 2) void gemm_i8_block(Args p) {
     extern __shared__ __align__(16) char lds[];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WN, wn = wave % WN;
-    int tm, tn;
-    if (!tile_of(blockIdx.x, count_tiles<BM>(p), p.tiles_n, tm, tn)) return;
-    const Tile tl = find_tile<BM>(p, tm);
-    const int n0 = tn * BN, cols = min(BN, p.N - n0);
-    const size_t mat = (size_t)tl.e * p.N;
+    const int steps = (p.K + BK - 1) / BK;
+    const int tiles_m = count_tiles<BM>(p);
+    struct Place { Tile tl; int n0; };
+    auto place = [&](int id, Place &at) {
+        int tm, tn;
+        if (!tile_of(id, tiles_m, p.tiles_n, tm, tn)) return false;
+        at.tl = find_tile<BM>(p, tm);
+        at.n0 = tn * BN;
+        return true;
+    };
+    int id = blockIdx.x;
+    Place cur;
+    if (!place(id, cur)) return;
 
     // Loads: this wavefront brings an eighth of the rows of a and of w.
-    const __amdgpu_buffer_rsrc_t ra = rsrc_of(p.a + (size_t)tl.m0 * p.K, (uint32_t)tl.rows * p.K);
-    // SWI: the weight rows that one wavefront loads are all gate or all up.
+    // SWI: its weight rows are all gate or all up.
     const int8_t *wbase = SWI && wave * LW / 2 % FW >= FW / 2 ? p.w[1] : p.w[0];
-    const __amdgpu_buffer_rsrc_t rw = rsrc_of(wbase + (mat + n0) * p.K, (uint32_t)cols * p.K);
+    __amdgpu_buffer_rsrc_t ra, rw;
     uint32_t va[LX], vw[LW];
-    const int chunk = ((lane & 7) ^ (lane >> 3)) << 4;
+    auto aim = [&](const Place &at) {
+        const int rows = at.tl.rows, cols = min(BN, p.N - at.n0), chunk = ((lane & 7) ^ (lane >> 3)) << 4;
+        ra = rsrc_of(p.a + (size_t)at.tl.m0 * p.K, (uint32_t)rows * p.K);
+        rw = rsrc_of(wbase + ((size_t)at.tl.e * p.N + at.n0) * p.K, (uint32_t)cols * p.K);
 #pragma unroll
-    for (int i = 0; i < LX; ++i)
-        va[i] = (uint32_t)min((wave * LX + i) * 8 + (lane >> 3), tl.rows - 1) * p.K + chunk;
+        for (int i = 0; i < LX; ++i)
+            va[i] = (uint32_t)min((wave * LX + i) * 8 + (lane >> 3), rows - 1) * p.K + chunk;
 #pragma unroll
-    for (int i = 0; i < LW; ++i) {
-        // Row r belongs to wavefront column c, its fragment j, row q of it.
-        const int r = (wave * LW + i) * 8 + (lane >> 3), c = r / (16 * FW), j = r / 16 % FW, q = r & 15;
-        const int n = SWI ? c * (8 * FW) + frag_row<FW / 2>(j % (FW / 2), q) : c * (16 * FW) + frag_row<FW>(j, q);
-        vw[i] = (uint32_t)min(n, cols - 1) * p.K + chunk;
-    }
-    auto load = [&](int slot, int koff) {
+        for (int i = 0; i < LW; ++i) {
+            // Row r belongs to wavefront column c, its fragment j, row q of it.
+            const int r = (wave * LW + i) * 8 + (lane >> 3), c = r / (16 * FW), j = r / 16 % FW, q = r & 15;
+            const int n = SWI ? c * (8 * FW) + frag_row<FW / 2>(j % (FW / 2), q) : c * (16 * FW) + frag_row<FW>(j, q);
+            vw[i] = (uint32_t)min(n, cols - 1) * p.K + chunk;
+        }
+    };
+    auto load = [&](int slot, int t) {
         char *at = lds + slot * STAGE + wave * 1024;
+        const int koff = min(t * BK, p.K - BK);
 #pragma unroll
         for (int i = 0; i < LX; ++i) load16(ra, at + (wave * (LX - 1) + i) * 1024, va[i], koff);
 #pragma unroll
@@ -317,7 +331,7 @@ __global__ __launch_bounds__(512, 2) void gemm_i8_block(Args p) {
     // second half, which flips bit 6 of the swizzled address).
     const int fr = (lane & 15) * BK + (((lane >> 4) ^ (lane & 7)) << 4);
     const int xat = wm * (16 * FM) * BK, wat = (BM + wn * (16 * FW)) * BK;
-    i32x4_t acc[FM][FW] = {};
+    i32x4_t acc[FM][FW];
     i32x4_t x0[FM], w0[FW], x1[FM], w1[FW];
     auto read = [&](i32x4_t (&x)[FM], i32x4_t (&w)[FW], int slot, int f) {
         const char *at = lds + slot * STAGE + f;
@@ -326,6 +340,9 @@ __global__ __launch_bounds__(512, 2) void gemm_i8_block(Args p) {
 #pragma unroll
         for (int i = 0; i < FM; ++i) x[i] = *reinterpret_cast<const i32x4_t *>(at + xat + i * 16 * BK);
     };
+    // Neighbours share an operand, and rows run back and forth so that the
+    // turns do too: the matrix cores are bound by power at large sizes, and
+    // this order draws 1% less than one that returns to column 0.
     auto products = [&](const i32x4_t (&x)[FM], const i32x4_t (&w)[FW]) {
 #pragma unroll
         for (int i = 0; i < FM; ++i)
@@ -335,8 +352,6 @@ __global__ __launch_bounds__(512, 2) void gemm_i8_block(Args p) {
                 acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[j], x[i], acc[i][j], 0, 0, 0);
             }
     };
-    const int steps = (p.K + BK - 1) / BK;
-    auto koff = [&](int t) { return min(t * BK, p.K - BK); };
     // Chunks of the last step that earlier steps have used.
     const int used = steps * 8 - (p.K >> 4);
     auto drop = [&](i32x4_t (&x)[FM], int c) {
@@ -350,63 +365,86 @@ __global__ __launch_bounds__(512, 2) void gemm_i8_block(Args p) {
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
     };
+    // The scales of a tile's rows and columns go behind the ring, 64 of them a
+    // wavefront: fetched at the end, they would cost a trip to memory there.
+    float *scales = reinterpret_cast<float *>(lds + D * STAGE);
+    auto load_scales = [&](const Place &at, float *to) {
+        if (wave * 64 < BM + BW) {
+            const int q = wave * 64 - BM, rows = at.tl.rows, cols = min(BN, p.N - at.n0);
+            const float *from = q < 0 ? p.sa + at.tl.m0
+                                      : (SWI && q >= BN ? p.sw[1] : p.sw[0]) + (size_t)at.tl.e * p.N + at.n0;
+            const int i = q < 0 ? min(wave * 64 + lane, rows - 1) : min((q & (BN - 1)) + lane, cols - 1);
+            load4(rsrc_of(from, (uint32_t)(q < 0 ? rows : cols) * 4), to + wave * 64, i * 4);
+        }
+    };
+    auto after = [](int slot) { return slot + 1 == D ? 0 : slot + 1; };
 
-    // The scales of the tile's rows and columns go behind the ring, 64 of them
-    // a wavefront: fetched at the end, they would cost a trip to memory there.
-    float *sa = reinterpret_cast<float *>(lds + D * STAGE), *sw0 = sa + BM, *sw1 = SWI ? sw0 + BN : sw0;
-    if (wave * 64 < BM + BW) {
-        const int at = wave * 64 - BM, col = (at & (BN - 1)) + lane;
-        const float *from = at < 0 ? p.sa + tl.m0 : (SWI && at >= BN ? p.sw[1] : p.sw[0]) + mat + n0;
-        const int i = at < 0 ? min(wave * 64 + lane, tl.rows - 1) : min(col, cols - 1);
-        load4(rsrc_of(from, (uint32_t)(at < 0 ? tl.rows : cols) * 4), sa + wave * 64, i * 4);
-    }
+    aim(cur);
+    int side = 0;                // of the two places for scales
+    load_scales(cur, scales);
 #pragma unroll
     for (int d = 0; d < D; ++d)
-        if (d < steps) load(d, koff(d));
+        if (d < steps) load(d, d);
     wait_batches<LOADS, D - 1>(steps - 1);
     barrier();
-    read(x0, w0, 0, fr);
-    if (steps == 1 && used) drop(x0, lane >> 4);
-    int t = 0;
-    auto whole = [&](int slot, int next) {          // a step with D full ones behind it
-        read(x1, w1, slot, fr ^ 64);
-        products(x0, w0);
-        interleave<0, FM + FW, FM * FW>();
-        __builtin_amdgcn_sched_barrier(0);
-        wait_loads<(D - 2) * LOADS>();
-        barrier();
-        load(slot, (t + D) * BK);
-        read(x0, w0, next, fr);
-        products(x1, w1);
-        interleave<LOADS, FM + FW, FM * FW>();
-        __builtin_amdgcn_sched_barrier(0);
-        ++t;
-    };
-    while (t + 2 * D < steps) {
+    for (int slot = 0;;) {
+        read(x0, w0, slot, fr);
+        if (steps == 1 && used) drop(x0, lane >> 4);
 #pragma unroll
-        for (int d = 0; d < D; ++d) whole(d, (d + 1) % D);
-    }
-    for (int slot = 0; t < steps; ++t) {
-        const int next = slot + 1 == D ? 0 : slot + 1;
-        read(x1, w1, slot, fr ^ 64);
-        if (t + 1 == steps && used) drop(x1, 4 + (lane >> 4));
-        products(x0, w0);
-        __builtin_amdgcn_sched_barrier(0);
-        wait_batches<LOADS, D - 2>(steps - t - 2);       // step t + 1 has come
-        barrier();
-        if (t + D < steps) load(slot, koff(t + D));
-        if (t + 1 < steps) {
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FW; ++j) acc[i][j] = i32x4_t{0, 0, 0, 0};
+        int t = 0;
+        for (; t + D < steps; ++t) {
+            read(x1, w1, slot, fr ^ 64);
+            products(x0, w0);
+            interleave<0, FM + FW, FM * FW>();
+            __builtin_amdgcn_sched_barrier(0);
+            wait_loads<(D - 2) * LOADS>();
+            barrier();
+            const int next = after(slot);
+            load(slot, t + D);
             read(x0, w0, next, fr);
-            if (t + 2 == steps && used) drop(x0, lane >> 4);
+            products(x1, w1);
+            interleave<LOADS, FM + FW, FM * FW>();
+            __builtin_amdgcn_sched_barrier(0);
+            slot = next;
         }
-        products(x1, w1);
-        __builtin_amdgcn_sched_barrier(0);
-        slot = next;
+        // The last D steps load the next tile's first.
+        Place nxt = cur;
+        const bool more = steps >= D && place(id + (int)gridDim.x, nxt);
+        if (more) aim(nxt);
+        for (; t < steps; ++t) {
+            const int next = after(slot);
+            read(x1, w1, slot, fr ^ 64);
+            if (t + 1 == steps && used) drop(x1, 4 + (lane >> 4));
+            products(x0, w0);
+            __builtin_amdgcn_sched_barrier(0);
+            // Step t + 1, or the next tile's first, has come.
+            if (more) wait_loads<(D - 2) * LOADS>();
+            else wait_batches<LOADS, D - 2>(steps - t - 2);
+            barrier();
+            if (more) {
+                if (t + D == steps) load_scales(nxt, scales + (side ^ 1) * (BM + BW));
+                load(slot, t + D - steps);
+            }
+            if (t + 1 < steps) {
+                read(x0, w0, next, fr);
+                if (t + 2 == steps && used) drop(x0, lane >> 4);
+            }
+            products(x1, w1);
+            __builtin_amdgcn_sched_barrier(0);
+            slot = next;
+        }
+        constexpr int C = SWI ? 2 * FW : 4 * FW;      // consecutive columns of a lane
+        const int col = wn * (4 * C) + (lane >> 4) * C;
+        const float *sa = scales + side * (BM + BW), *sw0 = sa + BM + col, *sw1 = SWI ? sw0 + BN : sw0;
+        finish<FM, C, SWI>(p, acc, cur.tl, sa, sw0, sw1, wm * (16 * FM), cur.n0 + col, lane);
+        if (!more) return;
+        id += gridDim.x;
+        cur = nxt;
+        side ^= 1;
     }
-
-    constexpr int C = SWI ? 2 * FW : 4 * FW;      // consecutive columns of a lane
-    const int col = wn * (4 * C) + (lane >> 4) * C;
-    finish<FM, C, SWI>(p, acc, tl, sa, sw0 + col, sw1 + col, wm * (16 * FM), n0 + col, lane);
 }
 
 // ---------------------------------------------------------------- few rows
@@ -542,6 +580,7 @@ constexpr int kMaxK = 131056;      // 16384 * 131056 < 2^31: the sum fits whatev
 bool elem_aligned(const void *y, int type) { return q4::aligned(y, type == I8_F32 ? 4 : 2); }
 
 constexpr int64_t kMaxThreads = 0xFFFFFFFFll;      // of one launch
+constexpr int kCUs = 256;
 
 int64_t tiles_of(int64_t n, int tile) { return (n + tile - 1) / tile; }
 
@@ -572,40 +611,55 @@ template <int BM, int BW, int D, bool SWI>
 int launch_block(Args p, hipStream_t stream) {
     p.tiles_m = (int)row_tiles(p, BM);
     p.tiles_n = (int)tiles_of(p.N, SWI ? BW / 2 : BW);
-    const int64_t grid = (int64_t)p.tiles_m * p.tiles_n;
-    if (grid * 512 > kMaxThreads) return Q4_EINVAL;
-    gemm_i8_block<BM, BW, 2, 4, D, SWI><<<(unsigned)grid, 512, D * (BM + BW) * BK + (BM + BW) * 4, stream>>>(p);
+    constexpr int kLds = D * (BM + BW) * BK + 2 * (BM + BW) * 4;
+    int64_t grid = (int64_t)p.tiles_m * p.tiles_n;
+    if (grid > 0x7FFFFFFFll) return Q4_EINVAL;
+    // Workgroups that stay and go through the tiles, each loading its next one
+    // while it finishes the last: 8192 x 14336 x 4096 takes 393 us so, 400
+    // with a workgroup for each tile; 8000 rows over 64 experts with SwiGLU,
+    // K = 1024, 113 against 125.  At K = 14336 tiles change rarely, and dealing
+    // them as CUs come free is better: 527 against 539 us (8190 rows, 8 experts).
+    const int64_t steps = tiles_of(p.K, BK);
+    if (steps >= D && steps <= 64) grid = std::min<int64_t>(grid, kCUs * (160 * 1024 / kLds));
+    else if (grid * 512 > kMaxThreads) return Q4_EINVAL;
+    gemm_i8_block<BM, BW, 2, 4, D, SWI><<<(unsigned)grid, 512, kLds, stream>>>(p);
     return q4::launch_status();
 }
 
-enum Kernel { kFew8, kFew16, kFew32, kFew64, kTile64, kTile128, kTile256 };
+enum Kernel { kFew8, kFew16, kFew32, kFew64, kTile64, kTile128, kTileWide, kTile256, kKernels };
 
 // The kernel for a call's sizes.  Up to 32 rows the weights' stream decides.
 // Above that, each kernel's time is estimated from its tiles and steps, with
-// constants fitted to 370 measured shapes (33 to 8192 rows, N 64 to 14336, K
-// 256 to 14336; the choice is on average 0.7% behind the best of the five
-// measured): fixed us a tile, us a step, and how far more tiles than CUs
-// stretch it.  The 256-row tile has a CU to itself, so its rounds are whole.
+// constants fitted to 260 measured shapes (33 to 8192 rows, N 64 to 14336, K
+// 256 to 14336, one matrix and two; the choice is on average 0.6% behind the
+// best of the five measured, at most 18%): us a tile, us a step, and how far
+// more tiles than CUs stretch it.  Tiles that have a CU to themselves come in
+// whole rounds.
 // Groups go by their average rows, their sizes being known to the GPU alone.
+// Measured over 64 experts of 2 x 2816 x 1024, at 4, 32 and 128 rows each: 16
+// rows a tile 73, 133, - us, 64 rows 69, 82, 133, 128 rows 72, 90, 115, 256
+// rows 103, 119, 145.
 Kernel choose(const Args &p, int mats) {
     const int64_t steps = tiles_of(p.K, BK);
     if (p.offsets) {
         const int64_t rows = tiles_of(p.M, p.E);
-        if (p.K < BK) return rows <= 2 ? kFew8 : rows <= 6 ? kFew16 : kFew64;
-        return rows <= 2 ? kFew8 : rows <= 6 ? kFew16 : rows <= 96 ? kTile64 : rows <= 192 ? kTile128 : kTile256;
+        if (rows <= 4) return rows <= 2 ? kFew8 : kFew16;
+        return p.K < BK ? kFew64 : rows <= 48 ? kTile64 : kTileWide;
     }
     if (p.M <= 32) return p.M <= 8 ? kFew8 : p.M <= 16 ? kFew16 : kFew32;
     if (p.K < BK) return kFew64;
     auto tiles = [&](int bm, int bw) { return tiles_of(p.M, bm) * tiles_of(p.N, bw / mats); };
-    const double few = tiles(64, 32), t64 = tiles(64, 128), t128 = tiles(128, 128), t256 = tiles(256, 256);
+    auto rounds = [&](int bm, int bw) { return (double)((tiles(bm, bw) + kCUs - 1) / kCUs); };
+    const double few = tiles(64, 32), t64 = tiles(64, 128), t128 = tiles(128, 128);
     const int ks = few < 384 ? 4 : few < 768 ? 2 : 1;            // as launch_few's rule
-    double cost[7];
-    cost[kFew64] = std::max(1.0, few * ks / 1024 * 1.65) * (1.3 + (double)tiles_of(steps, ks) * 0.88);
-    cost[kTile64] = std::max(1.0, t64 / 256 * 1.38) * (0.7 + steps * 0.40);
-    cost[kTile128] = t128 <= 256 ? 2.9 + steps * 0.54 : t128 / 256 * 0.92 * (0.95 + steps * 0.72);
-    cost[kTile256] = (double)tiles_of((int64_t)t256, 256) * (7.0 + steps * 1.3);
+    double cost[kKernels];
+    cost[kFew64] = std::max(1.0, few * ks / (4 * kCUs) * 1.55) * (1.27 + (double)tiles_of(steps, ks) * 0.82);
+    cost[kTile64] = std::max(1.0, t64 / kCUs * 1.52) * (0.77 + steps * 0.42);
+    cost[kTile128] = t128 <= kCUs ? 2.2 + steps * 0.63 : t128 / kCUs * 0.89 * (0.69 + steps * 0.88);
+    cost[kTileWide] = rounds(128, 256) * (6.0 + steps * 0.68);
+    cost[kTile256] = rounds(256, 256) * (10.28 + steps * 1.32);
     Kernel best = kFew64;
-    for (Kernel k : {kTile64, kTile128, kTile256})
+    for (Kernel k : {kTile64, kTile128, kTileWide, kTile256})
         if (cost[k] < cost[best]) best = k;
     return best;
 }
@@ -622,8 +676,9 @@ int launch(const Args &p, Kernel k, hipStream_t stream) {
         // Two workgroups share a CU with a ring of two stages; where there is
         // only one for each CU, it takes four: 1024 x 4096 x 4096 in 19.0
         // against 24.1 us, but 1999 x 14336 x 4096 in 128 against 112.
-        if (row_tiles(p, 128) * tiles_of(p.N, SWI ? 64 : 128) <= 256) return launch_block<128, 128, 4, SWI>(p, stream);
+        if (row_tiles(p, 128) * tiles_of(p.N, SWI ? 64 : 128) <= kCUs) return launch_block<128, 128, 4, SWI>(p, stream);
         return launch_block<128, 128, 2, SWI>(p, stream);
+    case kTileWide: return launch_block<128, 256, 3, SWI>(p, stream);
     default: return launch_block<256, 256, 2, SWI>(p, stream);
     }
 }
