@@ -211,8 +211,9 @@ __device__ __forceinline__ int slot(int r, int c) { return r * BK + ((c ^ (r & 7
 // ---------------------------------------------------------------- tiles
 //
 // A tile of BM rows and BW weight rows (with SWI: BW / 2 of each matrix) by
-// eight wavefronts, WM x WN of them.  Steps of 128 bytes of K pass through a
-// ring of D stages in LDS, loaded straight from memory (buffer loads to LDS,
+// WM x WN wavefronts, or by G groups of as many that share out K: group g
+// takes every G-th slice of 128 bytes, and the groups' sums meet in LDS at the
+// end.  Steps of G slices pass through a ring of D stages in LDS, loaded straight from memory (buffer loads to LDS,
 // 1 KiB an instruction: eight rows of 128 bytes, the lanes' chunk order
 // making the swizzle).  A step has two halves of 64 bytes; the fragments of
 // each half are read into registers while the other half's products run:
@@ -240,9 +241,10 @@ __device__ __forceinline__ void load16(__amdgpu_buffer_rsrc_t r, char *to, uint3
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t)to, 16, voff, soff, 0, 0);
 }
 
-// 4 bytes a lane, lane l's at `to` + l.
-__device__ __forceinline__ void load4(__amdgpu_buffer_rsrc_t r, float *to, uint32_t voff) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t)to, 4, voff, 0, 0, 0);
+// 4 bytes a lane from an address of its own, lane l's at `to` + l.
+__device__ __forceinline__ void load4(const float *from, float *to) {
+    __builtin_amdgcn_global_load_lds((__attribute__((address_space(1))) void *)const_cast<float *>(from), (lds_ptr_t)to,
+                                     4, 0, 0);
 }
 
 template <int N>
@@ -275,16 +277,17 @@ __device__ __forceinline__ void interleave() {
     }
 }
 
-template <int BM, int BW, int WM, int WN, int D, bool SWI>
-__global__ __launch_bounds__(512, 2) void gemm_i8_block(Args p) {
-    static_assert(WM * WN == 8, "eight wavefronts");
+template <int BM, int BW, int WM, int WN, int G, int D, bool SWI>
+__global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_i8_block(Args p) {
     constexpr int FM = BM / WM / 16, FW = BW / WN / 16, BN = SWI ? BW / 2 : BW;
-    constexpr int LX = BM / 64, LW = BW / 64, LOADS = LX + LW;       // load instructions of a wavefront and step
-    constexpr int STAGE = (BM + BW) * BK;
+    constexpr int W = WM * WN;                                      // wavefronts of a group
+    constexpr int LX = BM / 8 / W, LW = BW / 8 / W, LOADS = LX + LW; // load instructions of one of them and step
+    constexpr int SLICE = (BM + BW) * BK, STAGE = G * SLICE;
     extern __shared__ __align__(16) char lds[];
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int tid = threadIdx.x, lane = tid & 63, all_waves = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wave = all_waves % W, group = all_waves / W;
     const int wm = wave / WN, wn = wave % WN;
-    const int steps = (p.K + BK - 1) / BK;
+    const int steps = (p.K + G * BK - 1) / (G * BK);
     const int tiles_m = count_tiles<BM>(p);
     struct Place { Tile tl; int n0; };
     auto place = [&](int id, Place &at) {
@@ -319,8 +322,8 @@ __global__ __launch_bounds__(512, 2) void gemm_i8_block(Args p) {
         }
     };
     auto load = [&](int slot, int t) {
-        char *at = lds + slot * STAGE + wave * 1024;
-        const int koff = min(t * BK, p.K - BK);
+        char *at = lds + slot * STAGE + group * SLICE + wave * 1024;
+        const int koff = min((t * G + group) * BK, p.K - BK);
 #pragma unroll
         for (int i = 0; i < LX; ++i) load16(ra, at + (wave * (LX - 1) + i) * 1024, va[i], koff);
 #pragma unroll
@@ -334,7 +337,7 @@ __global__ __launch_bounds__(512, 2) void gemm_i8_block(Args p) {
     i32x4_t acc[FM][FW];
     i32x4_t x0[FM], w0[FW], x1[FM], w1[FW];
     auto read = [&](i32x4_t (&x)[FM], i32x4_t (&w)[FW], int slot, int f) {
-        const char *at = lds + slot * STAGE + f;
+        const char *at = lds + slot * STAGE + group * SLICE + f;
 #pragma unroll
         for (int j = 0; j < FW; ++j) w[j] = *reinterpret_cast<const i32x4_t *>(at + wat + j * 16 * BK);
 #pragma unroll
@@ -352,8 +355,8 @@ __global__ __launch_bounds__(512, 2) void gemm_i8_block(Args p) {
                 acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[j], x[i], acc[i][j], 0, 0, 0);
             }
     };
-    // Chunks of the last step that earlier steps have used.
-    const int used = steps * 8 - (p.K >> 4);
+    // Chunks of this group's last slice that others have used.
+    const int used = max(0, ((steps - 1) * G + group + 1) * 8 - (p.K >> 4));
     auto drop = [&](i32x4_t (&x)[FM], int c) {
         if (c < used) {
 #pragma unroll
@@ -369,12 +372,11 @@ __global__ __launch_bounds__(512, 2) void gemm_i8_block(Args p) {
     // wavefront: fetched at the end, they would cost a trip to memory there.
     float *scales = reinterpret_cast<float *>(lds + D * STAGE);
     auto load_scales = [&](const Place &at, float *to) {
-        if (wave * 64 < BM + BW) {
-            const int q = wave * 64 - BM, rows = at.tl.rows, cols = min(BN, p.N - at.n0);
-            const float *from = q < 0 ? p.sa + at.tl.m0
-                                      : (SWI && q >= BN ? p.sw[1] : p.sw[0]) + (size_t)at.tl.e * p.N + at.n0;
-            const int i = q < 0 ? min(wave * 64 + lane, rows - 1) : min((q & (BN - 1)) + lane, cols - 1);
-            load4(rsrc_of(from, (uint32_t)(q < 0 ? rows : cols) * 4), to + wave * 64, i * 4);
+        for (int q = all_waves * 64; q < BM + BW; q += W * G * 64) {
+            const int i = q + lane - BM, col = at.n0 + (i & (BN - 1));
+            const float *from = i < 0 ? p.sa + at.tl.m0 + min(q + lane, at.tl.rows - 1)
+                                      : (SWI && i >= BN ? p.sw[1] : p.sw[0]) + (size_t)at.tl.e * p.N + min(col, p.N - 1);
+            load4(from, to + q);
         }
     };
     auto after = [](int slot) { return slot + 1 == D ? 0 : slot + 1; };
@@ -412,7 +414,7 @@ __global__ __launch_bounds__(512, 2) void gemm_i8_block(Args p) {
         }
         // The last D steps load the next tile's first.
         Place nxt = cur;
-        const bool more = steps >= D && place(id + (int)gridDim.x, nxt);
+        const bool more = G == 1 && steps >= D && place(id + (int)gridDim.x, nxt);
         if (more) aim(nxt);
         for (; t < steps; ++t) {
             const int next = after(slot);
@@ -439,7 +441,29 @@ __global__ __launch_bounds__(512, 2) void gemm_i8_block(Args p) {
         constexpr int C = SWI ? 2 * FW : 4 * FW;      // consecutive columns of a lane
         const int col = wn * (4 * C) + (lane >> 4) * C;
         const float *sa = scales + side * (BM + BW), *sw0 = sa + BM + col, *sw1 = SWI ? sw0 + BN : sw0;
-        finish<FM, C, SWI>(p, acc, cur.tl, sa, sw0, sw1, wm * (16 * FM), cur.n0 + col, lane);
+        if constexpr (G == 1) {
+            finish<FM, C, SWI>(p, acc, cur.tl, sa, sw0, sw1, wm * (16 * FM), cur.n0 + col, lane);
+        } else {
+            // The groups' sums meet in the ring's place, and group g finishes
+            // rows g, g + G, .. of the fragments.
+            static_assert(G * W * FM * FW * 1024 <= D * STAGE, "the sums fit the ring");
+            __syncthreads();
+            i32x4_t *part = reinterpret_cast<i32x4_t *>(lds) + wave * (FM * FW * 64) + lane;
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int j = 0; j < FW; ++j) part[(group * W * FM * FW + i * FW + j) * 64] = acc[i][j];
+            __syncthreads();
+            for (int i = group; i < FM; i += G) {
+                i32x4_t sum[1][FW] = {};
+#pragma unroll
+                for (int g = 0; g < G; ++g)
+#pragma unroll
+                    for (int j = 0; j < FW; ++j) sum[0][j] += part[(g * W * FM * FW + i * FW + j) * 64];
+                finish<1, C, SWI>(p, sum, cur.tl, sa, sw0, sw1, wm * (16 * FM) + i * 16, cur.n0 + col, lane);
+            }
+            return;
+        }
         if (!more) return;
         id += gridDim.x;
         cur = nxt;
@@ -607,11 +631,11 @@ int launch_few(Args p, hipStream_t stream) {
     return q4::launch_status();
 }
 
-template <int BM, int BW, int D, bool SWI>
+template <int BM, int BW, int WM, int WN, int G, int D, bool SWI>
 int launch_block(Args p, hipStream_t stream) {
     p.tiles_m = (int)row_tiles(p, BM);
     p.tiles_n = (int)tiles_of(p.N, SWI ? BW / 2 : BW);
-    constexpr int kLds = D * (BM + BW) * BK + 2 * (BM + BW) * 4;
+    constexpr int kLds = G * D * (BM + BW) * BK + 2 * (BM + BW) * 4, kThreads = WM * WN * G * 64;
     int64_t grid = (int64_t)p.tiles_m * p.tiles_n;
     if (grid > 0x7FFFFFFFll) return Q4_EINVAL;
     // Workgroups that stay and go through the tiles, each loading its next one
@@ -620,19 +644,19 @@ int launch_block(Args p, hipStream_t stream) {
     // K = 1024, 113 against 125.  At K = 14336 tiles change rarely, and dealing
     // them as CUs come free is better: 527 against 539 us (8190 rows, 8 experts).
     const int64_t steps = tiles_of(p.K, BK);
-    if (steps >= D && steps <= 64) grid = std::min<int64_t>(grid, kCUs * (160 * 1024 / kLds));
-    else if (grid * 512 > kMaxThreads) return Q4_EINVAL;
-    gemm_i8_block<BM, BW, 2, 4, D, SWI><<<(unsigned)grid, 512, kLds, stream>>>(p);
+    if (G == 1 && steps >= D && steps <= 64) grid = std::min<int64_t>(grid, kCUs * (160 * 1024 / kLds));
+    else if (grid * kThreads > kMaxThreads) return Q4_EINVAL;
+    gemm_i8_block<BM, BW, WM, WN, G, D, SWI><<<(unsigned)grid, kThreads, kLds, stream>>>(p);
     return q4::launch_status();
 }
 
-enum Kernel { kFew8, kFew16, kFew32, kFew64, kTile64, kTile128, kTileWide, kTile256, kKernels };
+enum Kernel { kFew8, kFew16, kFew32, kFew64, kTile64, kTile128, kTileWide, kTile256, kTileDeep, kKernels };
 
 // The kernel for a call's sizes.  Up to 32 rows the weights' stream decides.
 // Above that, each kernel's time is estimated from its tiles and steps, with
-// constants fitted to 260 measured shapes (33 to 8192 rows, N 64 to 14336, K
+// constants fitted to 320 measured shapes (33 to 8192 rows, N 64 to 14336, K
 // 256 to 14336, one matrix and two; the choice is on average 0.6% behind the
-// best of the five measured, at most 18%): us a tile, us a step, and how far
+// best of the six measured, at most 29%): us a tile, us a step, and how far
 // more tiles than CUs stretch it.  Tiles that have a CU to themselves come in
 // whole rounds.
 // Groups go by their average rows, their sizes being known to the GPU alone.
@@ -650,36 +674,43 @@ Kernel choose(const Args &p, int mats) {
     if (p.K < BK) return kFew64;
     auto tiles = [&](int bm, int bw) { return tiles_of(p.M, bm) * tiles_of(p.N, bw / mats); };
     auto rounds = [&](int bm, int bw) { return (double)((tiles(bm, bw) + kCUs - 1) / kCUs); };
-    const double few = tiles(64, 32), t64 = tiles(64, 128), t128 = tiles(128, 128);
+    // Tiles a CU, 1 where there are fewer, and the time of one alone or of one among others.
+    auto each = [&](int64_t t, double one, double many) { return t <= kCUs ? one : (double)t / kCUs * many; };
+    const double few = tiles(64, 32);
     const int ks = few < 384 ? 4 : few < 768 ? 2 : 1;            // as launch_few's rule
     double cost[kKernels];
-    cost[kFew64] = std::max(1.0, few * ks / (4 * kCUs) * 1.55) * (1.27 + (double)tiles_of(steps, ks) * 0.82);
-    cost[kTile64] = std::max(1.0, t64 / kCUs * 1.52) * (0.77 + steps * 0.42);
-    cost[kTile128] = t128 <= kCUs ? 2.2 + steps * 0.63 : t128 / kCUs * 0.89 * (0.69 + steps * 0.88);
-    cost[kTileWide] = rounds(128, 256) * (6.0 + steps * 0.68);
-    cost[kTile256] = rounds(256, 256) * (10.28 + steps * 1.32);
+    cost[kFew64] = std::max(1.0, few * ks / (4 * kCUs) * 1.49) * (1.85 + (double)tiles_of(steps, ks) * 0.93);
+    cost[kTileDeep] = each(tiles(64, 64), 0.67 + steps * 0.38, 0.78 + steps * 0.40);
+    cost[kTile64] = std::max(1.0, (double)tiles(64, 128) / kCUs * 1.2) * (0.67 + steps * 0.42);
+    cost[kTile128] = each(tiles(128, 128), 2.25 + steps * 0.46, 0.63 + steps * 0.78);
+    cost[kTileWide] = rounds(128, 256) * (6.54 + steps * 0.75);
+    cost[kTile256] = rounds(256, 256) * (8.0 + steps * 1.33);
     Kernel best = kFew64;
-    for (Kernel k : {kTile64, kTile128, kTileWide, kTile256})
+    for (Kernel k : {kTileDeep, kTile64, kTile128, kTileWide, kTile256})
         if (cost[k] < cost[best]) best = k;
     return best;
 }
 
 template <bool SWI>
 int launch(const Args &p, Kernel k, hipStream_t stream) {
+    // Two workgroups share a CU with a ring of two stages; where there is only
+    // one for each CU, it takes four: 1024 x 4096 x 4096 in 19.0 against 24.1
+    // us, but 1999 x 14336 x 4096 in 128 against 112 (tiles of 128 x 128).
+    auto alone = [&](int bm, int bw) { return row_tiles(p, bm) * tiles_of(p.N, SWI ? bw / 2 : bw) <= kCUs; };
     switch (k) {
     case kFew8: return launch_few<1, 1, SWI, 8>(p, stream);
     case kFew16: return launch_few<2, 1, SWI, 8>(p, stream);
     case kFew32: return launch_few<4, 1, SWI, 8>(p, stream);
     case kFew64: return launch_few<8, SWI ? 1 : 2, SWI, 4>(p, stream);
-    case kTile64: return launch_block<64, 128, 3, SWI>(p, stream);
+    case kTile64: return launch_block<64, 128, 2, 4, 1, 3, SWI>(p, stream);
+    case kTileDeep:
+        if (alone(64, 64)) return launch_block<64, 64, 2, 2, 2, 4, SWI>(p, stream);
+        return launch_block<64, 64, 2, 2, 2, 2, SWI>(p, stream);
     case kTile128:
-        // Two workgroups share a CU with a ring of two stages; where there is
-        // only one for each CU, it takes four: 1024 x 4096 x 4096 in 19.0
-        // against 24.1 us, but 1999 x 14336 x 4096 in 128 against 112.
-        if (row_tiles(p, 128) * tiles_of(p.N, SWI ? 64 : 128) <= kCUs) return launch_block<128, 128, 4, SWI>(p, stream);
-        return launch_block<128, 128, 2, SWI>(p, stream);
-    case kTileWide: return launch_block<128, 256, 3, SWI>(p, stream);
-    default: return launch_block<256, 256, 2, SWI>(p, stream);
+        if (alone(128, 128)) return launch_block<128, 128, 2, 4, 1, 4, SWI>(p, stream);
+        return launch_block<128, 128, 2, 4, 1, 2, SWI>(p, stream);
+    case kTileWide: return launch_block<128, 256, 2, 4, 1, 3, SWI>(p, stream);
+    default: return launch_block<256, 256, 2, 4, 1, 2, SWI>(p, stream);
     }
 }
 
