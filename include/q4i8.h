@@ -87,6 +87,19 @@ int gemm_i8_grouped_swiglu(const int8_t *a, const float *a_scales, const int8_t 
                            const int32_t *offsets, void *y, int y_type, int M, int E, int N, int K,
                            void *stream);
 
+/* Launch geometry of the products for a shape, for reporting and tests;
+ * host-only, launches nothing and needs no device.  Any output pointer may be
+ * NULL.  Q4_EINVAL for an invalid shape.
+ *   matrices    1, or 2 for the SwiGLU forms
+ *   E           groups, or 0 for a product without groups
+ *   tile_rows, tile_cols   rows and columns of y that a workgroup makes at a
+ *               time (a workgroup may go through several such tiles)
+ *   grid        workgroups launched (groups: at most that many have work)
+ *   block       threads per workgroup
+ * All are 0 where nothing is launched. */
+int gemm_i8_geometry(int matrices, int M, int E, int N, int K, int *tile_rows, int *tile_cols,
+                     int *grid, int *block);
+
 #ifdef __cplusplus
 }
 #endif

@@ -34,7 +34,8 @@ EXPORTS = ("gemv_q4", "gemv_q4_ws", "gemv_q4_workspace_size", "gemv_q4_static", 
            "gemv_block_config", "scan2", "scan2_set_config", "scan2_config")
 
 # Exported C symbols, in the order include/q4i8.h declares them.
-EXPORTS_I8 = ("quant_i8", "gemm_i8", "gemm_i8_swiglu", "gemm_i8_grouped", "gemm_i8_grouped_swiglu")
+EXPORTS_I8 = ("quant_i8", "gemm_i8", "gemm_i8_swiglu", "gemm_i8_grouped", "gemm_i8_grouped_swiglu",
+              "gemm_i8_geometry")
 
 # Element types of include/q4i8.h.
 I8_F32, I8_F16, I8_BF16 = 0, 1, 2
@@ -95,6 +96,7 @@ def lib() -> ctypes.CDLL:
     L.gemm_i8_swiglu.argtypes = [P, P, P, P, P, P, P, I, I, I, I, P]
     L.gemm_i8_grouped.argtypes = [P, P, P, P, P, P, I, I, I, I, I, P]
     L.gemm_i8_grouped_swiglu.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, I, P]
+    L.gemm_i8_geometry.argtypes = [I, I, I, I, I, IP, IP, IP, IP]
     for f in EXPORTS_I8:
         getattr(L, f).restype = ctypes.c_int
     L.q4_strerror.argtypes = [I]
@@ -633,3 +635,11 @@ def gemm_i8_grouped_swiglu(a: torch.Tensor, a_scales: torch.Tensor, gate: tuple,
     _i8_call("gemm_i8_grouped_swiglu", dev, a.data_ptr(), a_scales.data_ptr(), wg.data_ptr(), sg.data_ptr(),
              wu.data_ptr(), su.data_ptr(), offsets.data_ptr(), out.data_ptr(), t, M, E, N, K)
     return out
+
+
+def gemm_i8_geometry(matrices: int, M: int, N: int, K: int, groups: int = 0) -> dict:
+    """Launch geometry of the products for a shape (host-only, needs no GPU):
+    matrices is 2 for the SwiGLU forms, groups 0 for a product without groups."""
+    vals = [ctypes.c_int() for _ in range(4)]
+    _check("gemm_i8_geometry", lib().gemm_i8_geometry(matrices, M, groups, N, K, *[ctypes.byref(v) for v in vals]))
+    return dict(zip(("tile_rows", "tile_cols", "grid", "block"), (v.value for v in vals)))

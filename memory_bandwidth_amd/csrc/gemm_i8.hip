@@ -98,15 +98,6 @@ __device__ __forceinline__ void store_run(const Args &p, int m, int n, const flo
 // rows == 0: no such tile.
 struct Tile { int m0, rows, e; };
 
-// A group's rows (0 past the last group), and its tiles of BM rows.  Offsets
-// are held to 0 .. M.
-struct Group { int lo, hi; };
-__device__ __forceinline__ Group group_of(const Args &p, int e) {
-    if (e >= p.E) return {0, 0};
-    const int lo = min(max(p.offsets[e], 0), p.M);
-    return {lo, min(max(p.offsets[e + 1], lo), p.M)};
-}
-
 // Sums over the lanes up to and with each lane.
 __device__ __forceinline__ int scan_lanes(int v) {
     const int lane = threadIdx.x & 63;
@@ -118,36 +109,68 @@ __device__ __forceinline__ int scan_lanes(int v) {
     return v;
 }
 
-// The tiles of BM rows that all groups have.
-template <int BM>
-__device__ __forceinline__ int count_tiles(const Args &p) {
-    if (!p.offsets) return p.tiles_m;
-    int all = 0;
-    for (int e0 = 0; e0 < p.E; e0 += 64) {
-        const Group g = group_of(p, e0 + (threadIdx.x & 63));
-        all += __builtin_amdgcn_readlane(scan_lanes((g.hi - g.lo + BM - 1) / BM), 63);
-    }
-    return all;
+// The rows of group e, none past the last group.  Offsets are held to 0 .. M
+// and to their order, so that whatever they are, rows stay inside a and y.
+struct Rows { int lo, hi; };
+__device__ __forceinline__ Rows rows_of(const Args &p, int e) {
+    if (e >= p.E) return {0, 0};
+    const int lo = min(max(p.offsets[e], 0), p.M);
+    return {lo, min(max(p.offsets[e + 1], lo), p.M)};
 }
 
-// Finds tile t of BM rows among the groups: 64 groups at a time, one a lane,
-// the lanes' tile counts summed by a scan.
+// Groups for each lane: lane l sums the tiles of groups l * groups_each ..
+__device__ __forceinline__ int groups_each(const Args &p) { return (p.E + 63) >> 6; }
+
+// The tiles of BM rows of all groups up to and with this lane's, at most
+// tiles_m for each lane (no more unless the offsets are out of order: the sums
+// cannot overflow).
 template <int BM>
-__device__ __forceinline__ Tile find_tile(const Args &p, int t) {
-    if (!p.offsets) return {t * BM, min(BM, p.M - t * BM), 0};
-    for (int e0 = 0; e0 < p.E; e0 += 64) {
-        const Group g = group_of(p, e0 + (threadIdx.x & 63));
-        const int mine = (g.hi - g.lo + BM - 1) / BM, upto = scan_lanes(mine);
-        const int all = __builtin_amdgcn_readlane(upto, 63);
-        if (t < all) {
-            const int owner = __ffsll((unsigned long long)__ballot(upto > t)) - 1;
-            const int m0 = __builtin_amdgcn_readlane(g.lo, owner) +
-                           (t - __builtin_amdgcn_readlane(upto - mine, owner)) * BM;
-            return {m0, min(BM, __builtin_amdgcn_readlane(g.hi, owner) - m0), e0 + owner};
-        }
-        t -= all;
+__device__ __forceinline__ int tiles_upto(const Args &p) {
+    if (!p.offsets) return 0;
+    const int each = groups_each(p), e0 = (threadIdx.x & 63) * each;
+    int mine = 0;
+#pragma unroll 4
+    for (int e = e0; e < e0 + each; ++e) {
+        const Rows r = rows_of(p, e);
+        mine = min(mine + (r.hi - r.lo + BM - 1) / BM, p.tiles_m);
     }
-    return {0, 0, 0};
+    return scan_lanes(mine);
+}
+
+// The tiles that there are, given tiles_upto.
+__device__ __forceinline__ int tile_count(const Args &p, int upto) {
+    return p.offsets ? min(__builtin_amdgcn_readlane(upto, 63), p.tiles_m) : p.tiles_m;
+}
+
+// Tile t of BM rows (rows == 0: there is none): the lane whose groups hold it,
+// then the group among that lane's.
+template <int BM>
+__device__ __forceinline__ Tile find_tile(const Args &p, int upto, int t) {
+    if (!p.offsets) return {t * BM, min(BM, p.M - t * BM), 0};
+    const unsigned long long past = __ballot(upto > t);
+    if (!past) return {0, 0, 0};
+    const int owner = __ffsll(past) - 1, each = groups_each(p);
+    if (owner) t -= __builtin_amdgcn_readlane(upto, owner - 1);
+    int e = owner * each;
+    if (each > 1) {
+        for (int c = 0;; c += 64) {
+            if (c >= each) return {0, 0, 0};
+            const int q = c + (threadIdx.x & 63);
+            const Rows r = q < each ? rows_of(p, e + q) : Rows{0, 0};
+            const int mine = (r.hi - r.lo + BM - 1) / BM, here = scan_lanes(min(mine, p.tiles_m));
+            const unsigned long long in = __ballot(here > t);
+            if (in) {
+                const int l = __ffsll(in) - 1;
+                if (l) t -= __builtin_amdgcn_readlane(here, l - 1);
+                e += c + l;
+                break;
+            }
+            t -= __builtin_amdgcn_readlane(here, 63);
+        }
+    }
+    const Rows r = rows_of(p, e);
+    const int m0 = __builtin_amdgcn_readfirstlane(r.lo) + t * BM;
+    return {m0, min(BM, __builtin_amdgcn_readfirstlane(r.hi) - m0), e};
 }
 
 // Scales a wavefront's sums and writes them.  acc[i][..]: rows row0 + 16 i +
@@ -288,14 +311,18 @@ __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_i8_block(Args p) {
     const int wave = all_waves % W, group = all_waves / W;
     const int wm = wave / WN, wn = wave % WN;
     const int steps = (p.K + G * BK - 1) / (G * BK);
-    const int tiles_m = count_tiles<BM>(p);
+    // Every wavefront leaves the same sums of the groups' tiles in LDS, and
+    // finds its own there whenever it looks for a tile.
+    int *sums = reinterpret_cast<int *>(lds + D * STAGE + 2 * (BM + BW) * 4) + lane;
+    *sums = tiles_upto<BM>(p);
+    const int tiles_m = tile_count(p, *sums);
     struct Place { Tile tl; int n0; };
     auto place = [&](int id, Place &at) {
         int tm, tn;
         if (!tile_of(id, tiles_m, p.tiles_n, tm, tn)) return false;
-        at.tl = find_tile<BM>(p, tm);
+        at.tl = find_tile<BM>(p, *sums, tm);
         at.n0 = tn * BN;
-        return true;
+        return at.tl.rows > 0;
     };
     int id = blockIdx.x;
     Place cur;
@@ -492,7 +519,7 @@ __global__ __launch_bounds__(W * 64) void gemm_i8_few(Args p, int ks_log2) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int KS = 1 << ks_log2, ks = wave & (KS - 1);
     const int tn = (int)(blockIdx.x % p.tiles_n);
-    const Tile tl = find_tile<BM>(p, (int)(blockIdx.x / p.tiles_n));
+    const Tile tl = find_tile<BM>(p, tiles_upto<BM>(p), (int)(blockIdx.x / p.tiles_n));
     if (tl.rows <= 0) return;
     const int n0 = (tn * (W >> ks_log2) + (wave >> ks_log2)) * (16 * FN);
     const size_t mat = (size_t)tl.e * p.N;
@@ -613,8 +640,12 @@ int64_t row_tiles(const Args &p, int bm) {
     return p.offsets ? p.M / bm + std::min(p.E, p.M) : tiles_of(p.M, bm);
 }
 
+// Where a launch goes: to the stream, or into a report of its plan.
+struct Report { int rows, cols, grid, block; };
+struct Target { hipStream_t stream; Report *report; };
+
 template <int NX, int FN, bool SWI, int W>
-int launch_few(Args p, hipStream_t stream) {
+int launch_few(Args p, const Target &to) {
     constexpr int FM = (NX + 1) / 2, FW = FN * (SWI ? 2 : 1), D = 2;
     const int64_t tiles_m = row_tiles(p, 8 * NX), strips = tiles_of(p.N, 16 * FN), units = tiles_of(p.K, BK);
     // Wavefronts on one strip's K: as many as it takes for 1536 wavefronts,
@@ -627,15 +658,19 @@ int launch_few(Args p, hipStream_t stream) {
     p.tiles_n = (int)tiles_of(strips, W >> log2);
     const int64_t grid = tiles_m * p.tiles_n;
     if (grid * (W * 64) > kMaxThreads) return Q4_EINVAL;
-    gemm_i8_few<NX, FN, SWI, W, D><<<(unsigned)grid, W * 64, W * D * (2 * FW + 2 * FM) * 1024, stream>>>(p, log2);
+    if (to.report) {
+        *to.report = {8 * NX, (W >> log2) * 16 * FN, (int)grid, W * 64};
+        return Q4_OK;
+    }
+    gemm_i8_few<NX, FN, SWI, W, D><<<(unsigned)grid, W * 64, W * D * (2 * FW + 2 * FM) * 1024, to.stream>>>(p, log2);
     return q4::launch_status();
 }
 
 template <int BM, int BW, int WM, int WN, int G, int D, bool SWI>
-int launch_block(Args p, hipStream_t stream) {
+int launch_block(Args p, const Target &to) {
     p.tiles_m = (int)row_tiles(p, BM);
     p.tiles_n = (int)tiles_of(p.N, SWI ? BW / 2 : BW);
-    constexpr int kLds = G * D * (BM + BW) * BK + 2 * (BM + BW) * 4, kThreads = WM * WN * G * 64;
+    constexpr int kLds = G * D * (BM + BW) * BK + 2 * (BM + BW) * 4 + 256, kThreads = WM * WN * G * 64;
     int64_t grid = (int64_t)p.tiles_m * p.tiles_n;
     if (grid > 0x7FFFFFFFll) return Q4_EINVAL;
     // Workgroups that stay and go through the tiles, each loading its next one
@@ -646,7 +681,11 @@ int launch_block(Args p, hipStream_t stream) {
     const int64_t steps = tiles_of(p.K, BK);
     if (G == 1 && steps >= D && steps <= 64) grid = std::min<int64_t>(grid, kCUs * (160 * 1024 / kLds));
     else if (grid * kThreads > kMaxThreads) return Q4_EINVAL;
-    gemm_i8_block<BM, BW, WM, WN, G, D, SWI><<<(unsigned)grid, kThreads, kLds, stream>>>(p);
+    if (to.report) {
+        *to.report = {BM, SWI ? BW / 2 : BW, (int)grid, kThreads};
+        return Q4_OK;
+    }
+    gemm_i8_block<BM, BW, WM, WN, G, D, SWI><<<(unsigned)grid, kThreads, kLds, to.stream>>>(p);
     return q4::launch_status();
 }
 
@@ -692,34 +731,39 @@ Kernel choose(const Args &p, int mats) {
 }
 
 template <bool SWI>
-int launch(const Args &p, Kernel k, hipStream_t stream) {
+int launch(const Args &p, Kernel k, const Target &to) {
     // Two workgroups share a CU with a ring of two stages; where there is only
     // one for each CU, it takes four: 1024 x 4096 x 4096 in 19.0 against 24.1
     // us, but 1999 x 14336 x 4096 in 128 against 112 (tiles of 128 x 128).
     auto alone = [&](int bm, int bw) { return row_tiles(p, bm) * tiles_of(p.N, SWI ? bw / 2 : bw) <= kCUs; };
     switch (k) {
-    case kFew8: return launch_few<1, 1, SWI, 8>(p, stream);
-    case kFew16: return launch_few<2, 1, SWI, 8>(p, stream);
-    case kFew32: return launch_few<4, 1, SWI, 8>(p, stream);
-    case kFew64: return launch_few<8, SWI ? 1 : 2, SWI, 4>(p, stream);
-    case kTile64: return launch_block<64, 128, 2, 4, 1, 3, SWI>(p, stream);
+    case kFew8: return launch_few<1, 1, SWI, 8>(p, to);
+    case kFew16: return launch_few<2, 1, SWI, 8>(p, to);
+    case kFew32: return launch_few<4, 1, SWI, 8>(p, to);
+    case kFew64: return launch_few<8, SWI ? 1 : 2, SWI, 4>(p, to);
+    case kTile64: return launch_block<64, 128, 2, 4, 1, 3, SWI>(p, to);
     case kTileDeep:
-        if (alone(64, 64)) return launch_block<64, 64, 2, 2, 2, 4, SWI>(p, stream);
-        return launch_block<64, 64, 2, 2, 2, 2, SWI>(p, stream);
+        if (alone(64, 64)) return launch_block<64, 64, 2, 2, 2, 4, SWI>(p, to);
+        return launch_block<64, 64, 2, 2, 2, 2, SWI>(p, to);
     case kTile128:
-        if (alone(128, 128)) return launch_block<128, 128, 2, 4, 1, 4, SWI>(p, stream);
-        return launch_block<128, 128, 2, 4, 1, 2, SWI>(p, stream);
-    case kTileWide: return launch_block<128, 256, 2, 4, 1, 3, SWI>(p, stream);
-    default: return launch_block<256, 256, 2, 4, 1, 2, SWI>(p, stream);
+        if (alone(128, 128)) return launch_block<128, 128, 2, 4, 1, 4, SWI>(p, to);
+        return launch_block<128, 128, 2, 4, 1, 2, SWI>(p, to);
+    case kTileWide: return launch_block<128, 256, 2, 4, 1, 3, SWI>(p, to);
+    default: return launch_block<256, 256, 2, 4, 1, 2, SWI>(p, to);
     }
 }
 
-int run(const Args &p, int mats, hipStream_t stream) {
+int check_sizes(const Args &p) {
     if (p.M < 0 || p.M > kMaxRows || p.N < 0 || p.N > kMaxRows || p.K < 16 || p.K % 16 || p.K > kMaxK)
         return Q4_EINVAL;
-    if (p.y_type != I8_F32 && p.y_type != I8_F16 && p.y_type != I8_BF16) return Q4_EINVAL;
     if (tiles_of(p.M, 16) * tiles_of(p.N, 16) > 0x7FFFFFFFll) return Q4_EINVAL;
     if (p.E < 1 || p.E > 65536 || (int64_t)p.E * p.N > 0x7FFFFFFFll) return Q4_EINVAL;
+    return Q4_OK;
+}
+
+int run(const Args &p, int mats, hipStream_t stream) {
+    if (int st = check_sizes(p)) return st;
+    if (p.y_type != I8_F32 && p.y_type != I8_F16 && p.y_type != I8_BF16) return Q4_EINVAL;
     if (p.M == 0 || p.N == 0) return Q4_OK;
     if (!p.a || !p.sa || !p.w[0] || !p.sw[0] || !p.y || (mats == 2 && (!p.w[1] || !p.sw[1]))) return Q4_ENULL;
     if (!q4::aligned(p.a, 16) || !q4::aligned(p.w[0], 16) || !q4::aligned(p.sa, 4) || !q4::aligned(p.sw[0], 4) ||
@@ -728,7 +772,8 @@ int run(const Args &p, int mats, hipStream_t stream) {
     if (mats == 2 && (!q4::aligned(p.w[1], 16) || !q4::aligned(p.sw[1], 4))) return Q4_EALIGN;
     if (int st = q4::check_device()) return st;
     const Kernel k = choose(p, mats);
-    return mats == 2 ? launch<true>(p, k, stream) : launch<false>(p, k, stream);
+    const Target to = {stream, nullptr};
+    return mats == 2 ? launch<true>(p, k, to) : launch<false>(p, k, to);
 }
 
 }  // namespace
@@ -761,4 +806,25 @@ extern "C" int gemm_i8_grouped_swiglu(const int8_t *a, const float *a_scales, co
     if (!offsets && M > 0 && N > 0) return Q4_ENULL;
     return run({a, a_scales, {w_gate, w_up}, {scales_gate, scales_up}, nullptr, offsets, y, y_type, M, N, K, E, 0, 0},
                2, static_cast<hipStream_t>(stream));
+}
+
+extern "C" int gemm_i8_geometry(int matrices, int M, int E, int N, int K, int *tile_rows, int *tile_cols, int *grid,
+                                int *block) {
+    static const int32_t kGrouped = 0;             // stands for offsets, never read
+    Args p = {};
+    p.M = M, p.N = N, p.K = K, p.E = E ? E : 1;
+    p.offsets = E ? &kGrouped : nullptr;
+    if (matrices != 1 && matrices != 2) return Q4_EINVAL;
+    if (int st = check_sizes(p)) return st;
+    Report r = {0, 0, 0, 0};
+    if (M > 0 && N > 0) {
+        const Kernel k = choose(p, matrices);
+        const Target to = {nullptr, &r};
+        if (int st = matrices == 2 ? launch<true>(p, k, to) : launch<false>(p, k, to)) return st;
+    }
+    if (tile_rows) *tile_rows = r.rows;
+    if (tile_cols) *tile_cols = r.cols;
+    if (grid) *grid = r.grid;
+    if (block) *block = r.block;
+    return Q4_OK;
 }

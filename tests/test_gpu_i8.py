@@ -123,6 +123,42 @@ def test_gemm(M, N, K, t):
     check(y, *i8.gemm(a, sa, w, sw), t, f"{M} {N} {K}")
 
 
+# Every tile that the products choose from, with rows and columns that end
+# inside tiles and K inside steps, and more tiles than workgroups.
+LARGE = [(64, 4100, 2064), (500, 2050, 2064), (330, 4870, 912), (1090, 5000, 528), (3775, 1827, 1056),
+         (3984, 3781, 656), (2900, 5050, 528), (4100, 4100, 272), (5000, 300, 4112)]
+LARGE_SWIGLU = [(64, 2100, 2064), (300, 1000, 2064), (200, 2320, 912), (1060, 2500, 528), (2593, 1533, 800),
+                (2365, 3095, 432), (1500, 4100, 400)]
+
+
+@pytest.mark.parametrize("M,N,K", LARGE)
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+def test_gemm_large(M, N, K, t):
+    a, w, sa, sw = codes(1, M, K), codes(2, N, K), small_scales(3, K, M), small_scales(4, K, N)
+    y = q4.gemm_i8(dev(a), dev(sa), dev(w), dev(sw), dtype=TYPES[t])
+    check(y, *i8.gemm(a, sa, w, sw), t, f"{M} {N} {K}")
+
+
+@pytest.mark.parametrize("M,N,K", LARGE_SWIGLU)
+def test_swiglu_large(M, N, K):
+    a, sa = codes(1, M, K), small_scales(3, K, M)
+    gate, up = (codes(2, N, K), small_scales(4, K, N) * 3), (codes(5, N, K), small_scales(6, K, N))
+    y = q4.gemm_i8_swiglu(dev(a), dev(sa), tuple(map(dev, gate)), tuple(map(dev, up)), dtype=torch.float16)
+    check(y, *i8.swiglu(a, sa, gate, up), "f16", f"{M} {N} {K}")
+
+
+def test_sizes_take_every_tile():
+    for mats, shapes, tiles in ((1, GEMM + LARGE, {(8,), (16,), (32,), (64, 32), (64, 64), (64, 128), (128, 128),
+                                                   (128, 256), (256, 256)}),
+                                (2, LARGE_SWIGLU, {(64, 16), (64, 32), (64, 64), (128, 64), (128, 128), (256, 128)})):
+        got = [q4.gemm_i8_geometry(mats, *s) for s in shapes]
+        seen = {(g["tile_rows"], g["tile_cols"]) for g in got} | {(g["tile_rows"],) for g in got}
+        assert tiles <= seen, tiles - seen
+        # Both kinds of launch: a workgroup for each tile, and workgroups that go through several.
+        many = [g["grid"] < -(-s[0] // g["tile_rows"]) * -(-s[1] // g["tile_cols"]) for g, s in zip(got, shapes)]
+        assert any(many) and not all(many)
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 77, 256), (40, 520, 144), (130, 64, 1024), (600, 515, 400)])
 @pytest.mark.parametrize("t", TYPES)
 def test_gemm_bias(M, N, K, t):
@@ -218,6 +254,8 @@ GROUPS = {
     "none, in the middle": [4, 4, 4, 4],
     "many": np.concatenate([[0], np.cumsum(np.random.default_rng(8).integers(0, 9, 150))]).tolist(),
     "uneven": [0, 1, 400, 402, 402, 700, 701],
+    "more than a lane's": np.concatenate([[0], np.cumsum(np.random.default_rng(9).integers(0, 3, 301) ** 2)]).tolist(),
+    "large and small": [0, 0, 1000, 1000, 1003, 1003, 1130, 2400, 2400],
 }
 
 
@@ -245,8 +283,42 @@ def test_grouped(name, swiglu, t, N, K):
     assert (y[torch.from_numpy(~inside).to(DEV)] == 7).all()
 
 
+@pytest.mark.parametrize("E,rows", [(5000, 1), (5000, 700), (65536, 40)])
+def test_grouped_many_experts(E, rows):
+    """Few rows among very many experts."""
+    N, K = 24, 32
+    M = rows
+    rng = np.random.default_rng(E)
+    chosen = np.sort(rng.integers(0, E, M))
+    off = np.concatenate([[0], np.cumsum(np.bincount(chosen, minlength=E))])
+    a, sa = codes(1, M, K), small_scales(3, K, M)
+    w, sw = codes(2, E, N, K), small_scales(4, K, E, N)
+    y = q4.gemm_i8_grouped(dev(a), dev(sa), dev(w), dev(sw), torch.tensor(off, dtype=torch.int32, device=DEV))
+    want = np.concatenate([i8.product(a[lo:hi], sa[lo:hi], w[e], sw[e]) for e, lo, hi in i8.groups(off)])
+    check(y, want, 3.1 * i8.U * np.abs(want), "f32", f"{E}")
+
+
+@pytest.mark.parametrize("M,N,K,E", [(2500, 4200, 1040, 4), (9000, 1030, 272, 3)])
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_grouped_goes_through_many_tiles(M, N, K, E, swiglu):
+    N = N // 2 if swiglu else N
+    off = [0, M // 3 + 1, M // 3 + 1, M - 50, M][:E] + [M]
+    E = len(off) - 1
+    a, sa = codes(1, M, K), small_scales(3, K, M)
+    gate, up = (codes(2, E, N, K), small_scales(4, K, E, N)), (codes(5, E, N, K), small_scales(6, K, E, N))
+    o = torch.tensor(off, dtype=torch.int32, device=DEV)
+    if swiglu:
+        y = q4.gemm_i8_grouped_swiglu(dev(a), dev(sa), tuple(map(dev, gate)), tuple(map(dev, up)), o)
+    else:
+        y = q4.gemm_i8_grouped(dev(a), dev(sa), dev(gate[0]), dev(gate[1]), o)
+    for e, lo, hi in i8.groups(off):
+        g, u = (gate[0][e], gate[1][e]), (up[0][e], up[1][e])
+        want = i8.swiglu(a[lo:hi], sa[lo:hi], g, u) if swiglu else i8.gemm(a[lo:hi], sa[lo:hi], *g)
+        check(y[lo:hi], *want, "f32", f"expert {e}")
+
+
 @pytest.mark.parametrize("off", [[0, 50, 30, 80], [-5, 10, 900, 40], [70, 60, 50, 40], [2**31 - 1, -2**31, 5, 9]])
-@pytest.mark.parametrize("M", [40, 300])
+@pytest.mark.parametrize("M", [10, 40, 300])
 def test_grouped_bad_offsets_stay_inside(off, M):
     """Offsets out of order and range: nothing outside y is written."""
     N, K, E = 40, 160, 3

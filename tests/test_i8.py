@@ -50,7 +50,8 @@ def call(L, fn, M, N, K, t=q4.I8_F32, E=2, p=None, at=()):
     return getattr(L, fn)(*ptr, t, *sizes, None)
 
 
-GEMMS = [f for f in q4.EXPORTS_I8 if f != "quant_i8"]
+CALLS = [f for f in q4.EXPORTS_I8 if f != "gemm_i8_geometry"]
+GEMMS = [f for f in CALLS if f != "quant_i8"]
 
 
 @pytest.mark.parametrize("fn", GEMMS)
@@ -64,7 +65,7 @@ def test_gemm_sizes(L, fn, M, N, K, want):
     assert call(L, fn, M, N, K) == want
 
 
-@pytest.mark.parametrize("fn", q4.EXPORTS_I8)
+@pytest.mark.parametrize("fn", CALLS)
 @pytest.mark.parametrize("t", [-1, 3])
 def test_types(L, fn, t):
     assert call(L, fn, 4, 8, 64, t=t) == q4.Q4_EINVAL
@@ -77,7 +78,7 @@ def test_group_counts(L, fn):
     assert call(L, fn, 4, 2**24, 64, E=256) == q4.Q4_EINVAL
 
 
-@pytest.mark.parametrize("fn", q4.EXPORTS_I8)
+@pytest.mark.parametrize("fn", CALLS)
 def test_pointers(L, fn):
     n = {"quant_i8": 3, "gemm_i8": 6, "gemm_i8_swiglu": 7, "gemm_i8_grouped": 6, "gemm_i8_grouped_swiglu": 8}[fn]
     for i in range(n):
@@ -97,7 +98,7 @@ def test_quant_sizes(L, M, K, want):
 
 
 @pytest.mark.skipif(torch.cuda.is_available(), reason="a GPU would be given fake addresses")
-@pytest.mark.parametrize("fn", q4.EXPORTS_I8)
+@pytest.mark.parametrize("fn", CALLS)
 def test_no_device(L, fn):
     assert call(L, fn, 4, 8, 64) == q4.Q4_EDEVICE
 
@@ -113,6 +114,35 @@ def test_binding_refuses_host_tensors_and_wrong_types():
         q4.quant_i8(a)
     with pytest.raises(ValueError):
         q4.quant_i8(a.float())
+
+
+# Shapes (matrices, M, N, K, groups) and the tile of y that they take.
+PLANS = [((1, 1, 14336, 4096, 0), (8, 64)), ((1, 12, 4096, 4096, 0), (16, 16)), ((1, 24, 4096, 14336, 0), (32, 16)),
+         ((1, 64, 4096, 14336, 0), (64, 32)), ((1, 512, 2048, 2048, 0), (64, 64)), ((1, 333, 4864, 896, 0), (64, 128)),
+         ((1, 1024, 14336, 512, 0), (128, 128)), ((1, 3775, 1826, 1056, 0), (128, 256)),
+         ((1, 8192, 14336, 4096, 0), (256, 256)), ((2, 8192, 14336, 4096, 0), (256, 128)),
+         ((2, 200, 2816, 1024, 64), (16, 128)), ((2, 900, 2816, 1024, 64), (64, 64)),
+         ((2, 8000, 2816, 1024, 64), (128, 128))]
+
+
+@pytest.mark.parametrize("shape,tile", PLANS)
+def test_geometry(L, shape, tile):
+    mats, M, N, K, E = shape
+    g = q4.gemm_i8_geometry(mats, M, N, K, E)
+    assert (g["tile_rows"], g["tile_cols"]) == tile
+    assert g["block"] in (256, 512)
+    tiles = -(-M // tile[0]) * -(-N // tile[1])
+    # One workgroup a tile, or a chip full of them that go through the tiles;
+    # groups may end inside a tile.
+    assert g["grid"] == tiles or g["grid"] in (256, 512) and g["grid"] < tiles or E and tiles < g["grid"]
+
+
+def test_geometry_refusals(L):
+    for shape in ((0, 4, 8, 64), (3, 4, 8, 64), (1, 4, 8, 24), (1, -1, 8, 64), (1, 4, 8, 64, -1),
+                  (1, 2**24, 2**24, 64)):
+        with pytest.raises(q4.Q4Error):
+            q4.gemm_i8_geometry(*shape)
+    assert q4.gemm_i8_geometry(1, 0, 8, 64)["grid"] == 0
 
 
 # ---------------------------------------------------------------- the oracle
