@@ -31,6 +31,7 @@ struct Args {
     void *y;
     int y_type, M, N, K, E;
     int tiles_m, tiles_n;
+    bool once;                 // the weights' stream is more than a cache would keep
 };
 
 // The fragment of 16 weight rows j (of F that share a run of 16 F rows) takes
@@ -259,9 +260,11 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void *base, uint
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, (int)bytes, 0x00020000);
 }
 
-// 16 bytes a lane from memory to LDS, lane l's at `to` + 16 l.
+// 16 bytes a lane from memory to LDS, lane l's at `to` + 16 l.  ONCE: read
+// once, so that the caches need not keep it (non-temporal).
+template <bool ONCE = false>
 __device__ __forceinline__ void load16(__amdgpu_buffer_rsrc_t r, char *to, uint32_t voff, int soff) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t)to, 16, voff, soff, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t)to, 16, voff, soff, 0, ONCE ? 2 : 0);
 }
 
 // 4 bytes a lane from an address of its own, lane l's at `to` + l.
@@ -549,8 +552,11 @@ __global__ __launch_bounds__(W * 64) void gemm_i8_few(Args p, int ks_log2) {
 #pragma unroll
             for (int s = 0; s < MATS; ++s)
 #pragma unroll
-                for (int i = 0; i < 2 * FN; ++i)
-                    load16(rw[s], at + (s * 2 * FN + i) * 1024, vw[i] + k, 0);
+                for (int i = 0; i < 2 * FN; ++i) {
+                    char *to = at + (s * 2 * FN + i) * 1024;
+                    if (p.once) load16<true>(rw[s], to, vw[i] + k, 0);
+                    else load16(rw[s], to, vw[i] + k, 0);
+                }
 #pragma unroll
             for (int i = 0; i < NX; ++i)
                 load16(rx, at + (2 * FW + i) * 1024, vx[i] + k, 0);
@@ -648,6 +654,12 @@ template <int NX, int FN, bool SWI, int W>
 int launch_few(Args p, const Target &to) {
     constexpr int FM = (NX + 1) / 2, FW = FN * (SWI ? 2 : 1), D = 2;
     const int64_t tiles_m = row_tiles(p, 8 * NX), strips = tiles_of(p.N, 16 * FN), units = tiles_of(p.K, BK);
+    // Weights of more than a quarter of the 256 MB cache are loaded
+    // non-temporally.  Cycling 2 GB of matrices, one row through 4096 -> 14336
+    // (59 MB) takes 12.6 us so and 14.2 without, the SwiGLU of two such 24.0
+    // and 26.3; but a small model's matrices can be found in the cache, and
+    // three of 59 MB in turn take 11.8 us so and 10.7 without.
+    p.once = (int64_t)(SWI ? 2 : 1) * p.E * p.N * p.K > (int64_t)64 << 20;
     // Wavefronts on one strip's K: as many as it takes for 1536 wavefronts,
     // 6 for each CU, while each has a unit.  At 8 rows, 4096 -> 14336, 2 of
     // them take 11.8 us and 8 take 13.6; at 24 rows, 14336 -> 4096, 8 take
@@ -780,14 +792,14 @@ int run(const Args &p, int mats, hipStream_t stream) {
 
 extern "C" int gemm_i8(const int8_t *a, const float *a_scales, const int8_t *w, const float *w_scales,
                        const float *bias, void *y, int y_type, int M, int N, int K, void *stream) {
-    return run({a, a_scales, {w, nullptr}, {w_scales, nullptr}, bias, nullptr, y, y_type, M, N, K, 1, 0, 0}, 1,
+    return run({a, a_scales, {w, nullptr}, {w_scales, nullptr}, bias, nullptr, y, y_type, M, N, K, 1, 0, 0, false}, 1,
                static_cast<hipStream_t>(stream));
 }
 
 extern "C" int gemm_i8_swiglu(const int8_t *a, const float *a_scales, const int8_t *w_gate,
                               const float *scales_gate, const int8_t *w_up, const float *scales_up, void *y,
                               int y_type, int M, int N, int K, void *stream) {
-    return run({a, a_scales, {w_gate, w_up}, {scales_gate, scales_up}, nullptr, nullptr, y, y_type, M, N, K, 1, 0, 0},
+    return run({a, a_scales, {w_gate, w_up}, {scales_gate, scales_up}, nullptr, nullptr, y, y_type, M, N, K, 1, 0, 0, false},
                2, static_cast<hipStream_t>(stream));
 }
 
@@ -795,7 +807,7 @@ extern "C" int gemm_i8_grouped(const int8_t *a, const float *a_scales, const int
                                const int32_t *offsets, void *y, int y_type, int M, int E, int N, int K,
                                void *stream) {
     if (!offsets && M > 0 && N > 0) return Q4_ENULL;
-    return run({a, a_scales, {w, nullptr}, {w_scales, nullptr}, nullptr, offsets, y, y_type, M, N, K, E, 0, 0}, 1,
+    return run({a, a_scales, {w, nullptr}, {w_scales, nullptr}, nullptr, offsets, y, y_type, M, N, K, E, 0, 0, false}, 1,
                static_cast<hipStream_t>(stream));
 }
 
@@ -804,7 +816,7 @@ extern "C" int gemm_i8_grouped_swiglu(const int8_t *a, const float *a_scales, co
                                       const int32_t *offsets, void *y, int y_type, int M, int E, int N, int K,
                                       void *stream) {
     if (!offsets && M > 0 && N > 0) return Q4_ENULL;
-    return run({a, a_scales, {w_gate, w_up}, {scales_gate, scales_up}, nullptr, offsets, y, y_type, M, N, K, E, 0, 0},
+    return run({a, a_scales, {w_gate, w_up}, {scales_gate, scales_up}, nullptr, offsets, y, y_type, M, N, K, E, 0, 0, false},
                2, static_cast<hipStream_t>(stream));
 }
 
