@@ -419,6 +419,82 @@ def test_graph_replays(M):
         assert all(torch.equal(a, b) for a, b in zip(got, want)), k
 
 
+@pytest.mark.parametrize("T", [6, 200, 900])
+def test_graph_replays_with_other_groups(T):
+    """The offsets are read on the GPU: a captured call takes the groups of the moment."""
+    E, D, F = 5, 512, 320
+    x = torch.randn(T, D, generator=torch.Generator().manual_seed(1)).bfloat16().to(DEV)
+    gate, up = [(dev(codes(k, E, F, D)), dev(small_scales(k + 1, D, E, F) * 5)) for k in (2, 4)]
+    down = dev(codes(7, E, D, F)), dev(small_scales(8, F, E, D))
+    o = torch.zeros(E + 1, dtype=torch.int32, device=DEV)
+
+    def experts():
+        c, s = q4.quant_i8(x)
+        h = q4.gemm_i8_grouped_swiglu(c, s, gate, up, o, dtype=torch.bfloat16)
+        return q4.gemm_i8_grouped(*q4.quant_i8(h), *down, o, dtype=torch.bfloat16)
+
+    def route(seed):
+        c = torch.from_numpy(np.random.default_rng(seed).multinomial(T, [0.6, 0, 0.25, 0.1, 0.05]))
+        o.copy_(torch.cat([torch.zeros(1, dtype=torch.long), c.cumsum(0)]).int())
+
+    route(0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        experts()
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = experts()
+    for k in range(1, 5):
+        route(k)
+        want = experts()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want), k
+
+
+def test_weights_past_32_bits():
+    """Experts whose matrices start beyond 4 GiB, by a few rows and by many."""
+    E, N, K = 80, 14336, 4096                              # 4.7 GB
+    w = torch.empty(E, N, K, dtype=torch.int8, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(3)
+    for part in w.view(-1).split(1 << 28):
+        part.copy_(torch.randint(-128, 128, part.shape, generator=g, device=DEV, dtype=torch.int8))
+    sw = dev(small_scales(4, K, E, N))
+    for T in (7, 300):
+        a, sa = codes(1, T, K), small_scales(3, K, T)
+        off = [0] * (E - 1) + [2, T]                       # all in the last two experts
+        y = q4.gemm_i8_grouped(dev(a), dev(sa), w, sw, torch.tensor(off, dtype=torch.int32, device=DEV))
+        for e, lo, hi in ((E - 2, 0, 2), (E - 1, 2, T)):
+            cols = slice(N - 500, N)
+            want = i8.gemm(a[lo:hi], sa[lo:hi], w[e, cols].cpu().numpy(), sw[e, cols].cpu().numpy())
+            check(y[lo:hi, cols], *want, "f32", f"{T} rows, expert {e}")
+
+
+def test_rows_past_32_bits():
+    """Inputs, codes and outputs whose last rows lie beyond 4 GiB."""
+    M, K, N = 270_000, 16384, 16
+    x = torch.empty(M, K, dtype=torch.float16, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(3)
+    for part in x.split(1 << 14):
+        part.copy_(torch.randn(part.shape, generator=g, device=DEV, dtype=torch.float16))
+    c, s = q4.quant_i8(x)
+    at = [0, M // 2, M - 1]
+    cw, sw = i8.quant(x[at].double().cpu().numpy())
+    assert np.array_equal(c[at].cpu().numpy(), cw) and np.array_equal(s[at].cpu().numpy(), sw)
+    del x
+    w, ws = codes(2, N, K), small_scales(4, K, N)
+    y = q4.gemm_i8(c, s, dev(w), dev(ws))
+    check(y[at], *i8.gemm(cw, sw, w, ws), "f32", "a")
+    del c
+    M, K, N = 70_000, 256, 32_768
+    a, sa, w, ws = codes(1, M, K), small_scales(3, K, M), codes(2, N, K), small_scales(4, K, N)
+    for K in (256, 48):                                    # tiles, and K below a step
+        y = q4.gemm_i8(dev(a[:, :K]), dev(sa), dev(w[:, :K]), dev(ws), dtype=torch.bfloat16)
+        check(y[at[:1] + [M - 1]], *i8.gemm(a[[0, M - 1], :K], sa[[0, M - 1]], w[:, :K], ws), "bf16", "y")
+
+
 @pytest.mark.parametrize("M", [3, 300])
 def test_two_streams(M):
     """Calls on two streams at once, each with its own outputs."""
