@@ -440,14 +440,18 @@ def scan2_config() -> tuple[int, int, int, int]:
 # entry point tests its arguments in one expression; only when that fails do
 # the checks below run one by one, to raise what is wrong.
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _i8_call(fn: str, dev: int, *args) -> None:
     """Calls the entry point on the device's current stream, with that device current."""
     f = getattr(_lib or lib(), fn)
-    if dev == torch._C._cuda_getDevice():
-        status = f(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if dev == _current_device():
+        status = f(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            status = f(*args, torch._C._cuda_getCurrentRawStream(dev))
+            status = f(*args, _raw_stream(dev))
     if status:
         raise Q4Error(fn, status)
 
@@ -471,6 +475,7 @@ def _i8_refuse(tensors: dict, shapes: dict, dtype=None) -> None:
 
 
 _I8, _F32, _I32 = torch.int8, torch.float32, torch.int32
+_X_TYPES = tuple(I8_TYPES)
 
 
 def _size(t, d: int):
@@ -483,14 +488,14 @@ def quant_i8(x: torch.Tensor, out: tuple | None = None) -> tuple[torch.Tensor, t
     bfloat16: scales[m] = max|x[m]| / 127 and codes = x / scales to the nearest
     integer.  K is a multiple of 16.  A row with an Inf or a NaN gets the scale
     NaN and zero codes."""
-    _need(x, "x", tuple(I8_TYPES))
+    _need(x, "x", _X_TYPES)
     if x.dim() != 2:
         raise ValueError("x must be [M, K]")
     M, K = x.shape
     dev = x.get_device()
     if out is None:
-        codes = torch.empty((M, K), dtype=_I8, device=x.device)
-        scales = torch.empty((M,), dtype=_F32, device=x.device)
+        codes = torch.empty_like(x, dtype=_I8)
+        scales = torch.empty(M, dtype=_F32, device=x.device)
     else:
         codes, scales = out
         _need(codes, "codes", (_I8,), x.device)
@@ -529,7 +534,7 @@ def gemm_i8(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scales: 
                     "w_scales": (w_scales, (_size(w, 0),)), "bias": (bias, (_size(w, 0),)),
                     "out": (out, (_size(a, 0), _size(w, 0)))}, dtype)
     if out is None:
-        out = torch.empty((M, N), dtype=dtype, device=a.device)
+        out = torch.empty(M, N, dtype=dtype, device=a.device)
     _i8_call("gemm_i8", dev, a.data_ptr(), a_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(),
              None if bias is None else bias.data_ptr(), out.data_ptr(), t, M, N, K)
     return out
@@ -573,7 +578,7 @@ def gemm_i8_swiglu(a: torch.Tensor, a_scales: torch.Tensor, gate: tuple, up: tup
         _i8_refuse_pair(a, a_scales, gate, up, None, out, dtype)
     N = wg.shape[0]
     if out is None:
-        out = torch.empty((M, N), dtype=dtype, device=a.device)
+        out = torch.empty(M, N, dtype=dtype, device=a.device)
     _i8_call("gemm_i8_swiglu", dev, a.data_ptr(), a_scales.data_ptr(), wg.data_ptr(), sg.data_ptr(), wu.data_ptr(),
              su.data_ptr(), out.data_ptr(), t, M, N, K)
     return out
@@ -606,7 +611,7 @@ def gemm_i8_grouped(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_
                     "w": (w, (E, None, _size(a, 1))), "w_scales": (w_scales, (E, _size(w, 1))),
                     "out": (out, (_size(a, 0), _size(w, 1)))}, dtype)
     if out is None:
-        out = torch.empty((M, N), dtype=dtype, device=a.device)
+        out = torch.empty(M, N, dtype=dtype, device=a.device)
     _i8_call("gemm_i8_grouped", dev, a.data_ptr(), a_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(),
              offsets.data_ptr(), out.data_ptr(), t, M, E, N, K)
     return out
@@ -631,7 +636,7 @@ def gemm_i8_grouped_swiglu(a: torch.Tensor, a_scales: torch.Tensor, gate: tuple,
     if not fine:
         _i8_refuse_pair(a, a_scales, gate, up, offsets, out, dtype)
     if out is None:
-        out = torch.empty((M, N), dtype=dtype, device=a.device)
+        out = torch.empty(M, N, dtype=dtype, device=a.device)
     _i8_call("gemm_i8_grouped_swiglu", dev, a.data_ptr(), a_scales.data_ptr(), wg.data_ptr(), sg.data_ptr(),
              wu.data_ptr(), su.data_ptr(), offsets.data_ptr(), out.data_ptr(), t, M, E, N, K)
     return out
