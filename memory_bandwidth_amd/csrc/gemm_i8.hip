@@ -21,6 +21,17 @@ typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 
+constexpr int kCUs = 256;
+
+// Tiles of 256 x 256 come in rounds of one for each CU.  Where the last round
+// would have up to 96, they are halved both ways, in a launch of their own: up
+// to 64 then take one round of a third of the time, more take two.  With and
+// without, 4600 x 4096 x 14336 (32 tiles left) takes 241 and 315 us, 5376 rows
+// (80 left) 295 and 316, 9000 x 8192 x 8192 (128 left) 502 and 483.  kWhole
+// and kRest are the two launches.
+enum Part { kAll, kWhole, kRest };
+constexpr int kRestMost = 96;
+
 struct Args {
     const int8_t *a;
     const float *sa;
@@ -30,7 +41,8 @@ struct Args {
     const int32_t *offsets;    // groups, or NULL
     void *y;
     int y_type, M, N, K, E;
-    int tiles_m, tiles_n;
+    int tiles_m, tiles_n;      // kRest: of the tiles that are halved
+    Part part;
     bool once;                 // the weights' stream is more than a cache would keep
 };
 
@@ -122,18 +134,17 @@ __device__ __forceinline__ Rows rows_of(const Args &p, int e) {
 // Groups for each lane: lane l sums the tiles of groups l * groups_each ..
 __device__ __forceinline__ int groups_each(const Args &p) { return (p.E + 63) >> 6; }
 
-// The tiles of BM rows of all groups up to and with this lane's, at most
+// The tiles of bm rows of all groups up to and with this lane's, at most
 // tiles_m for each lane (no more unless the offsets are out of order: the sums
 // cannot overflow).
-template <int BM>
-__device__ __forceinline__ int tiles_upto(const Args &p) {
+__device__ __forceinline__ int tiles_upto(const Args &p, int bm) {
     if (!p.offsets) return 0;
     const int each = groups_each(p), e0 = (threadIdx.x & 63) * each;
     int mine = 0;
 #pragma unroll 4
     for (int e = e0; e < e0 + each; ++e) {
         const Rows r = rows_of(p, e);
-        mine = min(mine + (r.hi - r.lo + BM - 1) / BM, p.tiles_m);
+        mine = min(mine + (int)((unsigned)(r.hi - r.lo + bm - 1) / (unsigned)bm), p.tiles_m);
     }
     return scan_lanes(mine);
 }
@@ -143,11 +154,10 @@ __device__ __forceinline__ int tile_count(const Args &p, int upto) {
     return p.offsets ? min(__builtin_amdgcn_readlane(upto, 63), p.tiles_m) : p.tiles_m;
 }
 
-// Tile t of BM rows (rows == 0: there is none): the lane whose groups hold it,
+// Tile t of bm rows (rows == 0: there is none): the lane whose groups hold it,
 // then the group among that lane's.
-template <int BM>
-__device__ __forceinline__ Tile find_tile(const Args &p, int upto, int t) {
-    if (!p.offsets) return {t * BM, min(BM, p.M - t * BM), 0};
+__device__ __forceinline__ Tile find_tile(const Args &p, int bm, int upto, int t) {
+    if (!p.offsets) return {t * bm, min(bm, p.M - t * bm), 0};
     const unsigned long long past = __ballot(upto > t);
     if (!past) return {0, 0, 0};
     const int owner = __ffsll(past) - 1, each = groups_each(p);
@@ -158,7 +168,7 @@ __device__ __forceinline__ Tile find_tile(const Args &p, int upto, int t) {
             if (c >= each) return {0, 0, 0};
             const int q = c + (threadIdx.x & 63);
             const Rows r = q < each ? rows_of(p, e + q) : Rows{0, 0};
-            const int mine = (r.hi - r.lo + BM - 1) / BM, here = scan_lanes(min(mine, p.tiles_m));
+            const int mine = (int)((unsigned)(r.hi - r.lo + bm - 1) / (unsigned)bm), here = scan_lanes(min(mine, p.tiles_m));
             const unsigned long long in = __ballot(here > t);
             if (in) {
                 const int l = __ffsll(in) - 1;
@@ -170,8 +180,8 @@ __device__ __forceinline__ Tile find_tile(const Args &p, int upto, int t) {
         }
     }
     const Rows r = rows_of(p, e);
-    const int m0 = __builtin_amdgcn_readfirstlane(r.lo) + t * BM;
-    return {m0, min(BM, __builtin_amdgcn_readfirstlane(r.hi) - m0), e};
+    const int m0 = __builtin_amdgcn_readfirstlane(r.lo) + t * bm;
+    return {m0, min(bm, __builtin_amdgcn_readfirstlane(r.hi) - m0), e};
 }
 
 // Scales a wavefront's sums and writes them.  acc[i][..]: rows row0 + 16 i +
@@ -224,6 +234,12 @@ __device__ __forceinline__ bool tile_of(int b, int tiles_m, int tiles_n, int &tm
     tm = first + in % rows;
     tn = in / rows;
     return true;
+}
+
+// Of `all` tiles, those that kWhole takes.
+__device__ __host__ __forceinline__ int whole_rounds(int all) {
+    const int left = all % kCUs;
+    return left <= kRestMost ? all - left : all;
 }
 
 // LDS tiles: rows of 128 bytes in eight 16-byte chunks; chunk c of row r
@@ -317,15 +333,23 @@ __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_i8_block(Args p) {
     // Every wavefront leaves the same sums of the groups' tiles in LDS, and
     // finds its own there whenever it looks for a tile.
     int *sums = reinterpret_cast<int *>(lds + D * STAGE + 2 * (BM + BW) * 4) + lane;
-    *sums = tiles_upto<BM>(p);
-    const int tiles_m = tile_count(p, *sums);
+    const int bm = p.part == kRest ? 2 * BM : BM;
+    *sums = tiles_upto(p, bm);
+    const int tiles_m = tile_count(p, *sums), all = tiles_m * p.tiles_n, whole = whole_rounds(all);
     struct Place { Tile tl; int n0; };
     auto place = [&](int id, Place &at) {
+        const int b = p.part == kRest ? whole + (id >> 2) : id;
         int tm, tn;
-        if (!tile_of(id, tiles_m, p.tiles_n, tm, tn)) return false;
-        at.tl = find_tile<BM>(p, *sums, tm);
+        if (b >= (p.part == kWhole ? whole : all) || !tile_of(b, tiles_m, p.tiles_n, tm, tn)) return false;
+        at.tl = find_tile(p, bm, *sums, tm);
         at.n0 = tn * BN;
-        return at.tl.rows > 0;
+        if (p.part == kRest) {
+            const int down = (id >> 1 & 1) * BM;
+            at.tl.m0 += down;
+            at.tl.rows = min(BM, at.tl.rows - down);
+            at.n0 = (2 * tn + (id & 1)) * BN;
+        }
+        return at.tl.rows > 0 && at.n0 < p.N;
     };
     int id = blockIdx.x;
     Place cur;
@@ -522,7 +546,7 @@ __global__ __launch_bounds__(W * 64) void gemm_i8_few(Args p, int ks_log2) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int KS = 1 << ks_log2, ks = wave & (KS - 1);
     const int tn = (int)(blockIdx.x % p.tiles_n);
-    const Tile tl = find_tile<BM>(p, tiles_upto<BM>(p), (int)(blockIdx.x / p.tiles_n));
+    const Tile tl = find_tile(p, BM, tiles_upto(p, BM), (int)(blockIdx.x / p.tiles_n));
     if (tl.rows <= 0) return;
     const int n0 = (tn * (W >> ks_log2) + (wave >> ks_log2)) * (16 * FN);
     const size_t mat = (size_t)tl.e * p.N;
@@ -637,7 +661,6 @@ constexpr int kMaxK = 131056;      // 16384 * 131056 < 2^31: the sum fits whatev
 bool elem_aligned(const void *y, int type) { return q4::aligned(y, type == I8_F32 ? 4 : 2); }
 
 constexpr int64_t kMaxThreads = 0xFFFFFFFFll;      // of one launch
-constexpr int kCUs = 256;
 
 int64_t tiles_of(int64_t n, int tile) { return (n + tile - 1) / tile; }
 
@@ -680,18 +703,23 @@ int launch_few(Args p, const Target &to) {
 
 template <int BM, int BW, int WM, int WN, int G, int D, bool SWI>
 int launch_block(Args p, const Target &to) {
-    p.tiles_m = (int)row_tiles(p, BM);
-    p.tiles_n = (int)tiles_of(p.N, SWI ? BW / 2 : BW);
     constexpr int kLds = G * D * (BM + BW) * BK + 2 * (BM + BW) * 4 + 256, kThreads = WM * WN * G * 64;
+    constexpr int kBN = SWI ? BW / 2 : BW;
+    const int half = p.part == kRest ? 2 : 1;
+    p.tiles_m = (int)row_tiles(p, half * BM);
+    p.tiles_n = (int)tiles_of(p.N, half * kBN);
     int64_t grid = (int64_t)p.tiles_m * p.tiles_n;
     if (grid > 0x7FFFFFFFll) return Q4_EINVAL;
+    if (p.part == kWhole) grid = p.offsets ? grid : whole_rounds((int)grid);
+    if (p.part == kRest) grid = 4 * (p.offsets ? std::min<int64_t>(grid, kRestMost) : grid - whole_rounds((int)grid));
     // Workgroups that stay and go through the tiles, each loading its next one
-    // while it finishes the last: 8192 x 14336 x 4096 takes 393 us so, 400
-    // with a workgroup for each tile; 8000 rows over 64 experts with SwiGLU,
-    // K = 1024, 113 against 125.  At K = 14336 tiles change rarely, and dealing
-    // them as CUs come free is better: 527 against 539 us (8190 rows, 8 experts).
+    // while it finishes the last: 8192 x 8192 x 512 takes 66 us so, 74 with a
+    // workgroup for each tile, x 1024 93 and 99; 8000 rows over 64 experts with
+    // SwiGLU, K = 1024, 113 and 125.  At long K tiles change rarely, and dealing
+    // them as CUs come free is better where they differ: 527 against 539 us
+    // for 8190 rows over 8 experts, K = 14336.
     const int64_t steps = tiles_of(p.K, BK);
-    if (G == 1 && steps >= D && steps <= 64) grid = std::min<int64_t>(grid, kCUs * (160 * 1024 / kLds));
+    if (G == 1 && p.part != kRest && steps >= D && steps <= 64) grid = std::min<int64_t>(grid, kCUs * (160 * 1024 / kLds));
     else if (grid * kThreads > kMaxThreads) return Q4_EINVAL;
     if (to.report) {
         *to.report = {BM, SWI ? BW / 2 : BW, (int)grid, kThreads};
@@ -719,7 +747,8 @@ Kernel choose(const Args &p, int mats) {
     if (p.offsets) {
         const int64_t rows = tiles_of(p.M, p.E);
         if (rows <= 4) return rows <= 2 ? kFew8 : kFew16;
-        return p.K < BK ? kFew64 : rows <= 48 ? kTile64 : kTileWide;
+        if (p.K < BK) return kFew64;
+        return rows <= 48 ? kTile64 : rows < (p.K < 8192 ? 1536 : 256) ? kTileWide : kTile256;
     }
     if (p.M <= 32) return p.M <= 8 ? kFew8 : p.M <= 16 ? kFew16 : kFew32;
     if (p.K < BK) return kFew64;
@@ -735,7 +764,10 @@ Kernel choose(const Args &p, int mats) {
     cost[kTile64] = std::max(1.0, (double)tiles(64, 128) / kCUs * 1.2) * (0.67 + steps * 0.42);
     cost[kTile128] = each(tiles(128, 128), 2.25 + steps * 0.46, 0.63 + steps * 0.78);
     cost[kTileWide] = rounds(128, 256) * (6.54 + steps * 0.75);
-    cost[kTile256] = rounds(256, 256) * (8.0 + steps * 1.33);
+    const int64_t t256 = tiles(256, 256), left = t256 % kCUs;
+    const double halved = (double)((4 * left + kCUs - 1) / kCUs) * (2.25 + steps * 0.46);
+    cost[kTile256] = t256 < kCUs || left > kRestMost ? rounds(256, 256) * (8.0 + steps * 1.33)
+                                                     : (double)(t256 / kCUs) * (8.0 + steps * 1.33) + halved;
     Kernel best = kFew64;
     for (Kernel k : {kTileDeep, kTile64, kTile128, kTileWide, kTile256})
         if (cost[k] < cost[best]) best = k;
@@ -761,7 +793,16 @@ int launch(const Args &p, Kernel k, const Target &to) {
         if (alone(128, 128)) return launch_block<128, 128, 2, 4, 1, 4, SWI>(p, to);
         return launch_block<128, 128, 2, 4, 1, 2, SWI>(p, to);
     case kTileWide: return launch_block<128, 256, 2, 4, 1, 3, SWI>(p, to);
-    default: return launch_block<256, 256, 2, 4, 1, 2, SWI>(p, to);
+    default: {
+        // Whole rounds, then the tiles that are left, halved both ways.
+        Args q = p;
+        const int64_t all = row_tiles(p, 256) * tiles_of(p.N, SWI ? 128 : 256);
+        if (all >= kCUs && (p.offsets || whole_rounds((int)std::min<int64_t>(all, 0x7FFFFFFF)) < all)) q.part = kWhole;
+        if (int st = launch_block<256, 256, 2, 4, 1, 2, SWI>(q, to)) return st;
+        if (q.part == kAll || to.report) return Q4_OK;
+        q.part = kRest;
+        return launch_block<128, 128, 2, 4, 1, 4, SWI>(q, to);
+    }
     }
 }
 
@@ -792,14 +833,14 @@ int run(const Args &p, int mats, hipStream_t stream) {
 
 extern "C" int gemm_i8(const int8_t *a, const float *a_scales, const int8_t *w, const float *w_scales,
                        const float *bias, void *y, int y_type, int M, int N, int K, void *stream) {
-    return run({a, a_scales, {w, nullptr}, {w_scales, nullptr}, bias, nullptr, y, y_type, M, N, K, 1, 0, 0, false}, 1,
+    return run({a, a_scales, {w, nullptr}, {w_scales, nullptr}, bias, nullptr, y, y_type, M, N, K, 1, 0, 0, kAll, false}, 1,
                static_cast<hipStream_t>(stream));
 }
 
 extern "C" int gemm_i8_swiglu(const int8_t *a, const float *a_scales, const int8_t *w_gate,
                               const float *scales_gate, const int8_t *w_up, const float *scales_up, void *y,
                               int y_type, int M, int N, int K, void *stream) {
-    return run({a, a_scales, {w_gate, w_up}, {scales_gate, scales_up}, nullptr, nullptr, y, y_type, M, N, K, 1, 0, 0, false},
+    return run({a, a_scales, {w_gate, w_up}, {scales_gate, scales_up}, nullptr, nullptr, y, y_type, M, N, K, 1, 0, 0, kAll, false},
                2, static_cast<hipStream_t>(stream));
 }
 
@@ -807,7 +848,7 @@ extern "C" int gemm_i8_grouped(const int8_t *a, const float *a_scales, const int
                                const int32_t *offsets, void *y, int y_type, int M, int E, int N, int K,
                                void *stream) {
     if (!offsets && M > 0 && N > 0) return Q4_ENULL;
-    return run({a, a_scales, {w, nullptr}, {w_scales, nullptr}, nullptr, offsets, y, y_type, M, N, K, E, 0, 0, false}, 1,
+    return run({a, a_scales, {w, nullptr}, {w_scales, nullptr}, nullptr, offsets, y, y_type, M, N, K, E, 0, 0, kAll, false}, 1,
                static_cast<hipStream_t>(stream));
 }
 
@@ -816,7 +857,7 @@ extern "C" int gemm_i8_grouped_swiglu(const int8_t *a, const float *a_scales, co
                                       const int32_t *offsets, void *y, int y_type, int M, int E, int N, int K,
                                       void *stream) {
     if (!offsets && M > 0 && N > 0) return Q4_ENULL;
-    return run({a, a_scales, {w_gate, w_up}, {scales_gate, scales_up}, nullptr, offsets, y, y_type, M, N, K, E, 0, 0, false},
+    return run({a, a_scales, {w_gate, w_up}, {scales_gate, scales_up}, nullptr, offsets, y, y_type, M, N, K, E, 0, 0, kAll, false},
                2, static_cast<hipStream_t>(stream));
 }
 

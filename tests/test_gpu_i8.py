@@ -147,6 +147,45 @@ def test_swiglu_large(M, N, K):
     check(y, *i8.swiglu(a, sa, gate, up), "f16", f"{M} {N} {K}")
 
 
+def exact_rows(a, sa, w, sw):
+    """P in float64 on the GPU, where the sums are exact as in the oracle, for sizes too large for it."""
+    return (dev(a).double() @ dev(w).double().t()) * dev(sa).double()[:, None] * dev(sw).double()
+
+
+@pytest.mark.parametrize("M,N,K", [(4300, 4100, 2064), (4096, 5300, 2000), (8200, 4097, 1040)])
+@pytest.mark.parametrize("groups", [0, 3])
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_last_round_halved(M, N, K, groups, swiglu):
+    """A last round of few tiles, taken by halved ones, whose quarters may lie past the rows or columns."""
+    N = (N + 1) // 2 if swiglu else N
+    E = max(groups, 1)
+    K = K * 5 if groups else K                              # long enough for the largest tiles
+    off = [0, M // 2 - 3, M - 1500, M] if groups else [0, M]
+    a, sa = codes(1, M, K), small_scales(3, K, M)
+    gate, up = (codes(2, E, N, K), small_scales(4, K, E, N)), (codes(5, E, N, K), small_scales(6, K, E, N))
+    mats = 2 if swiglu else 1
+    g = q4.gemm_i8_geometry(mats, M, N, K, groups)
+    assert (g["tile_rows"], g["tile_cols"]) == (256, 256 // mats)
+    if groups:
+        o = torch.tensor(off, dtype=torch.int32, device=DEV)
+        y = (q4.gemm_i8_grouped_swiglu(dev(a), dev(sa), tuple(map(dev, gate)), tuple(map(dev, up)), o) if swiglu else
+             q4.gemm_i8_grouped(dev(a), dev(sa), *map(dev, gate), o))
+    else:
+        y = (q4.gemm_i8_swiglu(dev(a), dev(sa), (dev(gate[0][0]), dev(gate[1][0])), (dev(up[0][0]), dev(up[1][0])))
+             if swiglu else q4.gemm_i8(dev(a), dev(sa), dev(gate[0][0]), dev(gate[1][0])))
+    for e in range(E):
+        rows = slice(off[e], off[e + 1])
+        p = exact_rows(a[rows], sa[rows], gate[0][e], gate[1][e])
+        bound = 3.1 * i8.U * p.abs()
+        if swiglu:                                          # as i8.swiglu
+            u = exact_rows(a[rows], sa[rows], up[0][e], up[1][e])
+            s = p * torch.sigmoid(p)
+            ds = 1.1 * bound + s.abs() * (2 * p.abs() + 9) * i8.U
+            p, bound = s * u, 1.01 * (u.abs() * ds + s.abs() * 3.1 * i8.U * u.abs()) + u.abs() * 2.0 ** -118
+        tol = bound + 2.0 ** -24 * (p.abs() + bound)
+        assert ((y[rows].double() - p).abs() <= tol).all(), f"expert {e}"
+
+
 def test_sizes_take_every_tile():
     for mats, shapes, tiles in ((1, GEMM + LARGE, {(8,), (16,), (32,), (64, 32), (64, 64), (64, 128), (128, 128),
                                                    (128, 256), (256, 256)}),
