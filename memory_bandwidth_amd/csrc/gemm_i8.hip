@@ -741,18 +741,25 @@ enum Kernel { kFew8, kFew16, kFew32, kFew64, kTile64, kTile128, kTileWide, kTile
 // Groups go by their average rows, their sizes being known to the GPU alone.
 // Measured over 64 experts of 2 x 2816 x 1024, at 4, 32 and 128 rows each: 16
 // rows a tile 73, 133, - us, 64 rows 69, 82, 133, 128 rows 72, 90, 115, 256
-// rows 103, 119, 145.
+// rows 103, 119, 145.  Over 8 experts of 4096 x 14336, at 256 rows each:
+// 128 rows a tile 218 us, 256 rows 192; of 2 x 4096 x 4096, at 512 rows 168
+// and 174, at 2048 535 and 504.  Where that leaves CUs idle, the estimates
+// decide, a group ending inside a tile half way: 769 rows over 3 experts of
+// 643 x 3648 take 12.1 us in tiles of 64 x 64, 30.3 in 128 x 256.
 Kernel choose(const Args &p, int mats) {
-    const int64_t steps = tiles_of(p.K, BK);
-    if (p.offsets) {
-        const int64_t rows = tiles_of(p.M, p.E);
-        if (rows <= 4) return rows <= 2 ? kFew8 : kFew16;
-        if (p.K < BK) return kFew64;
-        return rows <= 48 ? kTile64 : rows < (p.K < 8192 ? 1536 : 256) ? kTileWide : kTile256;
-    }
-    if (p.M <= 32) return p.M <= 8 ? kFew8 : p.M <= 16 ? kFew16 : kFew32;
+    const int64_t steps = tiles_of(p.K, BK), groups = p.offsets ? std::min(p.E, p.M) : 0;
+    const int64_t rows = p.offsets ? tiles_of(p.M, p.E) : p.M;
+    if (p.offsets && rows <= 4) return rows <= 2 ? kFew8 : kFew16;
+    if (!p.offsets && rows <= 32) return rows <= 8 ? kFew8 : rows <= 16 ? kFew16 : kFew32;
     if (p.K < BK) return kFew64;
-    auto tiles = [&](int bm, int bw) { return tiles_of(p.M, bm) * tiles_of(p.N, bw / mats); };
+    auto tiles = [&](int bm, int bw) {
+        return (p.offsets ? p.M / bm + (groups + 1) / 2 : tiles_of(p.M, bm)) * tiles_of(p.N, bw / mats);
+    };
+    if (p.offsets) {
+        if (rows <= 48 && tiles(64, 128) >= kCUs) return kTile64;
+        if (rows > 48 && rows < (p.K < 8192 ? 1536 : 256) && tiles(128, 256) >= kCUs) return kTileWide;
+        if (rows >= (p.K < 8192 ? 1536 : 256) && tiles(256, 256) >= kCUs) return kTile256;
+    }
     auto rounds = [&](int bm, int bw) { return (double)((tiles(bm, bw) + kCUs - 1) / kCUs); };
     // Tiles a CU, 1 where there are fewer, and the time of one alone or of one among others.
     auto each = [&](int64_t t, double one, double many) { return t <= kCUs ? one : (double)t / kCUs * many; };
@@ -768,9 +775,9 @@ Kernel choose(const Args &p, int mats) {
     const double halved = (double)((4 * left + kCUs - 1) / kCUs) * (2.25 + steps * 0.46);
     cost[kTile256] = t256 < kCUs || left > kRestMost ? rounds(256, 256) * (8.0 + steps * 1.33)
                                                      : (double)(t256 / kCUs) * (8.0 + steps * 1.33) + halved;
-    Kernel best = kFew64;
-    for (Kernel k : {kTileDeep, kTile64, kTile128, kTileWide, kTile256})
-        if (cost[k] < cost[best]) best = k;
+    Kernel best = kTileDeep;
+    for (Kernel k : {kFew64, kTile64, kTile128, kTileWide, kTile256})
+        if (cost[k] < cost[best] && !(p.offsets && k == kFew64)) best = k;
     return best;
 }
 
