@@ -681,8 +681,10 @@ int launch_few(Args p, const Target &to) {
     // non-temporally.  Cycling 2 GB of matrices, one row through 4096 -> 14336
     // (59 MB) takes 12.6 us so and 14.2 without, the SwiGLU of two such 24.0
     // and 26.3; but a small model's matrices can be found in the cache, and
-    // three of 59 MB in turn take 11.8 us so and 10.7 without.
-    p.once = (int64_t)(SWI ? 2 : 1) * p.E * p.N * p.K > (int64_t)64 << 20;
+    // three of 59 MB in turn take 11.8 us so and 10.7 without.  Rows that do not
+    // start on a 64-byte border share lines with their neighbours, which the
+    // caches have to keep: 8 rows, 2 x 4080 -> 14336, 29.3 us so, 27.8 without.
+    p.once = p.K % 64 == 0 && (int64_t)(SWI ? 2 : 1) * p.E * p.N * p.K > (int64_t)64 << 20;
     // Wavefronts on one strip's K: as many as it takes for 1536 wavefronts,
     // 6 for each CU, while each has a unit.  At 8 rows, 4096 -> 14336, 2 of
     // them take 11.8 us and 8 take 13.6; at 24 rows, 14336 -> 4096, 8 take
