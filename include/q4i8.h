@@ -26,7 +26,7 @@
  * Sizes: K a multiple of 16 with 16 <= K <= 131056 (the exact sum then fits
  * int32 whatever the codes); 0 <= M, N <= 2^24 with at most 2^31 - 1 tiles of
  * 16 x 16 (and no launch of 2^32 threads or more, which M N beyond about
- * 10^10 would need: Q4_EINVAL); M == 0 or N == 0 returns Q4_OK with nothing
+ * 10^9 can need, 10^10 without groups: Q4_EINVAL); M == 0 or N == 0 returns Q4_OK with nothing
  * launched, before any pointer check.  a and w 16-byte aligned, scales, bias
  * and offsets 4-byte aligned, outputs aligned to their element.  Outputs must
  * not overlap any input.

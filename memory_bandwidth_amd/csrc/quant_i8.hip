@@ -76,7 +76,8 @@ __device__ __forceinline__ uint32_t codes4(const float *v, float s, float inv) {
             if (over > 0.0 || (over == 0.0 && ((int)n & 1))) t[i] += (uint32_t)(int)to;
         }
     }
-    const uint32_t lo = __builtin_amdgcn_perm(t[1], t[0], 0x0C0C0400u), hi = __builtin_amdgcn_perm(t[3], t[2], 0x0C0C0400u);
+    const uint32_t lo = __builtin_amdgcn_perm(t[1], t[0], 0x0C0C0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(t[3], t[2], 0x0C0C0400u);
     return lo | hi << 16;
 }
 
