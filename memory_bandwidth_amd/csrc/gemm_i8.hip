@@ -44,6 +44,7 @@ struct Args {
     int tiles_m, tiles_n;      // kRest: of the tiles that are halved
     Part part;
     bool once;                 // the weights' stream is more than a cache would keep
+    bool share;                // several row tiles read the same weights
 };
 
 // The fragment of 16 weight rows j (of F that share a run of 16 F rows) takes
@@ -220,16 +221,20 @@ __device__ __forceinline__ void finish(const Args &p, const i32x4_t (&acc)[FM][S
     }
 }
 
+// Workgroups are dealt to the eight XCDs in turn, each with its own L2: XCD x
+// takes the x-th eighth of the tiles (of those that the groups have, not of
+// those that they might have needed).  -1: workgroup b has none.
+__device__ __forceinline__ int eighth_of(int b, int all) {
+    const int x = b & 7, per = all >> 3, more = all & 7;
+    return (b >> 3) < per + (x < more ? 1 : 0) ? x * per + min(x, more) + (b >> 3) : -1;
+}
+
 // The tile (tm, tn) that a workgroup takes, of tiles_m rows of them; false:
-// none.  Workgroups are dealt to the eight XCDs in turn, each with its own L2:
-// XCD x takes the x-th eighth of the tiles (of those that the groups have, not
-// of those that they might have needed), and tiles are ordered in bands of
-// eight tile rows, column by column, so that the tiles an XCD runs at one
-// time share rows of a and of w.
+// none.  Tiles are ordered in bands of eight tile rows, column by column, so
+// that the tiles an XCD runs at one time share rows of a and of w.
 __device__ __forceinline__ bool tile_of(int b, int tiles_m, int tiles_n, int &tm, int &tn) {
-    const int all = tiles_m * tiles_n, x = b & 7, per = all >> 3, more = all & 7;
-    if ((b >> 3) >= per + (x < more ? 1 : 0)) return false;
-    const int t = x * per + min(x, more) + (b >> 3);
+    const int t = eighth_of(b, tiles_m * tiles_n);
+    if (t < 0) return false;
     const int band = t / (8 * tiles_n), first = band * 8, rows = min(8, tiles_m - first);
     const int in = t - band * 8 * tiles_n;
     tm = first + in % rows;
@@ -538,8 +543,8 @@ __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_i8_block(Args p) {
 
 // ---------------------------------------------------------------- few rows
 //
-// Up to 8 NX rows: the weights are streamed once, and what counts is the
-// bytes in flight.  A wavefront takes FN strips of 16 weight rows (of each
+// Tiles of 8 NX rows: what counts is the bytes in flight, and that every CU
+// has its share of them.  A wavefront takes a strip of 16 weight rows (of each
 // matrix) and every KS-th unit of 128 bytes of K; KS wavefronts of a
 // workgroup meet in LDS at the end.  Its units pass through a ring of D
 // slots of its own in LDS, loaded straight from memory eight rows of 128
@@ -547,19 +552,33 @@ __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_i8_block(Args p) {
 // the same bytes at 3/4 of the rate or less), the next unit issued as soon
 // as a slot has been read: no barrier, and D - 1 units in flight while one
 // is multiplied.  Units past K repeat the row's last 16 bytes against
-// activations of zero.
-template <int NX, int FN, bool SWI, int W, int D>
+// activations of zero.  Up to a few hundred rows, where larger tiles leave
+// CUs idle, many such tiles are faster although each reads all its operands:
+// 64 x 2048 x 8192 takes 10.0 us in tiles of 32 rows, 21.7 in 64 x 64, 1024
+// columns of 4096 5.8 and 9.3.
+constexpr int kFewDepth = 2;
+
+template <int NX, bool SWI, int W>
 __global__ __launch_bounds__(W * 64) void gemm_i8_few(Args p, int ks_log2) {
-    constexpr int FM = (NX + 1) / 2, BM = 8 * NX, MATS = SWI ? 2 : 1, FW = FN * MATS;
-    constexpr int LOADS = 2 * FW + NX;             // load instructions of a unit
-    constexpr int SLOT = (2 * FW + 2 * FM) * 1024; // whole fragments, the last may be half loaded
+    constexpr int FM = (NX + 1) / 2, BM = 8 * NX, FW = SWI ? 2 : 1;       // FW: a fragment of each matrix
+    constexpr int D = kFewDepth, LOADS = 2 * FW + NX;                       // load instructions of a unit
+    constexpr int SLOT = (2 * FW + 2 * FM) * 1024;                          // whole fragments, the last may be half loaded
     extern __shared__ __align__(16) char lds[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int KS = 1 << ks_log2, ks = wave & (KS - 1);
-    const int tn = (int)(blockIdx.x % p.tiles_n);
-    const Tile tl = find_tile(p, BM, tiles_upto(p, BM), (int)(blockIdx.x / p.tiles_n));
+    // Row tiles that read the same weights lie side by side on one XCD, so that
+    // its L2 brings them once; others take the XCDs in turn.
+    const int upto = tiles_upto(p, BM);
+    int tm = (int)blockIdx.x / p.tiles_n, tn = (int)blockIdx.x - tm * p.tiles_n;
+    if (p.share) {
+        const int tiles_m = tile_count(p, upto), id = eighth_of(blockIdx.x, tiles_m * p.tiles_n);
+        if (id < 0) return;
+        tn = id / tiles_m;
+        tm = id - tn * tiles_m;
+    }
+    const Tile tl = find_tile(p, BM, upto, tm);
     if (tl.rows <= 0) return;
-    const int n0 = (tn * (W >> ks_log2) + (wave >> ks_log2)) * (16 * FN);
+    const int n0 = (tn * (W >> ks_log2) + (wave >> ks_log2)) * 16;
     const size_t mat = (size_t)tl.e * p.N;
     const int kc = p.K >> 4, units = (kc + 7) >> 3;
     const int g = lane >> 4, r = lane & 15;
@@ -567,28 +586,25 @@ __global__ __launch_bounds__(W * 64) void gemm_i8_few(Args p, int ks_log2) {
 
     if (n0 < p.N) {
         char *ring = lds + wave * (D * SLOT);
-        const int cols = min(16 * FN, p.N - n0);
+        const int cols = min(16, p.N - n0);
         const __amdgpu_buffer_rsrc_t rx = rsrc_of(p.a + (size_t)tl.m0 * p.K, (uint32_t)tl.rows * p.K);
-        __amdgpu_buffer_rsrc_t rw[MATS];
+        __amdgpu_buffer_rsrc_t rw[FW];
 #pragma unroll
-        for (int s = 0; s < MATS; ++s) rw[s] = rsrc_of(p.w[s] + (mat + n0) * p.K, (uint32_t)cols * p.K);
-        uint32_t vx[NX], vw[2 * FN];
+        for (int s = 0; s < FW; ++s) rw[s] = rsrc_of(p.w[s] + (mat + n0) * p.K, (uint32_t)cols * p.K);
+        uint32_t vx[NX], vw[2];
 #pragma unroll
         for (int i = 0; i < NX; ++i) vx[i] = (uint32_t)min(i * 8 + (lane >> 3), tl.rows - 1) * p.K;
 #pragma unroll
-        for (int i = 0; i < 2 * FN; ++i) {
-            const int q = (i & 1) * 8 + (lane >> 3);               // row of fragment i / 2
-            vw[i] = (uint32_t)min(frag_row<FN>(i >> 1, q), cols - 1) * p.K;
-        }
+        for (int i = 0; i < 2; ++i) vw[i] = (uint32_t)min(i * 8 + (lane >> 3), cols - 1) * p.K;
         const int chunk = (lane & 7) ^ (lane >> 3);
         auto load = [&](int slot, int u) {
             char *at = ring + slot * SLOT;
             const uint32_t k = (uint32_t)min(u * 8 + chunk, kc - 1) << 4;
 #pragma unroll
-            for (int s = 0; s < MATS; ++s)
+            for (int s = 0; s < FW; ++s)
 #pragma unroll
-                for (int i = 0; i < 2 * FN; ++i) {
-                    char *to = at + (s * 2 * FN + i) * 1024;
+                for (int i = 0; i < 2; ++i) {
+                    char *to = at + (s * 2 + i) * 1024;
                     if (p.once) load16<true>(rw[s], to, vw[i] + k, 0);
                     else load16(rw[s], to, vw[i] + k, 0);
                 }
@@ -630,9 +646,7 @@ __global__ __launch_bounds__(W * 64) void gemm_i8_few(Args p, int ks_log2) {
             if (++slot == D) slot = 0;
         }
         for (; left > 0; --left, u += KS) {
-            if (D > 3 && left == 4) wait_loads<3 * LOADS>();
-            else if (D > 2 && left == 3) wait_loads<2 * LOADS>();
-            else if (left == 2) wait_loads<LOADS>();
+            if (left == 2) wait_loads<LOADS>();
             else wait_loads<0>();
             products(slot, u);
             if (++slot == D) slot = 0;
@@ -656,14 +670,14 @@ __global__ __launch_bounds__(W * 64) void gemm_i8_few(Args p, int ks_log2) {
 #pragma unroll
                 for (int j = 0; j < FW; ++j) acc[i][j] += part[((wave + k) * FM * FW + i * FW + j) * 64];
     }
-    constexpr int C = 4 * FN;
+    constexpr int C = 4;
     const int n = n0 + g * C;
-    float sw[MATS][C];
+    float sw[FW][C];
 #pragma unroll
-    for (int s = 0; s < MATS; ++s)
+    for (int s = 0; s < FW; ++s)
 #pragma unroll
         for (int c = 0; c < C; ++c) sw[s][c] = n + c < p.N ? p.sw[s][mat + n + c] : 0.f;
-    finish<FM, C, SWI>(p, acc, tl, p.sa + tl.m0, sw[0], sw[MATS - 1], 0, n, lane);
+    finish<FM, C, SWI>(p, acc, tl, p.sa + tl.m0, sw[0], sw[FW - 1], 0, n, lane);
 }
 
 constexpr int kMaxRows = 1 << 24;
@@ -684,10 +698,26 @@ int64_t row_tiles(const Args &p, int bm) {
 struct Report { int rows, cols, grid, block; };
 struct Target { hipStream_t stream; Report *report; };
 
-template <int NX, int FN, bool SWI, int W>
-int launch_few(Args p, const Target &to) {
-    constexpr int FM = (NX + 1) / 2, FW = FN * (SWI ? 2 : 1), D = 2;
-    const int64_t tiles_m = row_tiles(p, 8 * NX), strips = tiles_of(p.N, 16 * FN), units = tiles_of(p.K, BK);
+// Wavefronts on one strip's K (log2) and in a workgroup of a few-rows kernel
+// of bm rows.  As many share K as it takes for 1536 wavefronts, 6 for each CU,
+// while each has a unit: at 8 rows, 4096 -> 14336, 2 of them take 11.8 us and
+// 8 take 13.6; at 24 rows, 14336 -> 4096, 8 take 12.0 and 2 take 26.1.
+// Workgroups of 4 are spread more evenly than of 8: at 31 rows, 3840 -> 8512,
+// 10.5 and 12.9 us; but 8 are as good where they come to no more than one a
+// CU, and then 14.1 against 14.6 us at 16 rows, 4096 -> 14336.
+struct Split { int64_t tiles, strips; int log2, waves; };
+Split split_of(const Args &p, int bm) {
+    Split s = {row_tiles(p, bm), tiles_of(p.N, 16), 0, 8};
+    const int64_t units = tiles_of(p.K, BK);
+    while (s.log2 < 3 && (units >> s.log2) > 1 && (s.tiles * s.strips) << s.log2 < 1536) ++s.log2;
+    const int64_t eights = s.tiles * tiles_of(s.strips, 8 >> s.log2);
+    if (s.log2 < 3 && (eights < kCUs / 2 || eights > kCUs)) s.waves = 4;
+    return s;
+}
+
+template <int NX, bool SWI, int W>
+int launch_few(Args p, const Split &s, const Target &to) {
+    constexpr int FM = (NX + 1) / 2, FW = SWI ? 2 : 1, kLds = W * kFewDepth * (2 * FW + 2 * FM) * 1024;
     // Weights of more than a quarter of the 256 MB cache are loaded
     // non-temporally.  Cycling 2 GB of matrices, one row through 4096 -> 14336
     // (59 MB) takes 12.6 us so and 14.2 without, the SwiGLU of two such 24.0
@@ -695,23 +725,25 @@ int launch_few(Args p, const Target &to) {
     // three of 59 MB in turn take 11.8 us so and 10.7 without.  Rows that do not
     // start on a 64-byte border share lines with their neighbours, which the
     // caches have to keep: 8 rows, 2 x 4080 -> 14336, 29.3 us so, 27.8 without.
-    p.once = p.K % 64 == 0 && (int64_t)(SWI ? 2 : 1) * p.E * p.N * p.K > (int64_t)64 << 20;
-    // Wavefronts on one strip's K: as many as it takes for 1536 wavefronts,
-    // 6 for each CU, while each has a unit.  At 8 rows, 4096 -> 14336, 2 of
-    // them take 11.8 us and 8 take 13.6; at 24 rows, 14336 -> 4096, 8 take
-    // 12.0 and 2 take 26.1.
-    int log2 = 0;
-    while ((2 << log2) <= W && (units >> log2) > 1 && (tiles_m * strips) << log2 < 1536) ++log2;
-    p.tiles_m = (int)tiles_m;
-    p.tiles_n = (int)tiles_of(strips, W >> log2);
-    const int64_t grid = tiles_m * p.tiles_n;
+    // Weights that several row tiles read are to be kept, too.
+    p.share = p.offsets ? p.M > (int64_t)p.E * (8 * NX) : s.tiles > 1;
+    p.once = p.K % 64 == 0 && !p.share && (int64_t)(SWI ? 2 : 1) * p.E * p.N * p.K > (int64_t)64 << 20;
+    p.tiles_m = (int)s.tiles;
+    p.tiles_n = (int)tiles_of(s.strips, W >> s.log2);
+    const int64_t grid = s.tiles * p.tiles_n;
     if (grid * (W * 64) > kMaxThreads) return Q4_EINVAL;
     if (to.report) {
-        *to.report = {8 * NX, (W >> log2) * 16 * FN, (int)grid, W * 64};
+        *to.report = {8 * NX, (W >> s.log2) * 16, (int)grid, W * 64};
         return Q4_OK;
     }
-    gemm_i8_few<NX, FN, SWI, W, D><<<(unsigned)grid, W * 64, W * D * (2 * FW + 2 * FM) * 1024, to.stream>>>(p, log2);
+    gemm_i8_few<NX, SWI, W><<<(unsigned)grid, W * 64, kLds, to.stream>>>(p, s.log2);
     return q4::launch_status();
+}
+
+template <int NX, bool SWI>
+int launch_few(const Args &p, const Target &to) {
+    const Split s = split_of(p, 8 * NX);
+    return s.waves == 8 ? launch_few<NX, SWI, 8>(p, s, to) : launch_few<NX, SWI, 4>(p, s, to);
 }
 
 template <int BM, int BW, int WM, int WN, int G, int D, bool SWI>
@@ -743,15 +775,18 @@ int launch_block(Args p, const Target &to) {
     return q4::launch_status();
 }
 
-enum Kernel { kFew8, kFew16, kFew32, kFew64, kTile64, kTile128, kTileWide, kTile256, kTileDeep, kKernels };
+enum Kernel { kFew8, kFew16, kFew32, kTile64, kTile128, kTileWide, kTile256, kTileDeep, kKernels };
 
-// The kernel for a call's sizes.  Up to 32 rows the weights' stream decides.
-// Above that, each kernel's time is estimated from its tiles and steps, with
-// constants fitted to 320 measured shapes (33 to 8192 rows, N 64 to 14336, K
-// 256 to 14336, one matrix and two; the choice is on average 0.6% behind the
-// best of the six measured, at most 29%): us a tile, us a step, and how far
-// more tiles than CUs stretch it.  Tiles that have a CU to themselves come in
-// whole rounds.
+// The kernel for a call's sizes.  Up to 8 rows the weights' stream decides.
+// Above that, each kernel's time is estimated, with constants fitted to
+// measured shapes: the tiles to 320 (33 to 8192 rows, N 64 to 14336, K 256 to
+// 14336, one matrix and two), in us a tile, us a step, and how far more tiles
+// than CUs stretch it; tiles that have a CU to themselves come in whole rounds.
+// The kernels of few rows to 550 (9 to 3000 rows): us a unit of a wavefront
+// alone and for each of the CU's, and, as they read weights past the L2 again
+// for every row tile, us a MB of weights.  The choice is on average 1.4%
+// behind the best of the seven there, at most 30%.  With 64 x 4096 x 14336 as
+// an example, 32 rows a workgroup take 21.2 us, 64 x 64 tiles 37.
 // Groups go by their average rows, their sizes being known to the GPU alone.
 // Measured over 64 experts of 2 x 2816 x 1024, at 4, 32 and 128 rows each: 16
 // rows a tile 73, 133, - us, 64 rows 69, 82, 133, 128 rows 72, 90, 115, 256
@@ -759,28 +794,39 @@ enum Kernel { kFew8, kFew16, kFew32, kFew64, kTile64, kTile128, kTileWide, kTile
 // 128 rows a tile 218 us, 256 rows 192; of 2 x 4096 x 4096, at 512 rows 168
 // and 174, at 2048 535 and 504.  Where that leaves CUs idle, the estimates
 // decide, a group ending inside a tile half way: 769 rows over 3 experts of
-// 643 x 3648 take 12.1 us in tiles of 64 x 64, 30.3 in 128 x 256.
+// 643 x 3648 take 12.1 us in tiles of 64 x 64, 30.3 in 128 x 256.  Over 220
+// calls (2 to 128 experts, 0.5 to 300 rows each) the choice is on average 2.7%
+// behind the best.
 Kernel choose(const Args &p, int mats) {
     const int64_t steps = tiles_of(p.K, BK), groups = p.offsets ? std::min(p.E, p.M) : 0;
     const int64_t rows = p.offsets ? tiles_of(p.M, p.E) : p.M;
-    if (p.offsets && rows <= 4) return rows <= 2 ? kFew8 : kFew16;
-    if (!p.offsets && rows <= 32) return rows <= 8 ? kFew8 : rows <= 16 ? kFew16 : kFew32;
-    if (p.K < BK) return kFew64;
-    auto tiles = [&](int bm, int bw) {
-        return (p.offsets ? p.M / bm + (groups + 1) / 2 : tiles_of(p.M, bm)) * tiles_of(p.N, bw / mats);
-    };
+    if (rows <= (p.offsets ? 2 : 8)) return kFew8;
+    if ((p.offsets && rows <= 8) || (p.K < BK && rows <= 16)) return kFew16;
+    if (p.K < BK) return kFew32;
+    auto row_tiles_likely = [&](int bm) { return p.offsets ? p.M / bm + (groups + 1) / 2 : tiles_of(p.M, bm); };
+    auto tiles = [&](int bm, int bw) { return row_tiles_likely(bm) * tiles_of(p.N, bw / mats); };
     if (p.offsets) {
+        const int many = p.K < 8192 ? 1536 : 256;
         if (rows <= 48 && tiles(64, 128) >= kCUs) return kTile64;
-        if (rows > 48 && rows < (p.K < 8192 ? 1536 : 256) && tiles(128, 256) >= kCUs) return kTileWide;
-        if (rows >= (p.K < 8192 ? 1536 : 256) && tiles(256, 256) >= kCUs) return kTile256;
+        if (rows > 48 && rows < many && tiles(128, 256) >= 2 * kCUs) return kTileWide;
+        if (rows >= many && tiles(256, 256) >= kCUs) return kTile256;
     }
     auto rounds = [&](int bm, int bw) { return (double)((tiles(bm, bw) + kCUs - 1) / kCUs); };
     // Tiles a CU, 1 where there are fewer, and the time of one alone or of one among others.
     auto each = [&](int64_t t, double one, double many) { return t <= kCUs ? one : (double)t / kCUs * many; };
-    const double few = tiles(64, 32);
-    const int ks = few < 384 ? 4 : few < 768 ? 2 : 1;            // as launch_few's rule
+    auto few = [&](int bm, double start, double unit, double shared, double first) {
+        const Split s = split_of(p, bm);
+        const int64_t tm = row_tiles_likely(bm), wgs = tm * tiles_of(s.strips, s.waves >> s.log2);
+        const double a_unit = std::max(unit, shared * (double)(tiles_of(wgs, kCUs) * s.waves));
+        const double mb = p.offsets ? 0. : (double)mats * p.N * p.K * 1e-6;
+        return std::max(start + a_unit * (first + (double)tiles_of(steps, 1 << s.log2)),
+                        0.32 * mb * (1. + 0.4 * (double)(tm - 1)) - 1.5);
+    };
+    const bool two = mats == 2;
     double cost[kKernels];
-    cost[kFew64] = std::max(1.0, few * ks / (4 * kCUs) * 1.49) * (1.85 + (double)tiles_of(steps, ks) * 0.93);
+    cost[kFew8] = few(8, -0.5, 0.15, two ? 0.050 : 0.031, 0.81);
+    cost[kFew16] = few(16, -0.7, 0.24, two ? 0.099 : 0.043, 0.5);
+    cost[kFew32] = few(32, -0.4, 0.30, two ? 0.154 : 0.11, 0.74);
     cost[kTileDeep] = each(tiles(64, 64), 0.67 + steps * 0.38, 0.78 + steps * 0.40);
     cost[kTile64] = std::max(1.0, (double)tiles(64, 128) / kCUs * 1.2) * (0.67 + steps * 0.42);
     cost[kTile128] = each(tiles(128, 128), 2.25 + steps * 0.46, 0.63 + steps * 0.78);
@@ -789,9 +835,9 @@ Kernel choose(const Args &p, int mats) {
     const double halved = (double)((4 * left + kCUs - 1) / kCUs) * (2.25 + steps * 0.46);
     cost[kTile256] = t256 < kCUs || left > kRestMost ? rounds(256, 256) * (8.0 + steps * 1.33)
                                                      : (double)(t256 / kCUs) * (8.0 + steps * 1.33) + halved;
-    Kernel best = kTileDeep;
-    for (Kernel k : {kFew64, kTile64, kTile128, kTileWide, kTile256})
-        if (cost[k] < cost[best] && !(p.offsets && k == kFew64)) best = k;
+    Kernel best = kFew16;
+    for (Kernel k : {kFew8, kFew32, kTileDeep, kTile64, kTile128, kTileWide, kTile256})
+        if (cost[k] < cost[best] && !(p.offsets && k == kFew8)) best = k;
     return best;
 }
 
@@ -802,10 +848,9 @@ int launch(const Args &p, Kernel k, const Target &to) {
     // us, but 1999 x 14336 x 4096 in 128 against 112 (tiles of 128 x 128).
     auto alone = [&](int bm, int bw) { return row_tiles(p, bm) * tiles_of(p.N, SWI ? bw / 2 : bw) <= kCUs; };
     switch (k) {
-    case kFew8: return launch_few<1, 1, SWI, 8>(p, to);
-    case kFew16: return launch_few<2, 1, SWI, 8>(p, to);
-    case kFew32: return launch_few<4, 1, SWI, 8>(p, to);
-    case kFew64: return launch_few<8, SWI ? 1 : 2, SWI, 4>(p, to);
+    case kFew8: return launch_few<1, SWI>(p, to);
+    case kFew16: return launch_few<2, SWI>(p, to);
+    case kFew32: return launch_few<4, SWI>(p, to);
     case kTile64: return launch_block<64, 128, 2, 4, 1, 3, SWI>(p, to);
     case kTileDeep:
         if (alone(64, 64)) return launch_block<64, 64, 2, 2, 2, 4, SWI>(p, to);
@@ -855,7 +900,7 @@ int run(const Args &p, int mats, hipStream_t stream) {
 extern "C" int gemm_i8(const int8_t *a, const float *a_scales, const int8_t *w, const float *w_scales,
                        const float *bias, void *y, int y_type, int M, int N, int K, void *stream) {
     return run({a, a_scales, {w, nullptr}, {w_scales, nullptr}, bias, nullptr, y,
-                y_type, M, N, K, 1, 0, 0, kAll, false},
+                y_type, M, N, K, 1, 0, 0, kAll, false, false},
                1, static_cast<hipStream_t>(stream));
 }
 
@@ -863,7 +908,7 @@ extern "C" int gemm_i8_swiglu(const int8_t *a, const float *a_scales, const int8
                               const float *scales_gate, const int8_t *w_up, const float *scales_up, void *y,
                               int y_type, int M, int N, int K, void *stream) {
     return run({a, a_scales, {w_gate, w_up}, {scales_gate, scales_up}, nullptr, nullptr, y,
-                y_type, M, N, K, 1, 0, 0, kAll, false},
+                y_type, M, N, K, 1, 0, 0, kAll, false, false},
                2, static_cast<hipStream_t>(stream));
 }
 
@@ -872,7 +917,7 @@ extern "C" int gemm_i8_grouped(const int8_t *a, const float *a_scales, const int
                                void *stream) {
     if (!offsets && M > 0 && N > 0) return Q4_ENULL;
     return run({a, a_scales, {w, nullptr}, {w_scales, nullptr}, nullptr, offsets, y,
-                y_type, M, N, K, E, 0, 0, kAll, false},
+                y_type, M, N, K, E, 0, 0, kAll, false, false},
                1, static_cast<hipStream_t>(stream));
 }
 
@@ -882,7 +927,7 @@ extern "C" int gemm_i8_grouped_swiglu(const int8_t *a, const float *a_scales, co
                                       void *stream) {
     if (!offsets && M > 0 && N > 0) return Q4_ENULL;
     return run({a, a_scales, {w_gate, w_up}, {scales_gate, scales_up}, nullptr, offsets, y,
-                y_type, M, N, K, E, 0, 0, kAll, false},
+                y_type, M, N, K, E, 0, 0, kAll, false, false},
                2, static_cast<hipStream_t>(stream));
 }
 

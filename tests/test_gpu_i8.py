@@ -126,9 +126,11 @@ def test_gemm(M, N, K, t):
 # Every tile that the products choose from, with rows and columns that end
 # inside tiles and K inside steps, and more tiles than workgroups.
 LARGE = [(64, 4100, 2064), (500, 2050, 2064), (330, 4870, 912), (1090, 5000, 528), (3775, 1827, 1056),
-         (3984, 3781, 656), (2900, 5050, 528), (4100, 4100, 272), (5000, 300, 4112)]
+         (3984, 3781, 656), (2900, 5050, 528), (4100, 4100, 272), (5000, 300, 4112), (64, 3999, 4112),
+         (230, 3313, 400), (36, 1373, 32)]
 LARGE_SWIGLU = [(64, 2100, 2064), (300, 1000, 2064), (200, 2320, 912), (1060, 2500, 528), (2593, 1533, 800),
-                (2365, 3095, 432), (1500, 4100, 400)]
+                (2365, 3095, 432), (1500, 4100, 400), (96, 999, 4112), (67, 3422, 368), (40, 1100, 1040),
+                (40, 499, 8208), (40, 1373, 48)]
 
 
 @pytest.mark.parametrize("M,N,K", LARGE)
@@ -187,12 +189,14 @@ def test_last_round_halved(M, N, K, groups, swiglu):
 
 
 def test_sizes_take_every_tile():
-    for mats, shapes, tiles in ((1, GEMM + LARGE, {(8,), (16,), (32,), (64, 32), (64, 64), (64, 128), (128, 128),
-                                                   (128, 256), (256, 256)}),
-                                (2, LARGE_SWIGLU, {(64, 16), (64, 32), (64, 64), (128, 64), (128, 128), (256, 128)})):
+    for mats, shapes, tiles in ((1, GEMM + LARGE, {(8,), (16,), (32,), (64, 64), (64, 128), (128, 128), (128, 256),
+                                                   (256, 256)}),
+                                (2, LARGE_SWIGLU, {(8,), (16,), (32,), (64, 32), (64, 64), (128, 64), (128, 128),
+                                                    (256, 128)})):
         got = [q4.gemm_i8_geometry(mats, *s) for s in shapes]
         seen = {(g["tile_rows"], g["tile_cols"]) for g in got} | {(g["tile_rows"],) for g in got}
         assert tiles <= seen, tiles - seen
+        assert {g["block"] for g in got if g["tile_rows"] <= 32} == {256, 512}
         # Both kinds of launch: a workgroup for each tile, and workgroups that go through several.
         many = [g["grid"] < -(-s[0] // g["tile_rows"]) * -(-s[1] // g["tile_cols"]) for g, s in zip(got, shapes)]
         assert any(many) and not all(many)

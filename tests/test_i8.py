@@ -118,10 +118,11 @@ def test_binding_refuses_host_tensors_and_wrong_types():
 
 # Shapes (matrices, M, N, K, groups) and the tile of y that they take.
 PLANS = [((1, 1, 14336, 4096, 0), (8, 64)), ((1, 12, 4096, 4096, 0), (16, 16)), ((1, 24, 4096, 14336, 0), (32, 16)),
-         ((1, 64, 4096, 14336, 0), (64, 32)), ((1, 512, 2048, 2048, 0), (64, 64)), ((1, 333, 4864, 896, 0), (64, 128)),
+         ((1, 64, 4096, 14336, 0), (32, 32)), ((1, 64, 1024, 4096, 0), (16, 16)),
+         ((1, 512, 2048, 2048, 0), (64, 64)), ((1, 333, 4864, 896, 0), (64, 128)),
          ((1, 1024, 14336, 512, 0), (128, 128)), ((1, 3775, 1826, 1056, 0), (128, 256)),
          ((1, 8192, 14336, 4096, 0), (256, 256)), ((2, 8192, 14336, 4096, 0), (256, 128)),
-         ((2, 200, 2816, 1024, 64), (16, 128)), ((2, 900, 2816, 1024, 64), (64, 64)),
+         ((2, 200, 2816, 1024, 64), (16, 64)), ((2, 900, 2816, 1024, 64), (64, 64)),
          ((2, 8000, 2816, 1024, 64), (128, 128))]
 
 
