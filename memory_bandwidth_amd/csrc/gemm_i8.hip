@@ -560,9 +560,9 @@ constexpr int kFewDepth = 2;
 
 template <int NX, bool SWI, int W>
 __global__ __launch_bounds__(W * 64) void gemm_i8_few(Args p, int ks_log2) {
-    constexpr int FM = (NX + 1) / 2, BM = 8 * NX, FW = SWI ? 2 : 1;       // FW: a fragment of each matrix
-    constexpr int D = kFewDepth, LOADS = 2 * FW + NX;                       // load instructions of a unit
-    constexpr int SLOT = (2 * FW + 2 * FM) * 1024;                          // whole fragments, the last may be half loaded
+    constexpr int FM = (NX + 1) / 2, BM = 8 * NX, FW = SWI ? 2 : 1;     // FW: a fragment of each matrix
+    constexpr int D = kFewDepth, LOADS = 2 * FW + NX;                   // load instructions of a unit
+    constexpr int SLOT = (2 * FW + 2 * FM) * 1024;                      // whole fragments, the last may be half loaded
     extern __shared__ __align__(16) char lds[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int KS = 1 << ks_log2, ks = wave & (KS - 1);
