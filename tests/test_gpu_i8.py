@@ -441,6 +441,24 @@ def test_a_row_does_not_depend_on_the_batch(M):
     assert torch.equal(q4.gemm_i8_grouped(a[:M], sa[:M], w[None], sw[None], o), whole[:M])
 
 
+@pytest.mark.parametrize("t", TYPES)
+def test_epilogues_do_not_depend_on_the_batch(t):
+    """Scales, bias and silu are the same steps in every kernel: 2600 rows, their first ones, and groups of them."""
+    R, N, K = 2600, 1500, 528
+    a, sa = dev(codes(1, R, K)), dev(small_scales(3, K, R))
+    gate = dev(codes(2, N, K)), dev(small_scales(4, K, N) * 4)
+    up = dev(codes(5, N, K)), dev(small_scales(6, K, N))
+    bias = torch.linspace(-2, 2, N, device=DEV)
+    y = q4.gemm_i8(a, sa, *gate, bias=bias, dtype=TYPES[t])
+    h = q4.gemm_i8_swiglu(a, sa, gate, up, dtype=TYPES[t])
+    for M in (1, 12, 30, 70, 150, 330, 700, 1300):
+        assert torch.equal(q4.gemm_i8(a[:M], sa[:M], *gate, bias=bias, dtype=TYPES[t]), y[:M]), M
+        assert torch.equal(q4.gemm_i8_swiglu(a[:M], sa[:M], gate, up, dtype=TYPES[t]), h[:M]), M
+        o = torch.tensor([0, M // 3, M], dtype=torch.int32, device=DEV)
+        twice = [tuple(torch.stack([p, p]) for p in m) for m in (gate, up)]
+        assert torch.equal(q4.gemm_i8_grouped_swiglu(a[:M], sa[:M], *twice, o, dtype=TYPES[t]), h[:M]), M
+
+
 @pytest.mark.parametrize("M", [2, 40, 300])
 def test_graph_replays(M):
     x, *mats = layer_problem(M, 512, 640)
