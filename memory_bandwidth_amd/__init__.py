@@ -3,8 +3,8 @@
 Every function has the name of the C entry point it calls and only marshals
 arguments: it checks dtypes, shapes, contiguity and device, passes raw device
 pointers and torch's current HIP stream, and raises Q4Error on a non-zero
-status.  All arithmetic runs in the library's HIP kernels; there is no other
-implementation here.  Importing this module without the built library works
+status.  (The 8-bit calls do so in C++, by the module _bind_i8.)  All arithmetic
+runs in the library's HIP kernels; there is no other implementation here.  Importing this module without the built library works
 (so CPU-only tooling can inspect it), but every call then raises.
 
 Storage format (see include/q4gemv.h): x float32 [M, K]; wq uint8 [N, K/2]
@@ -436,24 +436,27 @@ def scan2_config() -> tuple[int, int, int, int]:
 
 # ---------------------------------------------------------------- 8-bit activations and weights
 #
-# A call of these at one row takes as long on the host as on the GPU, so each
-# entry point tests its arguments in one expression; only when that fails do
-# the checks below run one by one, to raise what is wrong.
+# A call of these at one row takes longer on the host than on the GPU, so they
+# go through a module in C++ (csrc/bind_i8.cpp) that tests the arguments,
+# allocates and calls.  It returns None where an argument is not what it must
+# be; the checks here then run one by one, to raise what is wrong.
 
-_current_device = getattr(torch._C, "_cuda_getDevice", None)
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_bind = None
 
 
-def _i8_call(fn: str, dev: int, *args) -> None:
-    """Calls the entry point on the device's current stream, with that device current."""
-    f = getattr(_lib or lib(), fn)
-    if dev == _current_device():
-        status = f(*args, _raw_stream(dev))
-    else:
-        with torch.cuda.device(dev):
-            status = f(*args, _raw_stream(dev))
-    if status:
-        raise Q4Error(fn, status)
+def _load_bind():
+    """The module, given the library's entry points; raises if either has not been built."""
+    global _bind
+    L = lib()
+    try:
+        from . import _bind_i8
+    except ImportError as e:
+        raise RuntimeError("the module _bind_i8.so is not built; run "
+                           "`python -m memory_bandwidth_amd.build` first") from e
+    _bind_i8.init(getattr(torch._C, "_cuda_getCurrentRawStream", None),
+                  *(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in EXPORTS_I8[:5]))
+    _bind = _bind_i8
+    return _bind
 
 
 def _i8_refuse(tensors: dict, shapes: dict, dtype=None) -> None:
@@ -483,27 +486,49 @@ def _size(t, d: int):
     return t.shape[d] if isinstance(t, torch.Tensor) and -t.dim() <= d < t.dim() else None
 
 
+def _i8_refuse_product(a, a_scales, w, w_scales, bias, offsets, grouped, out, dtype) -> None:
+    E = (None if _size(offsets, 0) is None else _size(offsets, 0) - 1,) if grouped else ()
+    shape = (*E, _size(w, -2), _size(a, 1))
+    if grouped and offsets is None:
+        raise TypeError("offsets must be a torch.Tensor")
+    _i8_refuse({"a": (a, (_I8,)), "a_scales": (a_scales, (_F32,)), "w": (w, (_I8,)), "w_scales": (w_scales, (_F32,)),
+                "bias": (bias, (_F32,)), "offsets": (offsets, (_I32,)), "out": (out, (dtype,))},
+               {"a": (a, (None, None)), "a_scales": (a_scales, (_size(a, 0),)), "offsets": (offsets, (None,)),
+                "w": (w, shape), "w_scales": (w_scales, shape[:-1]), "bias": (bias, (shape[-2],)),
+                "out": (out, (_size(a, 0), shape[-2]))}, dtype)
+
+
+def _i8_refuse_pair(a, a_scales, gate, up, offsets, grouped, out, dtype) -> None:
+    for w, w_scales in (gate, up):
+        if not isinstance(w, torch.Tensor) or not isinstance(w_scales, torch.Tensor):
+            raise TypeError("gate and up must each be (weights, scales), two torch.Tensors")
+    if gate[0].shape != up[0].shape:
+        raise ValueError(f"gate and up must have one shape, got {list(gate[0].shape)} and {list(up[0].shape)}")
+    for w, w_scales in (gate, up):
+        try:
+            _i8_refuse_product(a, a_scales, w, w_scales, None, offsets, grouped, out, dtype)
+        except ValueError as e:
+            if w is gate[0] and str(e) == "unsupported arguments":
+                continue                               # gate is as it must be
+            raise
+
+
 def quant_i8(x: torch.Tensor, out: tuple | None = None) -> tuple[torch.Tensor, torch.Tensor]:
     """(codes int8 [M, K], scales float32 [M]) of x [M, K], float32, float16 or
     bfloat16: scales[m] = max|x[m]| / 127 and codes = x / scales to the nearest
     integer.  K is a multiple of 16.  A row with an Inf or a NaN gets the scale
     NaN and zero codes."""
-    _need(x, "x", _X_TYPES)
-    if x.dim() != 2:
-        raise ValueError("x must be [M, K]")
-    M, K = x.shape
-    dev = x.get_device()
-    if out is None:
-        codes = torch.empty_like(x, dtype=_I8)
-        scales = torch.empty(M, dtype=_F32, device=x.device)
-    else:
-        codes, scales = out
-        _need(codes, "codes", (_I8,), x.device)
-        _need(scales, "scales", (_F32,), x.device)
-        if tuple(codes.shape) != (M, K) or tuple(scales.shape) != (M,):
-            raise ValueError("out must be codes [M, K] and scales [M]")
-    _i8_call("quant_i8", dev, x.data_ptr(), I8_TYPES[x.dtype], codes.data_ptr(), scales.data_ptr(), M, K)
-    return codes, scales
+    codes, scales = (None, None) if out is None else out
+    got = (_bind or _load_bind()).quant(x, codes, scales)
+    if type(got) is tuple:
+        return got
+    if got is None:
+        _need(x, "x", _X_TYPES)
+        if x.dim() != 2:
+            raise ValueError(f"x must be [M, K], got {list(x.shape)}")
+        _i8_refuse({"x": (x, _X_TYPES), "codes": (codes, (_I8,)), "scales": (scales, (_F32,))},
+                   {"x": (x, (None, None)), "codes": (codes, x.shape), "scales": (scales, x.shape[:1])})
+    raise Q4Error("quant_i8", got)
 
 
 def gemm_i8(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
@@ -513,75 +538,24 @@ def gemm_i8(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scales: 
 
     a and w int8, scales and bias float32; y is of `dtype` (float32, float16
     or bfloat16).  K is a multiple of 16."""
-    t = I8_TYPES.get(dtype)
-    try:
-        dev, (M, K), (N, Kw) = a.get_device(), a.shape, w.shape
-        fine = (a.dtype is _I8 and w.dtype is _I8 and a_scales.dtype is _F32 and w_scales.dtype is _F32
-                and dev >= 0 and w.get_device() == dev and a_scales.get_device() == dev
-                and w_scales.get_device() == dev and K == Kw and a_scales.shape == (M,) and w_scales.shape == (N,)
-                and a.is_contiguous() and w.is_contiguous() and a_scales.is_contiguous()
-                and w_scales.is_contiguous() and t is not None
-                and (bias is None or (bias.dtype is _F32 and bias.get_device() == dev and bias.shape == (N,)
-                                      and bias.is_contiguous()))
-                and (out is None or (out.dtype is dtype and out.get_device() == dev and out.shape == (M, N)
-                                     and out.is_contiguous())))
-    except (AttributeError, ValueError):
-        fine = False
-    if not fine:
-        _i8_refuse({"a": (a, (_I8,)), "a_scales": (a_scales, (_F32,)), "w": (w, (_I8,)), "w_scales": (w_scales, (_F32,)),
-                    "bias": (bias, (_F32,)), "out": (out, (dtype,))},
-                   {"a": (a, (None, None)), "a_scales": (a_scales, (_size(a, 0),)), "w": (w, (None, _size(a, 1))),
-                    "w_scales": (w_scales, (_size(w, 0),)), "bias": (bias, (_size(w, 0),)),
-                    "out": (out, (_size(a, 0), _size(w, 0)))}, dtype)
-    if out is None:
-        out = torch.empty(M, N, dtype=dtype, device=a.device)
-    _i8_call("gemm_i8", dev, a.data_ptr(), a_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(),
-             None if bias is None else bias.data_ptr(), out.data_ptr(), t, M, N, K)
-    return out
-
-
-def _i8_pair_fine(dev, K, lead, wg, sg, wu, su) -> bool:
-    """Gate and up: one shape [..lead, N, K], a scale for each row."""
-    return (wg.dtype is _I8 and wu.dtype is _I8 and sg.dtype is _F32 and su.dtype is _F32
-            and wg.get_device() == dev and wu.get_device() == dev and sg.get_device() == dev
-            and su.get_device() == dev and wg.shape[:-2] == lead and wg.shape[-1] == K and wu.shape == wg.shape
-            and sg.shape == wg.shape[:-1] and su.shape == sg.shape and wg.is_contiguous() and wu.is_contiguous()
-            and sg.is_contiguous() and su.is_contiguous())
-
-
-def _i8_refuse_pair(a, a_scales, gate, up, offsets, out, dtype) -> None:
-    (wg, sg), (wu, su) = gate, up
-    lead = () if offsets is None else (offsets.numel() - 1 if isinstance(offsets, torch.Tensor) else None,)
-    shape = (*lead, _size(wg, -2), _size(a, 1))
-    _i8_refuse({"a": (a, (_I8,)), "a_scales": (a_scales, (_F32,)), "gate": (wg, (_I8,)), "gate's scales": (sg, (_F32,)),
-                "up": (wu, (_I8,)), "up's scales": (su, (_F32,)), "offsets": (offsets, (_I32,)), "out": (out, (dtype,))},
-               {"a": (a, (None, None)), "a_scales": (a_scales, (_size(a, 0),)), "offsets": (offsets, (None,)),
-                "gate": (wg, shape), "gate's scales": (sg, shape[:-1]), "up": (wu, shape), "up's scales": (su, shape[:-1]),
-                "out": (out, (_size(a, 0), shape[-2]))}, dtype)
+    y = (_bind or _load_bind()).gemm(a, a_scales, w, w_scales, bias, None, dtype, out)
+    if y is None:
+        _i8_refuse_product(a, a_scales, w, w_scales, bias, None, False, out, dtype)
+    if type(y) is int:
+        raise Q4Error("gemm_i8", y)
+    return y
 
 
 def gemm_i8_swiglu(a: torch.Tensor, a_scales: torch.Tensor, gate: tuple, up: tuple,
                    dtype=torch.float32, out: torch.Tensor | None = None) -> torch.Tensor:
     """y = silu(g) * u with g, u the gemm_i8 of a with gate and up, each (w, w_scales)."""
-    t = I8_TYPES.get(dtype)
     (wg, sg), (wu, su) = gate, up
-    try:
-        dev, (M, K) = a.get_device(), a.shape
-        fine = (a.dtype is _I8 and a_scales.dtype is _F32 and dev >= 0 and a_scales.get_device() == dev
-                and a_scales.shape == (M,) and a.is_contiguous() and a_scales.is_contiguous() and t is not None
-                and wg.dim() == 2 and _i8_pair_fine(dev, K, (), wg, sg, wu, su)
-                and (out is None or (out.dtype is dtype and out.get_device() == dev
-                                     and out.shape == (M, wg.shape[0]) and out.is_contiguous())))
-    except (AttributeError, ValueError):
-        fine = False
-    if not fine:
-        _i8_refuse_pair(a, a_scales, gate, up, None, out, dtype)
-    N = wg.shape[0]
-    if out is None:
-        out = torch.empty(M, N, dtype=dtype, device=a.device)
-    _i8_call("gemm_i8_swiglu", dev, a.data_ptr(), a_scales.data_ptr(), wg.data_ptr(), sg.data_ptr(), wu.data_ptr(),
-             su.data_ptr(), out.data_ptr(), t, M, N, K)
-    return out
+    y = (_bind or _load_bind()).swiglu(a, a_scales, wg, sg, wu, su, None, dtype, out)
+    if y is None:
+        _i8_refuse_pair(a, a_scales, gate, up, None, False, out, dtype)
+    if type(y) is int:
+        raise Q4Error("gemm_i8_swiglu", y)
+    return y
 
 
 def gemm_i8_grouped(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
@@ -590,56 +564,27 @@ def gemm_i8_grouped(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_
     """The gemm_i8 of rows offsets[e] .. offsets[e + 1] of a with matrix e of w
     [E, N, K], w_scales [E, N].  offsets is int32 [E + 1] on the GPU, and is
     read there.  Rows outside every group are not written."""
-    t = I8_TYPES.get(dtype)
-    try:
-        dev, (M, K), (E, N, Kw) = a.get_device(), a.shape, w.shape
-        fine = (a.dtype is _I8 and w.dtype is _I8 and a_scales.dtype is _F32 and w_scales.dtype is _F32
-                and offsets.dtype is _I32 and dev >= 0 and w.get_device() == dev and a_scales.get_device() == dev
-                and w_scales.get_device() == dev and offsets.get_device() == dev and K == Kw
-                and a_scales.shape == (M,) and w_scales.shape == (E, N) and offsets.shape == (E + 1,)
-                and a.is_contiguous() and w.is_contiguous() and a_scales.is_contiguous()
-                and w_scales.is_contiguous() and offsets.is_contiguous() and t is not None
-                and (out is None or (out.dtype is dtype and out.get_device() == dev and out.shape == (M, N)
-                                     and out.is_contiguous())))
-    except (AttributeError, ValueError):
-        fine = False
-    if not fine:
-        E = None if _size(offsets, 0) is None else _size(offsets, 0) - 1
-        _i8_refuse({"a": (a, (_I8,)), "a_scales": (a_scales, (_F32,)), "w": (w, (_I8,)), "w_scales": (w_scales, (_F32,)),
-                    "offsets": (offsets, (_I32,)), "out": (out, (dtype,))},
-                   {"a": (a, (None, None)), "a_scales": (a_scales, (_size(a, 0),)), "offsets": (offsets, (None,)),
-                    "w": (w, (E, None, _size(a, 1))), "w_scales": (w_scales, (E, _size(w, 1))),
-                    "out": (out, (_size(a, 0), _size(w, 1)))}, dtype)
-    if out is None:
-        out = torch.empty(M, N, dtype=dtype, device=a.device)
-    _i8_call("gemm_i8_grouped", dev, a.data_ptr(), a_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(),
-             offsets.data_ptr(), out.data_ptr(), t, M, E, N, K)
-    return out
+    y = None if offsets is None else \
+        (_bind or _load_bind()).gemm(a, a_scales, w, w_scales, None, offsets, dtype, out)
+    if y is None:
+        _i8_refuse_product(a, a_scales, w, w_scales, None, offsets, True, out, dtype)
+    if type(y) is int:
+        raise Q4Error("gemm_i8_grouped", y)
+    return y
 
 
 def gemm_i8_grouped_swiglu(a: torch.Tensor, a_scales: torch.Tensor, gate: tuple, up: tuple,
                            offsets: torch.Tensor, dtype=torch.float32,
                            out: torch.Tensor | None = None) -> torch.Tensor:
     """gemm_i8_swiglu of rows offsets[e] .. offsets[e + 1] with matrices e of gate and up."""
-    t = I8_TYPES.get(dtype)
     (wg, sg), (wu, su) = gate, up
-    try:
-        dev, (M, K), (E, N, _) = a.get_device(), a.shape, wg.shape
-        fine = (a.dtype is _I8 and a_scales.dtype is _F32 and offsets.dtype is _I32 and dev >= 0
-                and a_scales.get_device() == dev and offsets.get_device() == dev and a_scales.shape == (M,)
-                and offsets.shape == (E + 1,) and a.is_contiguous() and a_scales.is_contiguous()
-                and offsets.is_contiguous() and t is not None and _i8_pair_fine(dev, K, (E,), wg, sg, wu, su)
-                and (out is None or (out.dtype is dtype and out.get_device() == dev and out.shape == (M, N)
-                                     and out.is_contiguous())))
-    except (AttributeError, ValueError):
-        fine = False
-    if not fine:
-        _i8_refuse_pair(a, a_scales, gate, up, offsets, out, dtype)
-    if out is None:
-        out = torch.empty(M, N, dtype=dtype, device=a.device)
-    _i8_call("gemm_i8_grouped_swiglu", dev, a.data_ptr(), a_scales.data_ptr(), wg.data_ptr(), sg.data_ptr(),
-             wu.data_ptr(), su.data_ptr(), offsets.data_ptr(), out.data_ptr(), t, M, E, N, K)
-    return out
+    y = None if offsets is None else \
+        (_bind or _load_bind()).swiglu(a, a_scales, wg, sg, wu, su, offsets, dtype, out)
+    if y is None:
+        _i8_refuse_pair(a, a_scales, gate, up, offsets, True, out, dtype)
+    if type(y) is int:
+        raise Q4Error("gemm_i8_grouped_swiglu", y)
+    return y
 
 
 def gemm_i8_geometry(matrices: int, M: int, N: int, K: int, groups: int = 0) -> dict:

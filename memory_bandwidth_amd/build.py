@@ -1,7 +1,10 @@
-"""Compile the HIP library libq4gemv.so in-tree for gfx950.
+"""Compile the HIP library libq4gemv.so in-tree for gfx950, and the CPython
+module _bind_i8.so, which calls its 8-bit entry points.
 
 Each source under csrc/ is compiled with hipcc to an object in _build/, in
 parallel, and the objects are linked into memory_bandwidth_amd/libq4gemv.so.
+The module is host code against torch's headers, compiled with the host
+compiler.
 Run as ``python -m memory_bandwidth_amd.build`` (or through
 ``__graft_entry__.build()``).  Compiles every time it is called.
 """
@@ -12,12 +15,14 @@ import concurrent.futures
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libq4gemv.so")
+BIND = os.path.join(HERE, "_bind_i8.so")
 SOURCES = ["api.cpp", "gemv_q4.hip", "gemv_f32.hip", "dequant_q4.hip", "probes.hip", "gemv_blocks.hip",
            "scan2.hip", "quant_i8.hip", "gemm_i8.hip"]
 ARCH = "gfx950"
@@ -46,11 +51,31 @@ def _compile(src: str) -> str:
     return obj
 
 
+def build_bind() -> str:
+    import torch
+    top = os.path.dirname(torch.__file__)
+    tmp = BIND + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", os.path.join(ROOT, "include"), "-I", os.path.join(top, "include"),
+           "-I", os.path.join(top, "include", "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "bind_i8.cpp"), "-o", tmp,
+           "-L", os.path.join(top, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
+           f"-Wl,-rpath,{os.path.join(top, 'lib')}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for bind_i8.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BIND)
+    return BIND
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    jobs = min(len(SOURCES), max(1, min(8, os.cpu_count() or 1)))
+    jobs = min(len(SOURCES) + 1, max(1, min(8, os.cpu_count() or 1)))
     with concurrent.futures.ThreadPoolExecutor(jobs) as ex:
+        bind = ex.submit(build_bind)
         objs = list(ex.map(_compile, SOURCES))
+        bind.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -58,7 +83,7 @@ def build(verbose: bool = False) -> str:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
     if verbose:
-        print(f"built {LIB}")
+        print(f"built {LIB} and {BIND}")
     return LIB
 
 

@@ -8,6 +8,9 @@ end inside a tile, K that ends inside a step, and groups that are empty, of
 one row, or cross tiles.
 """
 
+import sys
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -602,3 +605,101 @@ def test_refusals():
         q4.gemm_i8_grouped(a, sa, w, sw, o)
     with pytest.raises(ValueError):
         q4.gemm_i8_grouped(a, sa, w[None].cpu(), sw[None], o)
+
+
+def test_refusals_of_sizes_past_32_bits():
+    """Row counts that an int of 32 bits would take for others."""
+    M = 2**32 + 5
+    a = torch.empty(1, 16, dtype=torch.int8, device=DEV).expand(M, 16)
+    with pytest.raises(ValueError):
+        q4.gemm_i8(a, torch.ones(1, device=DEV).expand(M), a[:4].contiguous(), torch.ones(4, device=DEV))
+    a = torch.empty(2**31 + 5, 16, dtype=torch.int8, device=DEV)        # 34 GB, never touched
+    with pytest.raises(q4.Q4Error):
+        q4.gemm_i8(a[:4], torch.ones(4, device=DEV), a, torch.empty(2**31 + 5, device=DEV))
+    with pytest.raises(q4.Q4Error):
+        q4.gemm_i8(a, torch.empty(2**31 + 5, device=DEV), a[:4], torch.ones(4, device=DEV))
+
+
+def test_refusals_of_the_quantiser():
+    x = torch.randn(4, 64, device=DEV)
+    c, s = q4.quant_i8(x)
+    for bad in (x.double(), x.int()):
+        with pytest.raises(TypeError):
+            q4.quant_i8(bad)
+    for bad in (x[0], x[None], x.t()):
+        with pytest.raises(ValueError):
+            q4.quant_i8(bad)
+    with pytest.raises(q4.Q4Error):
+        q4.quant_i8(x[:, :24].contiguous())
+    for out in ((c[:3], s), (c, s[:3]), (c, s[:, None])):
+        with pytest.raises(ValueError):
+            q4.quant_i8(x, out=out)
+    for out in ((c.float(), s), (c, s.half()), (None, s), (c, None)):
+        with pytest.raises((TypeError, ValueError)):
+            q4.quant_i8(x, out=out)
+
+
+def test_refusals_name_the_argument():
+    a, w, sa, sw = dev(codes(1, 4, 64)), dev(codes(2, 8, 64)), dev(scales(3, 4)), dev(scales(4, 8))
+    o = torch.tensor([0, 4], dtype=torch.int32, device=DEV)
+    cases = [(lambda: q4.gemm_i8(a, sa.double(), w, sw), "a_scales"), (lambda: q4.gemm_i8(a, sa, w, sw[:7]), "w_scales"),
+             (lambda: q4.gemm_i8(a, sa, w.t(), sw), "w"), (lambda: q4.gemm_i8(a, sa, w, sw, bias=sw.half()), "bias"),
+             (lambda: q4.gemm_i8_swiglu(a, sa, (w, sw), (w, sw[:7])), "w_scales"),
+             (lambda: q4.gemm_i8_swiglu(a, sa, (w, sw), (w.float(), sw)), "w"),
+             (lambda: q4.gemm_i8_swiglu(a, sa, (w, sw), (w, None)), "up"),
+             (lambda: q4.gemm_i8_grouped(a, sa, w[None], sw[None], None), "offsets"),
+             (lambda: q4.gemm_i8_grouped(a, sa, w[None], sw[None], o[None]), "offsets"),
+             (lambda: q4.gemm_i8_grouped(a, sa, w[None], sw, o), "w_scales"),
+             (lambda: q4.gemm_i8_grouped_swiglu(a, sa, (w[None], sw[None]), (w[None], sw[None]), None), "offsets"),
+             (lambda: q4.gemm_i8_grouped_swiglu(a, sa, (w[None], sw[None]), (w[None], sw[None]), o, out=sw), "out")]
+    for call, name in cases:
+        with pytest.raises((TypeError, ValueError), match=name):
+            call()
+
+
+def test_calls_keep_nothing():
+    """Outputs are freed with their last name, and a given output is returned itself."""
+    a, w, sa, sw = dev(codes(1, 40, 64)), dev(codes(2, 80, 64)), dev(scales(3, 40)), dev(scales(4, 80))
+    x, o = torch.randn(40, 64, device=DEV), torch.tensor([0, 9, 40], dtype=torch.int32, device=DEV)
+    y = torch.empty(40, 80, device=DEV)
+    two = torch.stack([w, w]), torch.stack([sw, sw])
+
+    def calls():
+        q4.quant_i8(x)
+        assert q4.gemm_i8(a, sa, w, sw, out=y) is y
+        assert q4.gemm_i8_swiglu(a, sa, (w, sw), (w, sw), out=y) is y
+        q4.gemm_i8(a, sa, w, sw, bias=sw)
+        q4.gemm_i8_grouped(a, sa, *two, o)
+        q4.gemm_i8_grouped_swiglu(a, sa, two, two, o)
+
+    calls()
+    names = (a, w, sa, sw, x, o, y, two)
+    before = torch.cuda.memory_allocated(), [sys.getrefcount(n) for n in names]
+    for _ in range(50):
+        calls()
+    assert before == (torch.cuda.memory_allocated(), [sys.getrefcount(n) for n in names])
+
+
+def test_threads():
+    """Threads that call at once, each on a stream of its own."""
+    x, *mats = layer_problem(70, 512, 640)
+    mats = [tuple(map(dev, m)) for m in mats]
+    xs = [(x * (i + 1)).to(DEV) for i in range(4)]
+    want = [layer(v, *mats) for v in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    got = [None] * 4
+
+    def work(i):
+        with torch.cuda.stream(streams[i]):
+            for _ in range(30):
+                got[i] = layer(xs[i], *mats)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for i in range(4):
+        assert all(torch.equal(p, q) for p, q in zip(got[i], want[i]))
