@@ -135,55 +135,58 @@ __device__ __forceinline__ Rows rows_of(const Args &p, int e) {
 // Groups for each lane: lane l sums the tiles of groups l * groups_each ..
 __device__ __forceinline__ int groups_each(const Args &p) { return (p.E + 63) >> 6; }
 
-// The tiles of bm rows of all groups up to and with this lane's, at most
+// Of a lane: the tiles of bm rows of all groups up to and with its own, at most
 // tiles_m for each lane (no more unless the offsets are out of order: the sums
-// cannot overflow).
-__device__ __forceinline__ int tiles_upto(const Args &p, int bm) {
-    if (!p.offsets) return 0;
+// cannot overflow), and the rows of its first group.
+struct Groups { int upto; Rows rows; };
+__device__ __forceinline__ Groups groups_of(const Args &p, int bm) {
+    if (!p.offsets) return {0, {0, 0}};
     const int each = groups_each(p), e0 = (threadIdx.x & 63) * each;
-    int mine = 0;
+    const Rows first = rows_of(p, e0);
+    int mine = min((int)((unsigned)(first.hi - first.lo + bm - 1) / (unsigned)bm), p.tiles_m);
 #pragma unroll 4
-    for (int e = e0; e < e0 + each; ++e) {
+    for (int e = e0 + 1; e < e0 + each; ++e) {
         const Rows r = rows_of(p, e);
         mine = min(mine + (int)((unsigned)(r.hi - r.lo + bm - 1) / (unsigned)bm), p.tiles_m);
     }
-    return scan_lanes(mine);
+    return {scan_lanes(mine), first};
 }
 
-// The tiles that there are, given tiles_upto.
-__device__ __forceinline__ int tile_count(const Args &p, int upto) {
-    return p.offsets ? min(__builtin_amdgcn_readlane(upto, 63), p.tiles_m) : p.tiles_m;
+// The tiles that there are.
+__device__ __forceinline__ int tile_count(const Args &p, const Groups &g) {
+    return p.offsets ? min(__builtin_amdgcn_readlane(g.upto, 63), p.tiles_m) : p.tiles_m;
 }
 
 // Tile t of bm rows (rows == 0: there is none): the lane whose groups hold it,
 // then the group among that lane's.
-__device__ __forceinline__ Tile find_tile(const Args &p, int bm, int upto, int t) {
+__device__ __forceinline__ Tile find_tile(const Args &p, int bm, const Groups &g, int t) {
     if (!p.offsets) return {t * bm, min(bm, p.M - t * bm), 0};
-    const unsigned long long past = __ballot(upto > t);
+    const unsigned long long past = __ballot(g.upto > t);
     if (!past) return {0, 0, 0};
     const int owner = __ffsll(past) - 1, each = groups_each(p);
-    if (owner) t -= __builtin_amdgcn_readlane(upto, owner - 1);
+    if (owner) t -= __builtin_amdgcn_readlane(g.upto, owner - 1);
     int e = owner * each;
+    Rows r = {__builtin_amdgcn_readlane(g.rows.lo, owner), __builtin_amdgcn_readlane(g.rows.hi, owner)};
     if (each > 1) {
         for (int c = 0;; c += 64) {
             if (c >= each) return {0, 0, 0};
             const int q = c + (threadIdx.x & 63);
-            const Rows r = q < each ? rows_of(p, e + q) : Rows{0, 0};
-            const int mine = (int)((unsigned)(r.hi - r.lo + bm - 1) / (unsigned)bm);
+            const Rows here_rows = q < each ? rows_of(p, e + q) : Rows{0, 0};
+            const int mine = (int)((unsigned)(here_rows.hi - here_rows.lo + bm - 1) / (unsigned)bm);
             const int here = scan_lanes(min(mine, p.tiles_m));
             const unsigned long long in = __ballot(here > t);
             if (in) {
                 const int l = __ffsll(in) - 1;
                 if (l) t -= __builtin_amdgcn_readlane(here, l - 1);
                 e += c + l;
+                r = {__builtin_amdgcn_readlane(here_rows.lo, l), __builtin_amdgcn_readlane(here_rows.hi, l)};
                 break;
             }
             t -= __builtin_amdgcn_readlane(here, 63);
         }
     }
-    const Rows r = rows_of(p, e);
-    const int m0 = __builtin_amdgcn_readfirstlane(r.lo) + t * bm;
-    return {m0, min(bm, __builtin_amdgcn_readfirstlane(r.hi) - m0), e};
+    const int m0 = r.lo + t * bm;
+    return {m0, min(bm, r.hi - m0), e};
 }
 
 // Scales a wavefront's sums and writes them.  acc[i][..]: rows row0 + 16 i +
@@ -346,17 +349,18 @@ __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_i8_block(Args p) {
     const int wm = wave / WN, wn = wave % WN;
     const int steps = (p.K + G * BK - 1) / (G * BK);
     // Every wavefront leaves the same sums of the groups' tiles in LDS, and
-    // finds its own there whenever it looks for a tile.
-    int *sums = reinterpret_cast<int *>(lds + D * STAGE + 2 * (BM + BW) * 4) + lane;
+    // finds its own there whenever it looks for a tile: a load from memory would
+    // wait for all of the ring's.
+    Groups *groups = reinterpret_cast<Groups *>(lds + D * STAGE + 2 * (BM + BW) * 4) + lane;
     const int bm = p.part == kRest ? 2 * BM : BM;
-    *sums = tiles_upto(p, bm);
-    const int tiles_m = tile_count(p, *sums), all = tiles_m * p.tiles_n, whole = whole_rounds(all);
+    *groups = groups_of(p, bm);
+    const int tiles_m = tile_count(p, *groups), all = tiles_m * p.tiles_n, whole = whole_rounds(all);
     struct Place { Tile tl; int n0; };
     auto place = [&](int id, Place &at) {
         const int b = p.part == kRest ? whole + (id >> 2) : id;
         int tm, tn;
         if (b >= (p.part == kWhole ? whole : all) || !tile_of(b, tiles_m, p.tiles_n, tm, tn)) return false;
-        at.tl = find_tile(p, bm, *sums, tm);
+        at.tl = find_tile(p, bm, *groups, tm);
         at.n0 = tn * BN;
         if (p.part == kRest) {
             const int down = (id >> 1 & 1) * BM;
@@ -568,15 +572,15 @@ __global__ __launch_bounds__(W * 64) void gemm_i8_few(Args p, int ks_log2) {
     const int KS = 1 << ks_log2, ks = wave & (KS - 1);
     // Row tiles that read the same weights lie side by side on one XCD, so that
     // its L2 brings them once; others take the XCDs in turn.
-    const int upto = tiles_upto(p, BM);
+    const Groups groups = groups_of(p, BM);
     int tm = (int)blockIdx.x / p.tiles_n, tn = (int)blockIdx.x - tm * p.tiles_n;
     if (p.share) {
-        const int tiles_m = tile_count(p, upto), id = eighth_of(blockIdx.x, tiles_m * p.tiles_n);
+        const int tiles_m = tile_count(p, groups), id = eighth_of(blockIdx.x, tiles_m * p.tiles_n);
         if (id < 0) return;
         tn = id / tiles_m;
         tm = id - tn * tiles_m;
     }
-    const Tile tl = find_tile(p, BM, upto, tm);
+    const Tile tl = find_tile(p, BM, groups, tm);
     if (tl.rows <= 0) return;
     const int n0 = (tn * (W >> ks_log2) + (wave >> ks_log2)) * 16;
     const size_t mat = (size_t)tl.e * p.N;
@@ -748,7 +752,7 @@ int launch_few(const Args &p, const Target &to) {
 
 template <int BM, int BW, int WM, int WN, int G, int D, bool SWI>
 int launch_block(Args p, const Target &to) {
-    constexpr int kLds = G * D * (BM + BW) * BK + 2 * (BM + BW) * 4 + 256, kThreads = WM * WN * G * 64;
+    constexpr int kLds = G * D * (BM + BW) * BK + 2 * (BM + BW) * 4 + 64 * (int)sizeof(Groups), kThreads = WM * WN * G * 64;
     constexpr int kBN = SWI ? BW / 2 : BW;
     const int half = p.part == kRest ? 2 : 1;
     p.tiles_m = (int)row_tiles(p, half * BM);
