@@ -24,13 +24,15 @@ typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 constexpr int kCUs = 256;
 
 // Tiles of 256 x 256 come in rounds of one for each CU.  Where the last round
-// would have up to 96, they are halved both ways, in a launch of their own: up
-// to 64 then take one round of a third of the time, more take two.  With and
-// without, 4600 x 4096 x 14336 (32 tiles left) takes 241 and 315 us, 5376 rows
-// (80 left) 295 and 316, 9000 x 8192 x 8192 (128 left) 502 and 483.  kWhole
-// and kRest are the two launches.
-enum Part { kAll, kWhole, kRest };
-constexpr int kRestMost = 96;
+// would have up to 128, they go to a launch of their own (kHalves, 128 rows
+// each, where there are more than 64; kQuarters, 128 x 128, else), which takes
+// one round of two thirds or a third of the time: 4600 x 4096 x 14336 (32 tiles
+// left) takes 225 us so and 315 without, 5376 rows (80 left) 254 and 316 (287
+// as quarters, in two rounds), 9000 x 8192 x 8192 (128 left) 469 and 481.
+// With groups the count is the GPU's to know: both are launched, and one has
+// no work.
+enum Part { kAll, kWhole, kHalves, kQuarters };
+constexpr int kRestMost = 128, kQuartersMost = 64;
 
 struct Args {
     const int8_t *a;
@@ -41,7 +43,7 @@ struct Args {
     const int32_t *offsets;    // groups, or NULL
     void *y;
     int y_type, M, N, K, E;
-    int tiles_m, tiles_n;      // kRest: of the tiles that are halved
+    int tiles_m, tiles_n;      // kHalves, kQuarters: of the tiles that are divided
     Part part;
     bool once;                 // the weights' stream is more than a cache would keep
     bool share;                // several row tiles read the same weights
@@ -352,21 +354,22 @@ __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_i8_block(Args p) {
     // finds its own there whenever it looks for a tile: a load from memory would
     // wait for all of the ring's.
     Groups *groups = reinterpret_cast<Groups *>(lds + D * STAGE + 2 * (BM + BW) * 4) + lane;
-    const int bm = p.part == kRest ? 2 * BM : BM;
+    const int bm = p.part >= kHalves ? 2 * BM : BM;
     *groups = groups_of(p, bm);
     const int tiles_m = tile_count(p, *groups), all = tiles_m * p.tiles_n, whole = whole_rounds(all);
+    if (p.part >= kHalves && (all - whole <= kQuartersMost) != (p.part == kQuarters)) return;
     struct Place { Tile tl; int n0; };
     auto place = [&](int id, Place &at) {
-        const int b = p.part == kRest ? whole + (id >> 2) : id;
+        const int b = p.part >= kHalves ? whole + (id >> (p.part - kHalves + 1)) : id;
         int tm, tn;
         if (b >= (p.part == kWhole ? whole : all) || !tile_of(b, tiles_m, p.tiles_n, tm, tn)) return false;
         at.tl = find_tile(p, bm, *groups, tm);
         at.n0 = tn * BN;
-        if (p.part == kRest) {
-            const int down = (id >> 1 & 1) * BM;
+        if (p.part >= kHalves) {
+            const int down = (id & 1) * BM;
             at.tl.m0 += down;
             at.tl.rows = min(BM, at.tl.rows - down);
-            at.n0 = (2 * tn + (id & 1)) * BN;
+            if (p.part == kQuarters) at.n0 = (2 * tn + (id >> 1 & 1)) * BN;
         }
         return at.tl.rows > 0 && at.n0 < p.N;
     };
@@ -754,13 +757,15 @@ template <int BM, int BW, int WM, int WN, int G, int D, bool SWI>
 int launch_block(Args p, const Target &to) {
     constexpr int kLds = G * D * (BM + BW) * BK + 2 * (BM + BW) * 4 + 64 * (int)sizeof(Groups), kThreads = WM * WN * G * 64;
     constexpr int kBN = SWI ? BW / 2 : BW;
-    const int half = p.part == kRest ? 2 : 1;
-    p.tiles_m = (int)row_tiles(p, half * BM);
-    p.tiles_n = (int)tiles_of(p.N, half * kBN);
+    p.tiles_m = (int)row_tiles(p, (p.part >= kHalves ? 2 : 1) * BM);
+    p.tiles_n = (int)tiles_of(p.N, (p.part == kQuarters ? 2 : 1) * kBN);
     int64_t grid = (int64_t)p.tiles_m * p.tiles_n;
     if (grid > 1 << 30) return Q4_EINVAL;
     if (p.part == kWhole) grid = p.offsets ? grid : whole_rounds((int)grid);
-    if (p.part == kRest) grid = 4 * (p.offsets ? std::min<int64_t>(grid, kRestMost) : grid - whole_rounds((int)grid));
+    if (p.part >= kHalves) {
+        const int most = p.part == kHalves ? kRestMost : kQuartersMost;
+        grid = (p.offsets ? std::min<int64_t>(grid, most) : grid - whole_rounds((int)grid)) << (p.part - kHalves + 1);
+    }
     // Workgroups that stay and go through the tiles, each loading its next one
     // while it finishes the last: 8192 x 8192 x 512 takes 66 us so, 74 with a
     // workgroup for each tile, x 1024 93 and 99; 8000 rows over 64 experts with
@@ -768,7 +773,7 @@ int launch_block(Args p, const Target &to) {
     // them as CUs come free is better where they differ: 527 against 539 us
     // for 8190 rows over 8 experts, K = 14336.
     const int64_t steps = tiles_of(p.K, BK);
-    if (G == 1 && p.part != kRest && steps >= D && steps <= 64)
+    if (G == 1 && p.part < kHalves && steps >= D && steps <= 64)
         grid = std::min<int64_t>(grid, kCUs * (160 * 1024 / kLds));
     else if (grid * kThreads > kMaxThreads) return Q4_EINVAL;
     if (to.report) {
@@ -836,9 +841,9 @@ Kernel choose(const Args &p, int mats) {
     cost[kTile128] = each(tiles(128, 128), 2.25 + steps * 0.46, 0.63 + steps * 0.78);
     cost[kTileWide] = rounds(128, 256) * (6.54 + steps * 0.75);
     const int64_t t256 = tiles(256, 256), left = t256 % kCUs;
-    const double halved = (double)((4 * left + kCUs - 1) / kCUs) * (2.25 + steps * 0.46);
+    const double divided = left > kQuartersMost ? 6.54 + steps * 0.75 : left ? 2.25 + steps * 0.46 : 0.;
     cost[kTile256] = t256 < kCUs || left > kRestMost ? rounds(256, 256) * (8.0 + steps * 1.33)
-                                                     : (double)(t256 / kCUs) * (8.0 + steps * 1.33) + halved;
+                                                     : (double)(t256 / kCUs) * (8.0 + steps * 1.33) + divided;
     Kernel best = kFew16;
     for (Kernel k : {kFew8, kFew32, kTileDeep, kTile64, kTile128, kTileWide, kTile256})
         if (cost[k] < cost[best] && !(p.offsets && k == kFew8)) best = k;
@@ -864,13 +869,18 @@ int launch(const Args &p, Kernel k, const Target &to) {
         return launch_block<128, 128, 2, 4, 1, 2, SWI>(p, to);
     case kTileWide: return launch_block<128, 256, 2, 4, 1, 3, SWI>(p, to);
     default: {
-        // Whole rounds, then the tiles that are left, halved both ways.
+        // Whole rounds, then the tiles that are left, divided.
         Args q = p;
-        const int64_t all = row_tiles(p, 256) * tiles_of(p.N, SWI ? 128 : 256);
-        if (all >= kCUs && (p.offsets || whole_rounds((int)std::min<int64_t>(all, 0x7FFFFFFF)) < all)) q.part = kWhole;
+        const int64_t all = row_tiles(p, 256) * tiles_of(p.N, SWI ? 128 : 256), left = all % kCUs;
+        if (all >= kCUs && (p.offsets || (left && left <= kRestMost))) q.part = kWhole;
         if (int st = launch_block<256, 256, 2, 4, 1, 2, SWI>(q, to)) return st;
         if (q.part == kAll || to.report) return Q4_OK;
-        q.part = kRest;
+        if (p.offsets || left > kQuartersMost) {
+            q.part = kHalves;
+            if (int st = launch_block<128, 256, 2, 4, 1, 3, SWI>(q, to)) return st;
+        }
+        if (!p.offsets && left > kQuartersMost) return Q4_OK;
+        q.part = kQuarters;
         return launch_block<128, 128, 2, 4, 1, 4, SWI>(q, to);
     }
     }

@@ -157,7 +157,7 @@ def exact_rows(a, sa, w, sw):
     return (dev(a).double() @ dev(w).double().t()) * dev(sa).double()[:, None] * dev(sw).double()
 
 
-@pytest.mark.parametrize("M,N,K", [(4300, 4100, 2064), (4096, 5300, 2000), (8200, 4097, 1040)])
+@pytest.mark.parametrize("M,N,K", [(4300, 4100, 2064), (4096, 5300, 2000), (8200, 4097, 1040), (4300, 5000, 2064)])
 @pytest.mark.parametrize("groups", [0, 3])
 @pytest.mark.parametrize("swiglu", [False, True])
 def test_last_round_halved(M, N, K, groups, swiglu):
