@@ -551,8 +551,8 @@ __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_i8_block(Args p) {
 // ---------------------------------------------------------------- few rows
 //
 // Tiles of 8 NX rows: what counts is the bytes in flight, and that every CU
-// has its share of them.  A wavefront takes a strip of 16 weight rows (of each
-// matrix) and every KS-th unit of 128 bytes of K; KS wavefronts of a
+// has its share of them.  A wavefront takes FN strips of 16 weight rows (of
+// each matrix) and every KS-th unit of 128 bytes of K; KS wavefronts of a
 // workgroup meet in LDS at the end.  Its units pass through a ring of D
 // slots of its own in LDS, loaded straight from memory eight rows of 128
 // bytes an instruction (a fragment's own order, 16 rows of 64 bytes, loads
@@ -565,9 +565,9 @@ __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_i8_block(Args p) {
 // columns of 4096 5.8 and 9.3.
 constexpr int kFewDepth = 2;
 
-template <int NX, bool SWI, int W>
+template <int NX, int FN, bool SWI, int W>
 __global__ __launch_bounds__(W * 64) void gemm_i8_few(Args p, int ks_log2) {
-    constexpr int FM = (NX + 1) / 2, BM = 8 * NX, FW = SWI ? 2 : 1;     // FW: a fragment of each matrix
+    constexpr int FM = (NX + 1) / 2, BM = 8 * NX, MATS = SWI ? 2 : 1, FW = FN * MATS;
     constexpr int D = kFewDepth, LOADS = 2 * FW + NX;                   // load instructions of a unit
     constexpr int SLOT = (2 * FW + 2 * FM) * 1024;                      // whole fragments, the last may be half loaded
     extern __shared__ __align__(16) char lds[];
@@ -585,7 +585,7 @@ __global__ __launch_bounds__(W * 64) void gemm_i8_few(Args p, int ks_log2) {
     }
     const Tile tl = find_tile(p, BM, groups, tm);
     if (tl.rows <= 0) return;
-    const int n0 = (tn * (W >> ks_log2) + (wave >> ks_log2)) * 16;
+    const int n0 = (tn * (W >> ks_log2) + (wave >> ks_log2)) * (16 * FN);
     const size_t mat = (size_t)tl.e * p.N;
     const int kc = p.K >> 4, units = (kc + 7) >> 3;
     const int g = lane >> 4, r = lane & 15;
@@ -593,25 +593,28 @@ __global__ __launch_bounds__(W * 64) void gemm_i8_few(Args p, int ks_log2) {
 
     if (n0 < p.N) {
         char *ring = lds + wave * (D * SLOT);
-        const int cols = min(16, p.N - n0);
+        const int cols = min(16 * FN, p.N - n0);
         const __amdgpu_buffer_rsrc_t rx = rsrc_of(p.a + (size_t)tl.m0 * p.K, (uint32_t)tl.rows * p.K);
-        __amdgpu_buffer_rsrc_t rw[FW];
+        __amdgpu_buffer_rsrc_t rw[MATS];
 #pragma unroll
-        for (int s = 0; s < FW; ++s) rw[s] = rsrc_of(p.w[s] + (mat + n0) * p.K, (uint32_t)cols * p.K);
-        uint32_t vx[NX], vw[2];
+        for (int s = 0; s < MATS; ++s) rw[s] = rsrc_of(p.w[s] + (mat + n0) * p.K, (uint32_t)cols * p.K);
+        uint32_t vx[NX], vw[2 * FN];
 #pragma unroll
         for (int i = 0; i < NX; ++i) vx[i] = (uint32_t)min(i * 8 + (lane >> 3), tl.rows - 1) * p.K;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) vw[i] = (uint32_t)min(i * 8 + (lane >> 3), cols - 1) * p.K;
+        for (int i = 0; i < 2 * FN; ++i) {
+            const int q = (i & 1) * 8 + (lane >> 3);               // row of fragment i / 2
+            vw[i] = (uint32_t)min(frag_row<FN>(i >> 1, q), cols - 1) * p.K;
+        }
         const int chunk = (lane & 7) ^ (lane >> 3);
         auto load = [&](int slot, int u) {
             char *at = ring + slot * SLOT;
             const uint32_t k = (uint32_t)min(u * 8 + chunk, kc - 1) << 4;
 #pragma unroll
-            for (int s = 0; s < FW; ++s)
+            for (int s = 0; s < MATS; ++s)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    char *to = at + (s * 2 + i) * 1024;
+                for (int i = 0; i < 2 * FN; ++i) {
+                    char *to = at + (s * 2 * FN + i) * 1024;
                     if (p.once) load16<true>(rw[s], to, vw[i] + k, 0);
                     else load16(rw[s], to, vw[i] + k, 0);
                 }
@@ -677,14 +680,14 @@ __global__ __launch_bounds__(W * 64) void gemm_i8_few(Args p, int ks_log2) {
 #pragma unroll
                 for (int j = 0; j < FW; ++j) acc[i][j] += part[((wave + k) * FM * FW + i * FW + j) * 64];
     }
-    constexpr int C = 4;
+    constexpr int C = 4 * FN;
     const int n = n0 + g * C;
-    float sw[FW][C];
+    float sw[MATS][C];
 #pragma unroll
-    for (int s = 0; s < FW; ++s)
+    for (int s = 0; s < MATS; ++s)
 #pragma unroll
         for (int c = 0; c < C; ++c) sw[s][c] = n + c < p.N ? p.sw[s][mat + n + c] : 0.f;
-    finish<FM, C, SWI>(p, acc, tl, p.sa + tl.m0, sw[0], sw[FW - 1], 0, n, lane);
+    finish<FM, C, SWI>(p, acc, tl, p.sa + tl.m0, sw[0], sw[MATS - 1], 0, n, lane);
 }
 
 constexpr int kMaxRows = 1 << 24;
@@ -713,18 +716,18 @@ struct Target { hipStream_t stream; Report *report; };
 // 10.5 and 12.9 us; but 8 are as good where they come to no more than one a
 // CU, and then 14.1 against 14.6 us at 16 rows, 4096 -> 14336.
 struct Split { int64_t tiles, strips; int log2, waves; };
-Split split_of(const Args &p, int bm) {
-    Split s = {row_tiles(p, bm), tiles_of(p.N, 16), 0, 8};
+Split split_of(const Args &p, int bm, int cols, int most) {
+    Split s = {row_tiles(p, bm), tiles_of(p.N, cols), 0, most};
     const int64_t units = tiles_of(p.K, BK);
-    while (s.log2 < 3 && (units >> s.log2) > 1 && (s.tiles * s.strips) << s.log2 < 1536) ++s.log2;
-    const int64_t eights = s.tiles * tiles_of(s.strips, 8 >> s.log2);
+    while ((2 << s.log2) <= most && (units >> s.log2) > 1 && (s.tiles * s.strips) << s.log2 < 1536) ++s.log2;
+    const int64_t eights = most == 8 ? s.tiles * tiles_of(s.strips, 8 >> s.log2) : 0;
     if (s.log2 < 3 && (eights < kCUs / 2 || eights > kCUs)) s.waves = 4;
     return s;
 }
 
-template <int NX, bool SWI, int W>
+template <int NX, int FN, bool SWI, int W>
 int launch_few(Args p, const Split &s, const Target &to) {
-    constexpr int FM = (NX + 1) / 2, FW = SWI ? 2 : 1, kLds = W * kFewDepth * (2 * FW + 2 * FM) * 1024;
+    constexpr int FM = (NX + 1) / 2, FW = SWI ? 2 * FN : FN, kLds = W * kFewDepth * (2 * FW + 2 * FM) * 1024;
     // Weights of more than a quarter of the 256 MB cache are loaded
     // non-temporally.  Cycling 2 GB of matrices, one row through 4096 -> 14336
     // (59 MB) takes 12.6 us so and 14.2 without, the SwiGLU of two such 24.0
@@ -740,22 +743,25 @@ int launch_few(Args p, const Split &s, const Target &to) {
     const int64_t grid = s.tiles * p.tiles_n;
     if (grid * (W * 64) > kMaxThreads) return Q4_EINVAL;
     if (to.report) {
-        *to.report = {8 * NX, (W >> s.log2) * 16, (int)grid, W * 64};
+        *to.report = {8 * NX, (W >> s.log2) * 16 * FN, (int)grid, W * 64};
         return Q4_OK;
     }
-    gemm_i8_few<NX, SWI, W><<<(unsigned)grid, W * 64, kLds, to.stream>>>(p, s.log2);
+    gemm_i8_few<NX, FN, SWI, W><<<(unsigned)grid, W * 64, kLds, to.stream>>>(p, s.log2);
     return q4::launch_status();
 }
 
-template <int NX, bool SWI>
+template <int NX, int FN, bool SWI, int MOST = 8>
 int launch_few(const Args &p, const Target &to) {
-    const Split s = split_of(p, 8 * NX);
-    return s.waves == 8 ? launch_few<NX, SWI, 8>(p, s, to) : launch_few<NX, SWI, 4>(p, s, to);
+    const Split s = split_of(p, 8 * NX, 16 * FN, MOST);
+    if constexpr (MOST == 8)
+        if (s.waves == 8) return launch_few<NX, FN, SWI, 8>(p, s, to);
+    return launch_few<NX, FN, SWI, 4>(p, s, to);
 }
 
 template <int BM, int BW, int WM, int WN, int G, int D, bool SWI>
 int launch_block(Args p, const Target &to) {
-    constexpr int kLds = G * D * (BM + BW) * BK + 2 * (BM + BW) * 4 + 64 * (int)sizeof(Groups), kThreads = WM * WN * G * 64;
+    constexpr int kLds = G * D * (BM + BW) * BK + 2 * (BM + BW) * 4 + 64 * (int)sizeof(Groups);
+    constexpr int kThreads = WM * WN * G * 64;
     constexpr int kBN = SWI ? BW / 2 : BW;
     p.tiles_m = (int)row_tiles(p, (p.part >= kHalves ? 2 : 1) * BM);
     p.tiles_n = (int)tiles_of(p.N, (p.part == kQuarters ? 2 : 1) * kBN);
@@ -784,18 +790,19 @@ int launch_block(Args p, const Target &to) {
     return q4::launch_status();
 }
 
-enum Kernel { kFew8, kFew16, kFew32, kTile64, kTile128, kTileWide, kTile256, kTileDeep, kKernels };
+enum Kernel { kFew8, kFew16, kFew32, kFew32x32, kFew64, kTile64, kTile128, kTileWide, kTile256, kTileDeep, kKernels };
 
 // The kernel for a call's sizes.  Up to 8 rows the weights' stream decides.
 // Above that, each kernel's time is estimated, with constants fitted to
 // measured shapes: the tiles to 320 (33 to 8192 rows, N 64 to 14336, K 256 to
 // 14336, one matrix and two), in us a tile, us a step, and how far more tiles
 // than CUs stretch it; tiles that have a CU to themselves come in whole rounds.
-// The kernels of few rows to 550 (9 to 3000 rows): us a unit of a wavefront
+// The kernels of few rows to 1070 (9 to 3000 rows): us a unit of a wavefront
 // alone and for each of the CU's, and, as they read weights past the L2 again
-// for every row tile, us a MB of weights.  The choice is on average 1.4%
-// behind the best of the seven there, at most 30%.  With 64 x 4096 x 14336 as
-// an example, 32 rows a workgroup take 21.2 us, 64 x 64 tiles 37.
+// for every row tile, us a MB of weights.  The choice is on average 1.2%
+// behind the best of the nine there.  64 x 4096 x 14336 takes 21.2 us in tiles
+// of 32 x 32, 26.4 in 32 x 16, 28.4 in 64 x 32, 36.7 in 64 x 64; at 128 rows
+// these are 32.9, 41.3, 26.8 and 36.3.
 // Groups go by their average rows, their sizes being known to the GPU alone.
 // Measured over 64 experts of 2 x 2816 x 1024, at 4, 32 and 128 rows each: 16
 // rows a tile 73, 133, - us, 64 rows 69, 82, 133, 128 rows 72, 90, 115, 256
@@ -823,8 +830,8 @@ Kernel choose(const Args &p, int mats) {
     auto rounds = [&](int bm, int bw) { return (double)((tiles(bm, bw) + kCUs - 1) / kCUs); };
     // Tiles a CU, 1 where there are fewer, and the time of one alone or of one among others.
     auto each = [&](int64_t t, double one, double many) { return t <= kCUs ? one : (double)t / kCUs * many; };
-    auto few = [&](int bm, double start, double unit, double shared, double first) {
-        const Split s = split_of(p, bm);
+    auto few = [&](int bm, int cols, int most, double start, double unit, double shared, double first) {
+        const Split s = split_of(p, bm, cols, most);
         const int64_t tm = row_tiles_likely(bm), wgs = tm * tiles_of(s.strips, s.waves >> s.log2);
         const double a_unit = std::max(unit, shared * (double)(tiles_of(wgs, kCUs) * s.waves));
         const double mb = p.offsets ? 0. : (double)mats * p.N * p.K * 1e-6;
@@ -833,9 +840,11 @@ Kernel choose(const Args &p, int mats) {
     };
     const bool two = mats == 2;
     double cost[kKernels];
-    cost[kFew8] = few(8, -0.5, 0.15, two ? 0.050 : 0.031, 0.81);
-    cost[kFew16] = few(16, -0.7, 0.24, two ? 0.099 : 0.043, 0.5);
-    cost[kFew32] = few(32, -0.4, 0.30, two ? 0.154 : 0.11, 0.74);
+    cost[kFew8] = few(8, 16, 8, -0.5, 0.15, two ? 0.050 : 0.031, 0.81);
+    cost[kFew16] = few(16, 16, 8, -0.7, 0.24, two ? 0.099 : 0.043, 0.5);
+    cost[kFew32] = few(32, 16, 8, -0.4, 0.30, two ? 0.154 : 0.11, 0.74);
+    cost[kFew32x32] = few(32, 32, 8, -0.23, 0.33, 0.14, 0.56);       // with one matrix
+    cost[kFew64] = few(64, two ? 16 : 32, 4, 0.74, 0.63, 0.25, 0.75);
     cost[kTileDeep] = each(tiles(64, 64), 0.67 + steps * 0.38, 0.78 + steps * 0.40);
     cost[kTile64] = std::max(1.0, (double)tiles(64, 128) / kCUs * 1.2) * (0.67 + steps * 0.42);
     cost[kTile128] = each(tiles(128, 128), 2.25 + steps * 0.46, 0.63 + steps * 0.78);
@@ -844,9 +853,13 @@ Kernel choose(const Args &p, int mats) {
     const double divided = left > kQuartersMost ? 6.54 + steps * 0.75 : left ? 2.25 + steps * 0.46 : 0.;
     cost[kTile256] = t256 < kCUs || left > kRestMost ? rounds(256, 256) * (8.0 + steps * 1.33)
                                                      : (double)(t256 / kCUs) * (8.0 + steps * 1.33) + divided;
+    // Of few rows, groups take 16 or 32 a tile: at 8, most are read in several.
     Kernel best = kFew16;
-    for (Kernel k : {kFew8, kFew32, kTileDeep, kTile64, kTile128, kTileWide, kTile256})
-        if (cost[k] < cost[best] && !(p.offsets && k == kFew8)) best = k;
+    for (Kernel k : {kFew32, kTileDeep, kTile64, kTile128, kTileWide, kTile256})
+        if (cost[k] < cost[best]) best = k;
+    if (p.offsets) return best;
+    for (Kernel k : {kFew8, kFew32x32, kFew64})
+        if (cost[k] < cost[best] && !(two && k == kFew32x32)) best = k;
     return best;
 }
 
@@ -857,9 +870,11 @@ int launch(const Args &p, Kernel k, const Target &to) {
     // us, but 1999 x 14336 x 4096 in 128 against 112 (tiles of 128 x 128).
     auto alone = [&](int bm, int bw) { return row_tiles(p, bm) * tiles_of(p.N, SWI ? bw / 2 : bw) <= kCUs; };
     switch (k) {
-    case kFew8: return launch_few<1, SWI>(p, to);
-    case kFew16: return launch_few<2, SWI>(p, to);
-    case kFew32: return launch_few<4, SWI>(p, to);
+    case kFew8: return launch_few<1, 1, SWI>(p, to);
+    case kFew16: return launch_few<2, 1, SWI>(p, to);
+    case kFew32: return launch_few<4, 1, SWI>(p, to);
+    case kFew32x32: return launch_few<4, SWI ? 1 : 2, SWI>(p, to);
+    case kFew64: return launch_few<8, SWI ? 1 : 2, SWI, 4>(p, to);
     case kTile64: return launch_block<64, 128, 2, 4, 1, 3, SWI>(p, to);
     case kTileDeep:
         if (alone(64, 64)) return launch_block<64, 64, 2, 2, 2, 4, SWI>(p, to);

@@ -130,10 +130,10 @@ def test_gemm(M, N, K, t):
 # inside tiles and K inside steps, and more tiles than workgroups.
 LARGE = [(64, 4100, 2064), (500, 2050, 2064), (330, 4870, 912), (1090, 5000, 528), (3775, 1827, 1056),
          (3984, 3781, 656), (2900, 5050, 528), (4100, 4100, 272), (5000, 300, 4112), (64, 3999, 4112),
-         (230, 3313, 400), (36, 1373, 32)]
+         (230, 3313, 400), (36, 1373, 32), (126, 2093, 6016), (64, 4090, 14336), (128, 3990, 4112)]
 LARGE_SWIGLU = [(64, 2100, 2064), (300, 1000, 2064), (200, 2320, 912), (1060, 2500, 528), (2593, 1533, 800),
                 (2365, 3095, 432), (1500, 4100, 400), (96, 999, 4112), (67, 3422, 368), (40, 1100, 1040),
-                (40, 499, 8208), (40, 1373, 48)]
+                (40, 499, 8208), (40, 1373, 48), (100, 1789, 6160)]
 
 
 @pytest.mark.parametrize("M,N,K", LARGE)
@@ -192,10 +192,10 @@ def test_last_round_halved(M, N, K, groups, swiglu):
 
 
 def test_sizes_take_every_tile():
-    for mats, shapes, tiles in ((1, GEMM + LARGE, {(8,), (16,), (32,), (64, 64), (64, 128), (128, 128), (128, 256),
-                                                   (256, 256)}),
-                                (2, LARGE_SWIGLU, {(8,), (16,), (32,), (64, 32), (64, 64), (128, 64), (128, 128),
-                                                    (256, 128)})):
+    for mats, shapes, tiles in ((1, GEMM + LARGE, {(8,), (16,), (32,), (64, 32), (64, 64), (64, 128), (128, 128),
+                                                   (128, 256), (256, 256)}),
+                                (2, LARGE_SWIGLU, {(8,), (16,), (32,), (64, 16), (64, 32), (64, 64), (128, 64),
+                                                   (128, 128), (256, 128)})):
         got = [q4.gemm_i8_geometry(mats, *s) for s in shapes]
         seen = {(g["tile_rows"], g["tile_cols"]) for g in got} | {(g["tile_rows"],) for g in got}
         assert tiles <= seen, tiles - seen
@@ -642,7 +642,8 @@ def test_refusals_of_the_quantiser():
 def test_refusals_name_the_argument():
     a, w, sa, sw = dev(codes(1, 4, 64)), dev(codes(2, 8, 64)), dev(scales(3, 4)), dev(scales(4, 8))
     o = torch.tensor([0, 4], dtype=torch.int32, device=DEV)
-    cases = [(lambda: q4.gemm_i8(a, sa.double(), w, sw), "a_scales"), (lambda: q4.gemm_i8(a, sa, w, sw[:7]), "w_scales"),
+    cases = [(lambda: q4.gemm_i8(a, sa.double(), w, sw), "a_scales"),
+             (lambda: q4.gemm_i8(a, sa, w, sw[:7]), "w_scales"),
              (lambda: q4.gemm_i8(a, sa, w.t(), sw), "w"), (lambda: q4.gemm_i8(a, sa, w, sw, bias=sw.half()), "bias"),
              (lambda: q4.gemm_i8_swiglu(a, sa, (w, sw), (w, sw[:7])), "w_scales"),
              (lambda: q4.gemm_i8_swiglu(a, sa, (w, sw), (w.float(), sw)), "w"),
