@@ -866,8 +866,8 @@ Kernel choose(const Args &p, int mats) {
 template <bool SWI>
 int launch(const Args &p, Kernel k, const Target &to) {
     // Two workgroups share a CU with a ring of two stages; where there is only
-    // one for each CU, it takes four: 1024 x 4096 x 4096 in 19.0 against 24.1
-    // us, but 1999 x 14336 x 4096 in 128 against 112 (tiles of 128 x 128).
+    // one for each CU, it takes four: 1024 x 4096 x 4096 in 24.7 against 33.6
+    // us, but 2048 x 4096 x 1024 in 16.8 against 14.5 (tiles of 128 x 128).
     auto alone = [&](int bm, int bw) { return row_tiles(p, bm) * tiles_of(p.N, SWI ? bw / 2 : bw) <= kCUs; };
     switch (k) {
     case kFew8: return launch_few<1, 1, SWI>(p, to);

@@ -19,8 +19,8 @@ A = 0x10000          # fake, aligned, never dereferenced device address
 
 @pytest.fixture(scope="module")
 def L():
-    if not os.path.exists(q4.LIB_PATH):
-        from memory_bandwidth_amd import build
+    from memory_bandwidth_amd import build
+    if not os.path.exists(q4.LIB_PATH) or not os.path.exists(build.BIND):
         build.build()
     return q4.lib()
 
@@ -103,7 +103,7 @@ def test_no_device(L, fn):
     assert call(L, fn, 4, 8, 64) == q4.Q4_EDEVICE
 
 
-def test_binding_refuses_host_tensors_and_wrong_types():
+def test_binding_refuses_host_tensors_and_wrong_types(L):
     a, s = torch.zeros(2, 32, dtype=torch.int8), torch.ones(2)
     w, sw = torch.zeros(4, 32, dtype=torch.int8), torch.ones(4)
     with pytest.raises(ValueError):
@@ -114,6 +114,21 @@ def test_binding_refuses_host_tensors_and_wrong_types():
         q4.quant_i8(a)
     with pytest.raises(ValueError):
         q4.quant_i8(a.float())
+
+
+def test_module_returns_none_for_what_it_cannot_take(L):
+    m = q4._load_bind()
+    a, s = torch.zeros(2, 32, dtype=torch.int8), torch.ones(2)
+    w, sw = torch.zeros(4, 32, dtype=torch.int8), torch.ones(4)
+    good = [a, s, w, sw, None, None, torch.float32, None]
+    assert m.gemm(*good) is None                           # on the host
+    for i in range(8):
+        assert m.gemm(*good[:i], "no", *good[i + 1:]) is None
+    assert m.swiglu(a, s, w, sw, w, sw, None, torch.float32, None) is None
+    assert m.quant(a.float(), None, None) is None and m.quant(None, None, None) is None
+    for fn in (m.gemm, m.swiglu, m.quant):
+        with pytest.raises(TypeError):
+            fn(a)
 
 
 # Shapes (matrices, M, N, K, groups) and the tile of y that they take.
