@@ -869,6 +869,11 @@ int launch(const Args &p, Kernel k, const Target &to) {
     // one for each CU, it takes four: 1024 x 4096 x 4096 in 24.7 against 33.6
     // us, but 2048 x 4096 x 1024 in 16.8 against 14.5 (tiles of 128 x 128).
     auto alone = [&](int bm, int bw) { return row_tiles(p, bm) * tiles_of(p.N, SWI ? bw / 2 : bw) <= kCUs; };
+    // Two matrices halve the columns of a lane's run: four rows of wavefronts
+    // then store whole lines.  4096 x 2 x 14336 x 1024 takes 142 us so, 154 with
+    // two rows of four; one matrix is faster in two (8192 x 14336 x 4096 404
+    // and 460: the fragments of four spill).
+    constexpr int kM = SWI ? 4 : 2, kN = SWI ? 2 : 4;
     switch (k) {
     case kFew8: return launch_few<1, 1, SWI>(p, to);
     case kFew16: return launch_few<2, 1, SWI>(p, to);
@@ -880,23 +885,23 @@ int launch(const Args &p, Kernel k, const Target &to) {
         if (alone(64, 64)) return launch_block<64, 64, 2, 2, 2, 4, SWI>(p, to);
         return launch_block<64, 64, 2, 2, 2, 2, SWI>(p, to);
     case kTile128:
-        if (alone(128, 128)) return launch_block<128, 128, 2, 4, 1, 4, SWI>(p, to);
-        return launch_block<128, 128, 2, 4, 1, 2, SWI>(p, to);
-    case kTileWide: return launch_block<128, 256, 2, 4, 1, 3, SWI>(p, to);
+        if (alone(128, 128)) return launch_block<128, 128, kM, kN, 1, 4, SWI>(p, to);
+        return launch_block<128, 128, kM, kN, 1, 2, SWI>(p, to);
+    case kTileWide: return launch_block<128, 256, kM, kN, 1, 3, SWI>(p, to);
     default: {
         // Whole rounds, then the tiles that are left, divided.
         Args q = p;
         const int64_t all = row_tiles(p, 256) * tiles_of(p.N, SWI ? 128 : 256), left = all % kCUs;
         if (all >= kCUs && (p.offsets || (left && left <= kRestMost))) q.part = kWhole;
-        if (int st = launch_block<256, 256, 2, 4, 1, 2, SWI>(q, to)) return st;
+        if (int st = launch_block<256, 256, kM, kN, 1, 2, SWI>(q, to)) return st;
         if (q.part == kAll || to.report) return Q4_OK;
         if (p.offsets || left > kQuartersMost) {
             q.part = kHalves;
-            if (int st = launch_block<128, 256, 2, 4, 1, 3, SWI>(q, to)) return st;
+            if (int st = launch_block<128, 256, kM, kN, 1, 3, SWI>(q, to)) return st;
         }
         if (!p.offsets && left > kQuartersMost) return Q4_OK;
         q.part = kQuarters;
-        return launch_block<128, 128, 2, 4, 1, 4, SWI>(q, to);
+        return launch_block<128, 128, kM, kN, 1, 4, SWI>(q, to);
     }
     }
 }
