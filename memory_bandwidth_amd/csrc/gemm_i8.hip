@@ -194,32 +194,32 @@ __device__ __forceinline__ Tile find_tile(const Args &p, int bm, const Groups &g
 // Scales a wavefront's sums and writes them.  acc[i][..]: rows row0 + 16 i +
 // lane % 16 of the tile; over its fragments a lane holds the C columns from n
 // on (with SWI: C of gate in the first half of the fragments, C of up in the
-// second).  sa, sw0, sw1: the scales of the tile's rows and of the lane's
-// columns (sw1: of up), anything past N.
+// second).  sa: the scales of its rows; sw0, sw1: of its columns (sw1: of up, or
+// without SWI the bias where there is one), anything past N.
 template <int FM, int C, bool SWI>
 __device__ __forceinline__ void finish(const Args &p, const i32x4_t (&acc)[FM][SWI ? C / 2 : C / 4], const Tile &tl,
-                                       const float *sa, const float *sw0, const float *sw1, int row0, int n, int lane) {
-    float w[SWI ? 2 : 1][C], bias[C];
+                                       const float (&sa)[FM], const float *sw0, const float *sw1, int row0, int n,
+                                       int lane) {
+    float w[2][C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         w[0][c] = sw0[c];
-        if constexpr (SWI) w[SWI][c] = sw1[c];
-        bias[c] = !SWI && p.bias && n + c < p.N ? p.bias[n + c] : 0.f;
+        w[1][c] = SWI || p.bias ? sw1[c] : 0.f;
     }
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
         const int r = row0 + i * 16 + (lane & 15);
         if (r >= tl.rows) continue;
-        const float s = sa[r];
+        const float s = sa[i];
         float v[C];
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             if constexpr (SWI) {
                 const float g = (float)acc[i][c >> 2][c & 3] * s * w[0][c];
-                const float u = (float)acc[i][(C + c) >> 2][c & 3] * s * w[SWI][c];
+                const float u = (float)acc[i][(C + c) >> 2][c & 3] * s * w[1][c];
                 v[c] = silu(g) * u;
             } else {
-                v[c] = (float)acc[i][c >> 2][c & 3] * s * w[0][c] + bias[c];
+                v[c] = (float)acc[i][c >> 2][c & 3] * s * w[0][c] + w[1][c];
             }
         }
         store_run<C>(p, tl.m0 + r, n, v);
@@ -344,7 +344,7 @@ __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_i8_block(Args p) {
     constexpr int FM = BM / WM / 16, FW = BW / WN / 16, BN = SWI ? BW / 2 : BW;
     constexpr int W = WM * WN;                                      // wavefronts of a group
     constexpr int LX = BM / 8 / W, LW = BW / 8 / W, LOADS = LX + LW; // load instructions of one of them and step
-    constexpr int SLICE = (BM + BW) * BK, STAGE = G * SLICE;
+    constexpr int SLICE = (BM + BW) * BK, STAGE = G * SLICE, SCALES = BM + 2 * BN;
     extern __shared__ __align__(16) char lds[];
     const int tid = threadIdx.x, lane = tid & 63, all_waves = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wave = all_waves % W, group = all_waves / W;
@@ -353,7 +353,7 @@ __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_i8_block(Args p) {
     // Every wavefront leaves the same sums of the groups' tiles in LDS, and
     // finds its own there whenever it looks for a tile: a load from memory would
     // wait for all of the ring's.
-    Groups *groups = reinterpret_cast<Groups *>(lds + D * STAGE + 2 * (BM + BW) * 4) + lane;
+    Groups *groups = reinterpret_cast<Groups *>(lds + D * STAGE + 2 * SCALES * 4) + lane;
     const int bm = p.part >= kHalves ? 2 * BM : BM;
     *groups = groups_of(p, bm);
     const int tiles_m = tile_count(p, *groups), all = tiles_m * p.tiles_n, whole = whole_rounds(all);
@@ -444,13 +444,15 @@ __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_i8_block(Args p) {
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
     };
-    // The scales of a tile's rows and columns go behind the ring, 64 of them a
-    // wavefront: fetched at the end, they would cost a trip to memory there.
+    // The scales of a tile's rows and columns, and the bias, go behind the ring,
+    // 64 of them a wavefront: fetched at the end, they would cost a trip to
+    // memory there.
     float *scales = reinterpret_cast<float *>(lds + D * STAGE);
+    const int most = BM + BN + (SWI || p.bias ? BN : 0);
     auto load_scales = [&](const Place &at, float *to) {
-        for (int q = all_waves * 64; q < BM + BW; q += W * G * 64) {
+        for (int q = all_waves * 64; q < most; q += W * G * 64) {
             const int i = q + lane - BM, col = at.n0 + (i & (BN - 1));
-            const float *sw = SWI && i >= BN ? p.sw[1] : p.sw[0];
+            const float *sw = i < BN ? p.sw[0] : SWI ? p.sw[1] : p.bias;
             const float *from = i < 0 ? p.sa + at.tl.m0 + min(q + lane, at.tl.rows - 1)
                                       : sw + (size_t)at.tl.e * p.N + min(col, p.N - 1);
             load4(from, to + q);
@@ -504,7 +506,7 @@ __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_i8_block(Args p) {
             else wait_batches<LOADS, D - 2>(steps - t - 2);
             barrier();
             if (more) {
-                if (t + D == steps) load_scales(nxt, scales + (side ^ 1) * (BM + BW));
+                if (t + D == steps) load_scales(nxt, scales + (side ^ 1) * SCALES);
                 load(slot, t + D - steps);
             }
             if (t + 1 < steps) {
@@ -517,8 +519,11 @@ __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_i8_block(Args p) {
         }
         constexpr int C = SWI ? 2 * FW : 4 * FW;      // consecutive columns of a lane
         const int col = wn * (4 * C) + (lane >> 4) * C;
-        const float *sa = scales + side * (BM + BW), *sw0 = sa + BM + col, *sw1 = SWI ? sw0 + BN : sw0;
+        const float *mine = scales + side * SCALES, *sw0 = mine + BM + col, *sw1 = sw0 + BN;
         if constexpr (G == 1) {
+            float sa[FM];
+#pragma unroll
+            for (int i = 0; i < FM; ++i) sa[i] = mine[wm * (16 * FM) + i * 16 + (lane & 15)];
             finish<FM, C, SWI>(p, acc, cur.tl, sa, sw0, sw1, wm * (16 * FM), cur.n0 + col, lane);
         } else {
             // The groups' sums meet in the ring's place, and group g finishes
@@ -537,6 +542,7 @@ __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_i8_block(Args p) {
                 for (int g = 0; g < G; ++g)
 #pragma unroll
                     for (int j = 0; j < FW; ++j) sum[0][j] += part[(g * W * FM * FW + i * FW + j) * 64];
+                const float sa[1] = {mine[wm * (16 * FM) + i * 16 + (lane & 15)]};
                 finish<1, C, SWI>(p, sum, cur.tl, sa, sw0, sw1, wm * (16 * FM) + i * 16, cur.n0 + col, lane);
             }
             return;
@@ -590,6 +596,19 @@ __global__ __launch_bounds__(W * 64) void gemm_i8_few(Args p, int ks_log2) {
     const int kc = p.K >> 4, units = (kc + 7) >> 3;
     const int g = lane >> 4, r = lane & 15;
     i32x4_t acc[FM][FW] = {};
+    // Scales and bias of the lane's rows and columns, fetched before the ring's
+    // loads: at the end they would cost a trip to memory.
+    constexpr int C = 4 * FN;
+    const int n = n0 + g * C;
+    float sa[FM], sw[2][C];
+#pragma unroll
+    for (int i = 0; i < FM; ++i) sa[i] = p.sa[tl.m0 + min(i * 16 + r, tl.rows - 1)];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int at = min(n + c, p.N - 1);
+        sw[0][c] = p.sw[0][mat + at];
+        sw[1][c] = SWI ? p.sw[1][mat + at] : p.bias ? p.bias[at] : 0.f;
+    }
 
     if (n0 < p.N) {
         char *ring = lds + wave * (D * SLOT);
@@ -680,14 +699,7 @@ __global__ __launch_bounds__(W * 64) void gemm_i8_few(Args p, int ks_log2) {
 #pragma unroll
                 for (int j = 0; j < FW; ++j) acc[i][j] += part[((wave + k) * FM * FW + i * FW + j) * 64];
     }
-    constexpr int C = 4 * FN;
-    const int n = n0 + g * C;
-    float sw[MATS][C];
-#pragma unroll
-    for (int s = 0; s < MATS; ++s)
-#pragma unroll
-        for (int c = 0; c < C; ++c) sw[s][c] = n + c < p.N ? p.sw[s][mat + n + c] : 0.f;
-    finish<FM, C, SWI>(p, acc, tl, p.sa + tl.m0, sw[0], sw[MATS - 1], 0, n, lane);
+    finish<FM, C, SWI>(p, acc, tl, sa, sw[0], sw[1], 0, n, lane);
 }
 
 constexpr int kMaxRows = 1 << 24;
@@ -760,9 +772,9 @@ int launch_few(const Args &p, const Target &to) {
 
 template <int BM, int BW, int WM, int WN, int G, int D, bool SWI>
 int launch_block(Args p, const Target &to) {
-    constexpr int kLds = G * D * (BM + BW) * BK + 2 * (BM + BW) * 4 + 64 * (int)sizeof(Groups);
-    constexpr int kThreads = WM * WN * G * 64;
     constexpr int kBN = SWI ? BW / 2 : BW;
+    constexpr int kLds = G * D * (BM + BW) * BK + 2 * (BM + 2 * kBN) * 4 + 64 * (int)sizeof(Groups);
+    constexpr int kThreads = WM * WN * G * 64;
     p.tiles_m = (int)row_tiles(p, (p.part >= kHalves ? 2 : 1) * BM);
     p.tiles_n = (int)tiles_of(p.N, (p.part == kQuarters ? 2 : 1) * kBN);
     int64_t grid = (int64_t)p.tiles_m * p.tiles_n;
