@@ -377,12 +377,23 @@ __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_i8_block(Args p) {
     Place cur;
     if (!place(id, cur)) return;
 
+    // In the largest tiles, what a tile's start and end compute from the lane is
+    // computed anew each time.  Kept, it takes registers that the fragments
+    // need, and the spills' reloads wait for all of the ring's loads: 8192 x
+    // 8192 x 512 58 us so and 66.  128 x 256 tiles are 1.5% slower with it.
+    auto lane_anew = [&]() {
+        int l = tid & 63;
+        if constexpr (FM * FW >= 32) asm volatile("" : "+v"(l));
+        return l;
+    };
+
     // Loads: this wavefront brings an eighth of the rows of a and of w.
     // SWI: its weight rows are all gate or all up.
     const int8_t *wbase = SWI && wave * LW / 2 % FW >= FW / 2 ? p.w[1] : p.w[0];
     __amdgpu_buffer_rsrc_t ra, rw;
     uint32_t va[LX], vw[LW];
     auto aim = [&](const Place &at) {
+        const int lane = lane_anew();
         const int rows = at.tl.rows, cols = min(BN, p.N - at.n0), chunk = ((lane & 7) ^ (lane >> 3)) << 4;
         ra = rsrc_of(p.a + (size_t)at.tl.m0 * p.K, (uint32_t)rows * p.K);
         rw = rsrc_of(wbase + ((size_t)at.tl.e * p.N + at.n0) * p.K, (uint32_t)cols * p.K);
@@ -450,6 +461,7 @@ __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_i8_block(Args p) {
     float *scales = reinterpret_cast<float *>(lds + D * STAGE);
     const int most = BM + BN + (SWI || p.bias ? BN : 0);
     auto load_scales = [&](const Place &at, float *to) {
+        const int lane = lane_anew();
         for (int q = all_waves * 64; q < most; q += W * G * 64) {
             const int i = q + lane - BM, col = at.n0 + (i & (BN - 1));
             const float *sw = i < BN ? p.sw[0] : SWI ? p.sw[1] : p.bias;
@@ -518,6 +530,7 @@ __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_i8_block(Args p) {
             slot = next;
         }
         constexpr int C = SWI ? 2 * FW : 4 * FW;      // consecutive columns of a lane
+        const int lane = lane_anew();
         const int col = wn * (4 * C) + (lane >> 4) * C;
         const float *mine = scales + side * SCALES, *sw0 = mine + BM + col, *sw1 = sw0 + BN;
         if constexpr (G == 1) {
