@@ -27,8 +27,8 @@ constexpr int kCUs = 256;
 // would have up to 128, they go to a launch of their own (kHalves, 128 rows
 // each, where there are more than 64; kQuarters, 128 x 128, else), which takes
 // one round of two thirds or a third of the time: 4600 x 4096 x 14336 (32 tiles
-// left) takes 225 us so and 315 without, 5376 rows (80 left) 254 and 316 (287
-// as quarters, in two rounds), 9000 x 8192 x 8192 (128 left) 469 and 481.
+// left) takes 223 us so and 315 without, 5376 rows (80 left) 251 and 316 (287
+// as quarters, in two rounds), 9000 x 8192 x 8192 (128 left) 461 and 481.
 // With groups the count is the GPU's to know: both are launched, and one has
 // no work.
 enum Part { kAll, kWhole, kHalves, kQuarters };
@@ -282,14 +282,15 @@ constexpr int BK = 128;
 // stays inside the rows.  Rows past the tile's end repeat its last row, and
 // their results are not stored.
 //
-// At large sizes the bound is the card's power: with codes of a normal
-// distribution 8192^3 takes 430 us (2560 TOP/s; the library's int8 product
-// reaches 2150), with all codes zero 350, and products alone, fed from
-// registers, reach 3700 to 4000 TOP/s.  v_mfma_i32_32x32x32_i8 reaches 2900 to
-// 3300 there.  LDS reads are free of bank conflicts and take a quarter of the
-// time; fetching into the L2 ahead changes nothing but the run on zeros.  In
-// middle sizes it is what one CU can have under way to memory, 50 to 65 bytes
-// a ns, so that tiles are as large as still leaves one for each CU.
+// At large sizes the bound is how fast the card runs the products under load:
+// with codes of a normal distribution 8192^3 takes 409 us (2690 TOP/s; the
+// library's int8 product reaches 2130 on them), with all codes zero 378, and
+// products alone, fed from registers, reach 3700 to 4000 TOP/s.
+// v_mfma_i32_32x32x32_i8 reaches 2900 to 3300 there.  LDS reads are free of bank
+// conflicts and take a quarter of the time; fetching into the L2 ahead changes
+// nothing but the run on zeros.  In middle sizes it is what one CU can have
+// under way to memory, 50 to 65 bytes a ns, so that tiles are as large as still
+// leaves one for each CU.
 typedef __attribute__((address_space(3))) void *lds_ptr_t;
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void *base, uint32_t bytes) {
@@ -798,9 +799,9 @@ int launch_block(Args p, const Target &to) {
         grid = (p.offsets ? std::min<int64_t>(grid, most) : grid - whole_rounds((int)grid)) << (p.part - kHalves + 1);
     }
     // Workgroups that stay and go through the tiles, each loading its next one
-    // while it finishes the last: 8192 x 8192 x 512 takes 66 us so, 74 with a
-    // workgroup for each tile, x 1024 93 and 99; 8000 rows over 64 experts with
-    // SwiGLU, K = 1024, 113 and 125.  At long K tiles change rarely, and dealing
+    // while it finishes the last: 8192 x 8192 x 512 takes 58 us so, 66 with a
+    // workgroup for each tile, x 1024 87 and 95; 8000 rows over 64 experts with
+    // SwiGLU, K = 1024, 108 and 122.  At long K tiles change rarely, and dealing
     // them as CUs come free is better where they differ: 527 against 539 us
     // for 8190 rows over 8 experts, K = 14336.
     const int64_t steps = tiles_of(p.K, BK);
@@ -895,7 +896,7 @@ int launch(const Args &p, Kernel k, const Target &to) {
     // us, but 2048 x 4096 x 1024 in 16.8 against 14.5 (tiles of 128 x 128).
     auto alone = [&](int bm, int bw) { return row_tiles(p, bm) * tiles_of(p.N, SWI ? bw / 2 : bw) <= kCUs; };
     // Two matrices halve the columns of a lane's run: four rows of wavefronts
-    // then store whole lines.  4096 x 2 x 14336 x 1024 takes 142 us so, 154 with
+    // then store whole lines.  4096 x 2 x 14336 x 1024 takes 134 us so, 154 with
     // two rows of four; one matrix is faster in two (8192 x 14336 x 4096 404
     // and 460: the fragments of four spill).
     constexpr int kM = SWI ? 4 : 2, kN = SWI ? 2 : 4;
