@@ -582,7 +582,7 @@ __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_i8_block(Args p) {
 // activations of zero.  Up to a few hundred rows, where larger tiles leave
 // CUs idle, many such tiles are faster although each reads all its operands:
 // 64 x 2048 x 8192 takes 10.0 us in tiles of 32 rows, 21.7 in 64 x 64, 1024
-// columns of 4096 5.8 and 9.3.
+// columns of 4096 5.0 and 9.3.
 constexpr int kFewDepth = 2;
 
 template <int NX, int FN, bool SWI, int W>
