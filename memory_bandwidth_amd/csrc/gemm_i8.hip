@@ -55,7 +55,19 @@ struct Args {
 template <int F>
 __device__ __forceinline__ int frag_row(int j, int i) { return (i >> 2) * (4 * F) + 4 * j + (i & 3); }
 
+// silu(v) = v / (1 + e^-v) for v >= kFar, where 1 + e^-v is below the 2^126 that
+// the reciprocal takes.
+constexpr float kFar = -87.f;
 __device__ __forceinline__ float silu(float v) { return v * __builtin_amdgcn_rcpf(1.f + __expf(-v)); }
+
+// silu(v) u below that, where silu(v) is v e^v to the last bit: e^v comes to be no
+// normal number, and the product may still be any, so that it takes the two
+// halves of e^v one before u and one after (each is normal down to v = -174.6,
+// and zero below).
+__device__ __forceinline__ float far_silu(float v, float u) {
+    const float half = __builtin_amdgcn_exp2f(0.72134752044f * v);
+    return v * half * u * half;
+}
 
 __device__ __forceinline__ uint32_t bits16(float v, int type) {
     if (type == I8_F16) return (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)v);
@@ -211,15 +223,24 @@ __device__ __forceinline__ void finish(const Args &p, const i32x4_t (&acc)[FM][S
         const int r = row0 + i * 16 + (lane & 15);
         if (r >= tl.rows) continue;
         const float s = sa[i];
-        float v[C];
+        float v[C], least = 0.f;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             if constexpr (SWI) {
                 const float g = (float)acc[i][c >> 2][c & 3] * s * w[0][c];
                 const float u = (float)acc[i][(C + c) >> 2][c & 3] * s * w[1][c];
                 v[c] = silu(g) * u;
+                least = __builtin_fminf(least, g);
             } else {
                 v[c] = (float)acc[i][c >> 2][c & 3] * s * w[0][c] + w[1][c];
+            }
+        }
+        if (SWI && __builtin_expect(least < kFar, 0)) {
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const float g = (float)acc[i][c >> 2][c & 3] * s * w[0][c];
+                const float u = (float)acc[i][(SWI ? C + c : c) >> 2][c & 3] * s * w[1][c];
+                if (g < kFar) v[c] = far_silu(g, u);
             }
         }
         store_run<C>(p, tl.m0 + r, n, v);

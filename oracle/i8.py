@@ -51,16 +51,25 @@ def gemm(a, sa, w, sw, bias=None) -> tuple[np.ndarray, np.ndarray]:
 def swiglu(a, sa, gate, up) -> tuple[np.ndarray, np.ndarray]:
     """(y, bound) of silu(g) * u.
 
-    |silu'| <= 1.1, so g's own error dg gives 1.1 dg.  For a given g, the
-    exponential of -g is off by at most 3 U from the function and (2 |g| + 1) U
-    from its argument's scaling to base 2, which reach silu times a factor
-    below 1; the addition, the reciprocal (2 U) and two multiplies add 5 U."""
+    With c = 1 / (1 + e^g), the weight of a relative error of e^-g in silu(g) =
+    g / (1 + e^-g):
+    - g's own error dg reaches silu times silu'(g) = (1 + g c) / (1 + e^-g), and in
+      the second order times at most e^-|g| (2 + |g|) / 2;
+    - the exponential is off by 2 |g| U from its argument's scaling to base 2 and
+      by 4 U from the function, taken whole or as the product of two halves,
+      times c;
+    - its addition to 1 and the reciprocal add 3 U, the products 4 U.
+    An exponential below the normal numbers, past |g| = 174.6, may be taken as
+    zero, which leaves out less than |u| 2^-244; a product of two small values
+    may be subnormal on the way."""
     g, u = product(a, sa, *gate), product(a, sa, *up)
-    with np.errstate(over="ignore"):
+    with np.errstate(over="ignore", invalid="ignore"):
+        sig, c, size = 1.0 / (1.0 + np.exp(-g)), 1.0 / (1.0 + np.exp(g)), np.abs(g)
         s = g / (1.0 + np.exp(-g))
-    dg, du = 3.1 * U * np.abs(g), 3.1 * U * np.abs(u)
-    ds = 1.1 * dg + np.abs(s) * (2 * np.abs(g) + 9) * U
-    return s * u, 1.01 * (np.abs(u) * ds + np.abs(s) * du) + np.abs(u) * 2.0 ** -118
+        dg, du = 3.1 * U * size, 3.1 * U * np.abs(u)
+        ds = sig * np.abs(1.0 + g * c) * dg + 0.51 * dg * dg * np.exp(-size) * (2 + size)
+        ds += np.abs(s) * ((2 * size + 4) * c + 7) * U
+        return s * u, 1.01 * (np.abs(u) * ds + np.abs(s) * du) + np.abs(u) * (size > 174) * 2.0 ** -244 + 2.0 ** -150
 
 
 def groups(offsets) -> list[tuple[int, int, int]]:

@@ -704,3 +704,20 @@ def test_threads():
     torch.cuda.synchronize()
     for i in range(4):
         assert all(torch.equal(p, q) for p, q in zip(got[i], want[i]))
+
+
+# ---------------------------------------------------------------- far gates, other scales and operands, every launch
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+@pytest.mark.parametrize("M", [1, 12, 40, 300])
+def test_swiglu_gates_far_below_zero(M, t):
+    """Gates from 0 down to -170, whose silu is far below fp32's subnormal
+    numbers at the end, with an up projection that brings the product back."""
+    N, K = 260, 144
+    a, wg, wu = (np.zeros((rows, K), dtype=np.int8) for rows in (M, N, N))
+    a[:, 140], wg[:, 140] = 1, -(np.arange(N) % 129)
+    wu[:, 140] = np.arange(N) % 50 - 75
+    sa = np.resize(np.array([1, 0.71, 1.33, 0.69], dtype=np.float32), M)
+    gate, up = (wg, np.ones(N, dtype=np.float32)), (wu, np.full(N, 2.0 ** 110, dtype=np.float32))
+    y = q4.gemm_i8_swiglu(dev(a), dev(sa), tuple(map(dev, gate)), tuple(map(dev, up)), dtype=TYPES[t])
+    check(y, *i8.swiglu(a, sa, gate, up), t, f"{M}")
