@@ -459,22 +459,18 @@ def _load_bind():
     return _bind
 
 
-def _i8_refuse(tensors: dict, shapes: dict, dtype=None) -> None:
+def _i8_check(tensors: dict) -> None:
     """Raises for the first tensor of the wrong type, place or layout, then for
-    the first of the wrong shape.  tensors: name -> (tensor, dtypes); shapes:
-    name -> (tensor, shape), None in a shape where any size will do."""
-    if dtype is not None and dtype not in I8_TYPES:
-        raise TypeError(f"dtype must be float32, float16 or bfloat16, got {dtype}")
+    the first of the wrong shape.  tensors: name -> (tensor, dtypes, shape), None
+    in a shape where any size will do."""
     dev = None
-    for name, (t, dtypes) in tensors.items():
-        if t is not None:
-            _need(t, name, dtypes, dev)
-            dev = t.device
-    for name, (t, shape) in shapes.items():
-        if t is not None and (t.dim() != len(shape) or any(s is not None and s != n for s, n in zip(shape, t.shape))):
+    for name, (t, dtypes, _) in tensors.items():
+        _need(t, name, dtypes, dev)
+        dev = t.device
+    for name, (t, _, shape) in tensors.items():
+        if t.dim() != len(shape) or any(s is not None and s != n for s, n in zip(shape, t.shape)):
             want = ", ".join("*" if s is None else str(s) for s in shape)
             raise ValueError(f"{name} must be [{want}], got {list(t.shape)}")
-    raise ValueError("unsupported arguments")
 
 
 _I8, _F32, _I32 = torch.int8, torch.float32, torch.int32
@@ -486,16 +482,26 @@ def _size(t, d: int):
     return t.shape[d] if isinstance(t, torch.Tensor) and -t.dim() <= d < t.dim() else None
 
 
-def _i8_refuse_product(a, a_scales, w, w_scales, bias, offsets, grouped, out, dtype) -> None:
+def _i8_check_product(a, a_scales, w, w_scales, bias, offsets, grouped, out, dtype) -> None:
+    if dtype not in I8_TYPES:
+        raise TypeError(f"dtype must be float32, float16 or bfloat16, got {dtype}")
     E = (None if _size(offsets, 0) is None else _size(offsets, 0) - 1,) if grouped else ()
-    shape = (*E, _size(w, -2), _size(a, 1))
-    if grouped and offsets is None:
-        raise TypeError("offsets must be a torch.Tensor")
-    _i8_refuse({"a": (a, (_I8,)), "a_scales": (a_scales, (_F32,)), "w": (w, (_I8,)), "w_scales": (w_scales, (_F32,)),
-                "bias": (bias, (_F32,)), "offsets": (offsets, (_I32,)), "out": (out, (dtype,))},
-               {"a": (a, (None, None)), "a_scales": (a_scales, (_size(a, 0),)), "offsets": (offsets, (None,)),
-                "w": (w, shape), "w_scales": (w_scales, shape[:-1]), "bias": (bias, (shape[-2],)),
-                "out": (out, (_size(a, 0), shape[-2]))}, dtype)
+    M, N, K = _size(a, 0), _size(w, -2), _size(a, 1)
+    tensors = {"a": (a, (_I8,), (None, None)), "a_scales": (a_scales, (_F32,), (M,))}
+    if grouped:
+        tensors["offsets"] = (offsets, (_I32,), (None,))
+    tensors["w"] = (w, (_I8,), (*E, N, K))
+    tensors["w_scales"] = (w_scales, (_F32,), (*E, N))
+    if bias is not None:
+        tensors["bias"] = (bias, (_F32,), (N,))
+    if out is not None:
+        tensors["out"] = (out, (dtype,), (M, N))
+    _i8_check(tensors)
+
+
+def _i8_refuse_product(*args) -> None:
+    _i8_check_product(*args)
+    raise ValueError("unsupported arguments")
 
 
 def _i8_refuse_pair(a, a_scales, gate, up, offsets, grouped, out, dtype) -> None:
@@ -505,12 +511,8 @@ def _i8_refuse_pair(a, a_scales, gate, up, offsets, grouped, out, dtype) -> None
     if gate[0].shape != up[0].shape:
         raise ValueError(f"gate and up must have one shape, got {list(gate[0].shape)} and {list(up[0].shape)}")
     for w, w_scales in (gate, up):
-        try:
-            _i8_refuse_product(a, a_scales, w, w_scales, None, offsets, grouped, out, dtype)
-        except ValueError as e:
-            if w is gate[0] and str(e) == "unsupported arguments":
-                continue                               # gate is as it must be
-            raise
+        _i8_check_product(a, a_scales, w, w_scales, None, offsets, grouped, out, dtype)
+    raise ValueError("unsupported arguments")
 
 
 def quant_i8(x: torch.Tensor, out: tuple | None = None) -> tuple[torch.Tensor, torch.Tensor]:
@@ -526,8 +528,11 @@ def quant_i8(x: torch.Tensor, out: tuple | None = None) -> tuple[torch.Tensor, t
         _need(x, "x", _X_TYPES)
         if x.dim() != 2:
             raise ValueError(f"x must be [M, K], got {list(x.shape)}")
-        _i8_refuse({"x": (x, _X_TYPES), "codes": (codes, (_I8,)), "scales": (scales, (_F32,))},
-                   {"x": (x, (None, None)), "codes": (codes, x.shape), "scales": (scales, x.shape[:1])})
+        tensors = {"x": (x, _X_TYPES, (None, None))}
+        if out is not None:
+            tensors.update(codes=(codes, (_I8,), x.shape), scales=(scales, (_F32,), x.shape[:1]))
+        _i8_check(tensors)
+        raise ValueError("unsupported arguments")
     raise Q4Error("quant_i8", got)
 
 

@@ -721,3 +721,27 @@ def test_swiglu_gates_far_below_zero(M, t):
     gate, up = (wg, np.ones(N, dtype=np.float32)), (wu, np.full(N, 2.0 ** 110, dtype=np.float32))
     y = q4.gemm_i8_swiglu(dev(a), dev(sa), tuple(map(dev, gate)), tuple(map(dev, up)), dtype=TYPES[t])
     check(y, *i8.swiglu(a, sa, gate, up), t, f"{M}")
+
+
+def test_refusals_of_what_is_no_tensor():
+    """An operand that is missing or no tensor is refused by its name, in every call."""
+    a, w, sa, sw = dev(codes(1, 4, 64)), dev(codes(2, 8, 64)), dev(scales(3, 4)), dev(scales(4, 8))
+    o = torch.tensor([0, 4], dtype=torch.int32, device=DEV)
+    pair, pairs = (w, sw), (w[None], sw[None])
+    for bad in (None, 3, [1.0]):
+        cases = [(lambda: q4.gemm_i8(bad, sa, w, sw), "a "), (lambda: q4.gemm_i8(a, bad, w, sw), "a_scales "),
+                 (lambda: q4.gemm_i8(a, sa, bad, sw), "w "), (lambda: q4.gemm_i8(a, sa, w, bad), "w_scales "),
+                 (lambda: q4.gemm_i8_swiglu(bad, sa, pair, pair), "a "),
+                 (lambda: q4.gemm_i8_swiglu(a, bad, pair, pair), "a_scales "),
+                 (lambda: q4.gemm_i8_grouped(bad, sa, *pairs, o), "a "),
+                 (lambda: q4.gemm_i8_grouped(a, sa, *pairs, bad), "offsets "),
+                 (lambda: q4.gemm_i8_grouped_swiglu(bad, sa, pairs, pairs, o), "a "),
+                 (lambda: q4.gemm_i8_grouped_swiglu(a, bad, pairs, pairs, o), "a_scales "),
+                 (lambda: q4.gemm_i8_grouped_swiglu(a, sa, pairs, pairs, bad), "offsets "),
+                 (lambda: q4.quant_i8(bad), "x "),
+                 (lambda: q4.quant_i8(sa[None, :4].repeat(4, 16), out=(a, bad)), "scales "),
+                 (lambda: q4.quant_i8(sa[None, :4].repeat(4, 16), out=(bad, sa)), "codes ")]
+        for i, (call, name) in enumerate(cases):
+            with pytest.raises(TypeError, match="^" + name):
+                call()
+                pytest.fail(f"case {i} with {bad} was taken")

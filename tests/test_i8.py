@@ -131,6 +131,19 @@ def test_module_returns_none_for_what_it_cannot_take(L):
             fn(a)
 
 
+@pytest.mark.parametrize("bad", [None, 3, [1.0]])
+def test_binding_refuses_what_is_no_tensor(L, bad):
+    s, w, sw = torch.ones(2), torch.zeros(4, 32, dtype=torch.int8), torch.ones(4)
+    off = torch.zeros(2, dtype=torch.int32)
+    for call in (lambda: q4.gemm_i8(bad, s, w, sw), lambda: q4.gemm_i8_swiglu(bad, s, (w, sw), (w, sw)),
+                 lambda: q4.gemm_i8_grouped(bad, s, w[None], sw[None], off),
+                 lambda: q4.gemm_i8_grouped_swiglu(bad, s, (w[None], sw[None]), (w[None], sw[None]), off)):
+        with pytest.raises(TypeError, match="^a must be a torch.Tensor"):
+            call()
+    with pytest.raises(TypeError, match="^x must be a torch.Tensor"):
+        q4.quant_i8(bad)
+
+
 # Shapes (matrices, M, N, K, groups) and the tile of y that they take.
 PLANS = [((1, 1, 14336, 4096, 0), (8, 64)), ((1, 12, 4096, 4096, 0), (16, 16)), ((1, 24, 4096, 14336, 0), (32, 16)),
          ((1, 64, 4096, 14336, 0), (32, 32)), ((1, 64, 1024, 4096, 0), (16, 16)),
