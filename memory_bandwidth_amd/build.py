@@ -51,31 +51,32 @@ def _compile(src: str) -> str:
     return obj
 
 
-def build_bind() -> str:
+def _compile_bind() -> str:
     import torch
+    out = os.path.join(BUILD, os.path.basename(BIND))
     top = os.path.dirname(torch.__file__)
-    tmp = BIND + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-I", os.path.join(ROOT, "include"), "-I", os.path.join(top, "include"),
            "-I", os.path.join(top, "include", "torch", "csrc", "api", "include"),
-           "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "bind_i8.cpp"), "-o", tmp,
+           "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "bind_i8.cpp"), "-o", out,
            "-L", os.path.join(top, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
            f"-Wl,-rpath,{os.path.join(top, 'lib')}"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+    except FileNotFoundError as e:
+        raise RuntimeError("g++, which compiles bind_i8.cpp, is not installed") from e
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for bind_i8.cpp:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, BIND)
-    return BIND
+    return out
 
 
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     jobs = min(len(SOURCES) + 1, max(1, min(8, os.cpu_count() or 1)))
     with concurrent.futures.ThreadPoolExecutor(jobs) as ex:
-        bind = ex.submit(build_bind)
+        bind = ex.submit(_compile_bind)
         objs = list(ex.map(_compile, SOURCES))
-        bind.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -83,7 +84,18 @@ def build(verbose: bool = False) -> str:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
     if verbose:
-        print(f"built {LIB} and {BIND}")
+        print(f"built {LIB}")
+    # The library and every call but the 8-bit ones need no module: a machine
+    # that cannot compile it has them all the same.  A module built for another
+    # library could call it wrongly, so an older one goes.
+    try:
+        os.replace(bind.result(), BIND)
+    except Exception:
+        if os.path.exists(BIND):
+            os.remove(BIND)
+        raise
+    if verbose:
+        print(f"built {BIND}")
     return LIB
 
 
