@@ -445,14 +445,18 @@ _bind = None
 
 
 def _load_bind():
-    """The module, given the library's entry points; raises if either has not been built."""
+    """The module, given the library's entry points; raises if either has not been
+    built, or the module for another torch."""
     global _bind
     L = lib()
     try:
         from . import _bind_i8
     except ImportError as e:
-        raise RuntimeError("the module _bind_i8.so is not built; run "
+        raise RuntimeError("the module _bind_i8 is not built for this Python; run "
                            "`python -m memory_bandwidth_amd.build` first") from e
+    if _bind_i8.torch != torch.__version__:
+        raise RuntimeError(f"the module _bind_i8 is built for torch {_bind_i8.torch}, this is {torch.__version__}; "
+                           "run `python -m memory_bandwidth_amd.build` again")
     _bind_i8.init(getattr(torch._C, "_cuda_getCurrentRawStream", None),
                   *(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in EXPORTS_I8[:5]))
     _bind = _bind_i8

@@ -1,10 +1,11 @@
 """Compile the HIP library libq4gemv.so in-tree for gfx950, and the CPython
-module _bind_i8.so, which calls its 8-bit entry points.
+module _bind_i8, which calls its 8-bit entry points.
 
 Each source under csrc/ is compiled with hipcc to an object in _build/, in
 parallel, and the objects are linked into memory_bandwidth_amd/libq4gemv.so.
 The module is host code against torch's headers, compiled with the host
-compiler.
+compiler, and works with the Python and the torch it was built for: its name
+has the one's tag, and it knows the other's version.
 Run as ``python -m memory_bandwidth_amd.build`` (or through
 ``__graft_entry__.build()``).  Compiles every time it is called.
 """
@@ -22,7 +23,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libq4gemv.so")
-BIND = os.path.join(HERE, "_bind_i8.so")
+BIND = os.path.join(HERE, "_bind_i8" + sysconfig.get_config_var("EXT_SUFFIX"))
 SOURCES = ["api.cpp", "gemv_q4.hip", "gemv_f32.hip", "dequant_q4.hip", "probes.hip", "gemv_blocks.hip",
            "scan2.hip", "quant_i8.hip", "gemm_i8.hip"]
 ARCH = "gfx950"
@@ -57,6 +58,7 @@ def _compile_bind() -> str:
     top = os.path.dirname(torch.__file__)
     cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DBUILT_FOR_TORCH="{torch.__version__}"',
            "-I", os.path.join(ROOT, "include"), "-I", os.path.join(top, "include"),
            "-I", os.path.join(top, "include", "torch", "csrc", "api", "include"),
            "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "bind_i8.cpp"), "-o", out,

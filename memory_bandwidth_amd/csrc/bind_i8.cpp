@@ -237,4 +237,9 @@ PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_bind_i8", nullptr, -1, kMethods,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__bind_i8() { return PyModule_Create(&kModule); }
+PyMODINIT_FUNC PyInit__bind_i8() {
+    PyObject *m = PyModule_Create(&kModule);
+    // What the tensors' layout here is that of.
+    if (m && PyModule_AddStringConstant(m, "torch", BUILT_FOR_TORCH) < 0) Py_CLEAR(m);
+    return m;
+}

@@ -2,9 +2,12 @@
 
 import os
 import subprocess
+import sysconfig
 
 import pytest
+import torch
 
+import memory_bandwidth_amd as q4
 from memory_bandwidth_amd import build
 
 
@@ -66,3 +69,16 @@ def test_a_library_that_does_not_build_leaves_both_as_they_were(places):
     with pytest.raises(RuntimeError, match="hipcc failed"):
         build.build()
     assert open(build.LIB).read() == "old" and open(build.BIND).read() == "old"
+
+
+def test_the_module_is_for_one_python_and_one_torch(monkeypatch):
+    """Another Python does not find it, and another torch is refused."""
+    assert build.BIND.endswith("_bind_i8" + sysconfig.get_config_var("EXT_SUFFIX"))
+    if not os.path.exists(q4.LIB_PATH) or not os.path.exists(build.BIND):
+        build.build()
+    module = q4._load_bind()
+    assert module.__file__ == build.BIND and module.torch == torch.__version__
+    monkeypatch.setattr(q4, "_bind", None)
+    monkeypatch.setattr(torch, "__version__", "1.0.0")
+    with pytest.raises(RuntimeError, match="torch"):
+        q4.quant_i8(torch.zeros(1, 16))
