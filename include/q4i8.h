@@ -61,8 +61,8 @@ int gemm_i8(const int8_t *a, const float *a_scales, const int8_t *w, const float
             const float *bias, void *y, int y_type, int M, int N, int K, void *stream);
 
 /* SwiGLU block: with g = P of (w_gate, scales_gate) and u = P of (w_up,
- * scales_up), y[m, n] = silu(g) * u, silu(v) = v / (1 + e^-v), in one launch
- * that stores neither g nor u.  Before it is rounded to the output type, y is
+ * scales_up), y[m, n] = silu(g) * u, silu(v) = v / (1 + e^-v); neither g
+ * nor u is stored.  Before it is rounded to the output type, y is
  * within (5.2 |g| + 17) * 2^-24 of itself where g < 0 and 17 * 2^-24 elsewhere,
  * for g, u and y inside the range of fp32, however small silu(g) is; only for
  * g below -174 it may be 0 instead, an error below |u| * 2^-244. */
@@ -90,15 +90,20 @@ int gemm_i8_grouped_swiglu(const int8_t *a, const float *a_scales, const int8_t 
                            const int32_t *offsets, void *y, int y_type, int M, int E, int N, int K,
                            void *stream);
 
-/* Launch geometry of the products for a shape, for reporting and tests;
+/* Launch geometry of the products for a shape (one to three launches), for reporting and tests;
  * host-only, launches nothing and needs no device.  Any output pointer may be
  * NULL.  Q4_EINVAL for an invalid shape.
  *   matrices    1, or 2 for the SwiGLU forms
  *   E           groups, or 0 for a product without groups
  *   tile_rows, tile_cols   rows and columns of y that a workgroup makes at a
- *               time (a workgroup may go through several such tiles)
- *   grid        workgroups launched (groups: at most that many have work)
- *   block       threads per workgroup
+ *               time (a workgroup may go through several such tiles).  The
+ *               largest tiles that are left over after whole rounds of one
+ *               for each CU are divided into halves or quarters, in a launch
+ *               of their own; with groups, whose tiles the GPU counts, there
+ *               are launches for both, and one of them finds no work.
+ *   grid        workgroups of all launches (groups: at most that many have
+ *               work)
+ *   block       threads per workgroup, the same in every launch
  * All are 0 where nothing is launched. */
 int gemm_i8_geometry(int matrices, int M, int E, int N, int K, int *tile_rows, int *tile_cols,
                      int *grid, int *block);

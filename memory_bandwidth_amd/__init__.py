@@ -598,7 +598,8 @@ def gemm_i8_grouped_swiglu(a: torch.Tensor, a_scales: torch.Tensor, gate: tuple,
 
 def gemm_i8_geometry(matrices: int, M: int, N: int, K: int, groups: int = 0) -> dict:
     """Launch geometry of the products for a shape (host-only, needs no GPU):
-    matrices is 2 for the SwiGLU forms, groups 0 for a product without groups."""
+    matrices is 2 for the SwiGLU forms, groups 0 for a product without groups.
+    grid is the workgroups of all launches, the tile that of the first."""
     vals = [ctypes.c_int() for _ in range(4)]
     _check("gemm_i8_geometry", lib().gemm_i8_geometry(matrices, M, groups, N, K, *[ctypes.byref(v) for v in vals]))
     return dict(zip(("tile_rows", "tile_cols", "grid", "block"), (v.value for v in vals)))

@@ -751,9 +751,17 @@ int64_t row_tiles(const Args &p, int bm) {
     return p.offsets ? p.M / bm + std::min(p.E, p.M) : tiles_of(p.M, bm);
 }
 
-// Where a launch goes: to the stream, or into a report of its plan.
-struct Report { int rows, cols, grid, block; };
+// Where a call's launches go: to the stream, or into a report of their plan,
+// with the first one's tile and all workgroups.
+struct Report { int rows, cols; int64_t grid; int block; };
 struct Target { hipStream_t stream; Report *report; };
+
+int planned(const Target &to, int rows, int cols, int64_t grid, int block) {
+    Report &r = *to.report;
+    if (!r.grid) r = {rows, cols, 0, block};
+    r.grid += grid;
+    return Q4_OK;
+}
 
 // Wavefronts on one strip's K (log2) and in a workgroup of a few-rows kernel
 // of bm rows.  As many share K as it takes for 1536 wavefronts, 6 for each CU,
@@ -789,10 +797,7 @@ int launch_few(Args p, const Split &s, const Target &to) {
     p.tiles_n = (int)tiles_of(s.strips, W >> s.log2);
     const int64_t grid = s.tiles * p.tiles_n;
     if (grid * (W * 64) > kMaxThreads) return Q4_EINVAL;
-    if (to.report) {
-        *to.report = {8 * NX, (W >> s.log2) * 16 * FN, (int)grid, W * 64};
-        return Q4_OK;
-    }
+    if (to.report) return planned(to, 8 * NX, (W >> s.log2) * 16 * FN, grid, W * 64);
     gemm_i8_few<NX, FN, SWI, W><<<(unsigned)grid, W * 64, kLds, to.stream>>>(p, s.log2);
     return q4::launch_status();
 }
@@ -829,10 +834,7 @@ int launch_block(Args p, const Target &to) {
     if (G == 1 && p.part < kHalves && steps >= D && steps <= 64)
         grid = std::min<int64_t>(grid, kCUs * (160 * 1024 / kLds));
     else if (grid * kThreads > kMaxThreads) return Q4_EINVAL;
-    if (to.report) {
-        *to.report = {BM, SWI ? BW / 2 : BW, (int)grid, kThreads};
-        return Q4_OK;
-    }
+    if (to.report) return planned(to, BM, kBN, grid, kThreads);
     gemm_i8_block<BM, BW, WM, WN, G, D, SWI><<<(unsigned)grid, kThreads, kLds, to.stream>>>(p);
     return q4::launch_status();
 }
@@ -941,7 +943,7 @@ int launch(const Args &p, Kernel k, const Target &to) {
         const int64_t all = row_tiles(p, 256) * tiles_of(p.N, SWI ? 128 : 256), left = all % kCUs;
         if (all >= kCUs && (p.offsets || (left && left <= kRestMost))) q.part = kWhole;
         if (int st = launch_block<256, 256, kM, kN, 1, 2, SWI>(q, to)) return st;
-        if (q.part == kAll || to.report) return Q4_OK;
+        if (q.part == kAll) return Q4_OK;
         if (p.offsets || left > kQuartersMost) {
             q.part = kHalves;
             if (int st = launch_block<128, 256, kM, kN, 1, 3, SWI>(q, to)) return st;
@@ -1020,7 +1022,7 @@ extern "C" int gemm_i8_geometry(int matrices, int M, int E, int N, int K, int *t
     p.offsets = E ? &kGrouped : nullptr;
     if (matrices != 1 && matrices != 2) return Q4_EINVAL;
     if (int st = check_sizes(p)) return st;
-    Report r = {0, 0, 0, 0};
+    Report r = {};
     if (M > 0 && N > 0) {
         const Kernel k = choose(p, matrices);
         const Target to = {nullptr, &r};
@@ -1028,7 +1030,7 @@ extern "C" int gemm_i8_geometry(int matrices, int M, int E, int N, int K, int *t
     }
     if (tile_rows) *tile_rows = r.rows;
     if (tile_cols) *tile_cols = r.cols;
-    if (grid) *grid = r.grid;
+    if (grid) *grid = (int)r.grid;      // at most 2^30 and two parts of 256
     if (block) *block = r.block;
     return Q4_OK;
 }

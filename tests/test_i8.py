@@ -166,6 +166,31 @@ def test_geometry(L, shape, tile):
     assert g["grid"] == tiles or g["grid"] in (256, 512) and g["grid"] < tiles or E and tiles < g["grid"]
 
 
+# Shapes of the largest tiles, the workgroups of their whole rounds (256 that
+# stay, or one a tile from 65 steps on), and of what is left: tiles x 2 halves
+# or 4 quarters.
+LAST_ROUNDS = [((1, 8192, 14336, 4096), 256, 0), ((1, 4300, 4100, 2064), 256, 33 * 4),
+               ((1, 4096, 5300, 2000), 256, 80 * 2), ((1, 8200, 4097, 1040), 256, 49 * 4),
+               ((1, 4352, 8192, 9216), 512, 32 * 4), ((1, 4300, 2050, 2064), 153, 0),
+               ((2, 4300, 4100, 2064), 256, 49 * 4), ((2, 4096, 5300, 2000), 256, 0),
+               ((2, 8200, 4097, 1040), 256, 65 * 2), ((2, 4352, 8192, 9216), 1024, 64 * 4),
+               ((2, 4096, 4700, 9216), 512, 80 * 2)]
+
+
+@pytest.mark.parametrize("shape,whole,divided", LAST_ROUNDS)
+def test_geometry_counts_every_launch(L, shape, whole, divided):
+    assert q4.gemm_i8_geometry(*shape) == {"tile_rows": 256, "tile_cols": 256 // shape[0], "grid": whole + divided,
+                                           "block": 512}
+
+
+@pytest.mark.parametrize("mats", [1, 2])
+def test_geometry_of_groups_counts_every_launch(L, mats):
+    """With groups the GPU counts the tiles: a launch for each way they may be left."""
+    g = q4.gemm_i8_geometry(mats, 8190, 4096 // mats, 14336, 8)
+    tiles = (8190 // 256 + 8) * (4096 // 256)
+    assert g == {"tile_rows": 256, "tile_cols": 256 // mats, "grid": tiles + 2 * 128 + 4 * 64, "block": 512}
+
+
 def test_geometry_refusals(L):
     for shape in ((0, 4, 8, 64), (3, 4, 8, 64), (1, 4, 8, 24), (1, -1, 8, 64), (1, 4, 8, 64, -1),
                   (1, 2**24, 2**24, 64)):
