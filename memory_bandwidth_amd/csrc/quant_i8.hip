@@ -185,8 +185,8 @@ void launch_vectors(const u32x4_t *x, int8_t *codes, float *scales, int M, int K
     const int grid = TPR == 64 ? (M + 3) / 4 : M, block = TPR == 64 ? 256 : TPR, each = (nv + TPR - 1) / TPR;
     if (each <= 1) quant_rows<T, TPR, 1><<<grid, block, 0, s>>>(x, codes, scales, M, K);
     else if (each <= 2) quant_rows<T, TPR, 2><<<grid, block, 0, s>>>(x, codes, scales, M, K);
-    else if (each <= 4) quant_rows<T, TPR, 4><<<grid, block, 0, s>>>(x, codes, scales, M, K);
-    else quant_rows<T, TPR, 8><<<grid, block, 0, s>>>(x, codes, scales, M, K);
+    else if (TPR == 64 || each <= 4) quant_rows<T, TPR, 4><<<grid, block, 0, s>>>(x, codes, scales, M, K);
+    else if constexpr (TPR > 64) quant_rows<T, TPR, 8><<<grid, block, 0, s>>>(x, codes, scales, M, K);
 }
 
 template <typename T>

@@ -745,3 +745,34 @@ def test_refusals_of_what_is_no_tensor():
             with pytest.raises(TypeError, match="^" + name):
                 call()
                 pytest.fail(f"case {i} with {bad} was taken")
+
+
+# Rows and 16-byte vectors a row for each form of the quantiser: 64 threads a row
+# take up to 4 vectors each (past one, only from 2048 rows on), 256 up to 8 (past
+# one, only from 512 rows on), 1024 up to 8, and longer rows are read twice.
+# Rows end inside the threads' last vectors and workgroups of four rows.
+QUANT_FORMS = [(6, 4), (2051, 64), (2051, 68), (2050, 132), (2049, 252),
+               (7, 68), (515, 256), (515, 260), (514, 516), (513, 1028), (515, 2044),
+               (9, 260), (3, 1024), (3, 1028), (5, 2052), (3, 4100), (2, 8192), (3, 8196)]
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("M,vectors", QUANT_FORMS)
+def test_quant_every_form(t, M, vectors):
+    K = vectors * (4 if t == "f32" else 8)
+    rng = np.random.default_rng(M * K)
+    x = rng.standard_normal((M, K), dtype=np.float32) * rng.uniform(0.01, 30, (M, 1)).astype(np.float32)
+    x[np.arange(M), rng.integers(0, K, M)] *= 9            # the largest one anywhere in a row
+    x[M - 1, K - 1] = -200                                 # and in the last vector of the last
+    x[M // 2] = 0
+    if M > 2:
+        x[1, K - 2] = np.inf
+    xt = torch.from_numpy(x).to(TYPES[t])
+    buf = torch.full((M * K + 32,), 77, dtype=torch.int8, device=DEV)
+    ends = torch.full((M + 8,), 7.0, device=DEV)
+    c, s = q4.quant_i8(xt.to(DEV), out=(buf[16:16 + M * K].view(M, K), ends[4:4 + M]))
+    cw, sw = i8.quant(xt.double().numpy())
+    assert np.array_equal(s.cpu().numpy(), sw, equal_nan=True)
+    assert np.array_equal(c.cpu().numpy(), cw)
+    assert (buf[:16] == 77).all() and (buf[16 + M * K:] == 77).all()
+    assert (ends[:4] == 7).all() and (ends[4 + M:] == 7).all()
