@@ -776,3 +776,100 @@ def test_quant_every_form(t, M, vectors):
     assert np.array_equal(c.cpu().numpy(), cw)
     assert (buf[:16] == 77).all() and (buf[16 + M * K:] == 77).all()
     assert (ends[:4] == 7).all() and (ends[4 + M:] == 7).all()
+
+
+@pytest.mark.parametrize("M", [1, 9, 40, 100, 600])
+def test_swiglu_rows_and_columns_do_not_mix(M):
+    """Scales of NaN and Inf in either matrix and a zero row stay in their rows and columns."""
+    N, K = 150, 400
+    a, sa = codes(1, M, K), small_scales(3, K, M)
+    gate, up = (codes(2, N, K), small_scales(4, K, N)), (codes(5, N, K), small_scales(6, K, N))
+    a[M // 2] = 0
+    sa[M - 1] = np.nan if M > 1 else 1
+    gate[1][3], gate[1][70], up[1][5], up[1][149] = np.inf, np.nan, np.nan, np.inf
+    with np.errstate(invalid="ignore"):
+        want, bound = i8.swiglu(a, sa, gate, up)
+    y = q4.gemm_i8_swiglu(dev(a), dev(sa), tuple(map(dev, gate)), tuple(map(dev, up))).cpu().numpy()
+    fine = np.isfinite(want)
+    assert fine[:, [0, 4, 6, 148]][:M - 1].all()
+    assert np.array_equal(np.isnan(y), np.isnan(want)) and np.array_equal(np.isposinf(y), np.isposinf(want))
+    assert np.array_equal(np.isneginf(y), np.isneginf(want))
+    assert (np.abs(y[fine] - want[fine]) <= i8.tolerance(want, bound, "f32")[fine]).all()
+
+
+# A bias in every tile: columns past the end, K inside a step, workgroups that go
+# on to a next tile, and a last round in halves and in quarters.
+BIAS = [(1, 896, 896), (12, 333, 4096), (36, 1373, 32), (24, 512, 2816), (64, 4090, 2064), (100, 896, 4864),
+        (500, 2050, 2064), (330, 4870, 912), (1090, 5000, 528), (3775, 1827, 1056), (3984, 3781, 656),
+        (5000, 300, 4112), (128, 3990, 4112), (56, 5099, 1984), (4209, 132, 400), (5511, 186, 8432),
+        (2307, 3403, 256), (3099, 5093, 1328), (4300, 4100, 2064), (4096, 5300, 2000), (8200, 4097, 1040)]
+
+
+@pytest.mark.parametrize("M,N,K", BIAS)
+def test_bias_in_every_tile(M, N, K):
+    a, w, sa, sw = codes(1, M, K), codes(2, N, K), small_scales(3, K, M), small_scales(4, K, N)
+    b = np.random.default_rng(5).standard_normal(N).astype(np.float32) * 3
+    y = q4.gemm_i8(dev(a), dev(sa), dev(w), dev(sw), bias=dev(b))
+    want = exact_rows(a, sa, w, sw)
+    bound = 3.1 * i8.U * want.abs()
+    want = want + dev(b).double()
+    bound = bound + 1.1 * i8.U * want.abs()                # as i8.gemm
+    assert ((y.double() - want).abs() <= bound + i8.U * (want.abs() + bound)).all()
+
+
+def test_bias_takes_every_tile():
+    got = [q4.gemm_i8_geometry(1, *s) for s in BIAS]
+    tiles = [(g["tile_rows"], g["tile_cols"]) for g in got]
+    assert {8, 16, 32} <= {r for r, c in tiles}
+    assert {(32, 32), (64, 32), (64, 64), (64, 128), (128, 128), (128, 256), (256, 256)} <= set(tiles)
+    count = [-(-m // r) * -(-n // c) for (m, n, _), (r, c) in zip(BIAS, tiles)]
+    # Workgroups that go through several tiles, with one matrix's bias past 512 scales and below.
+    assert {(128, 128), (128, 256), (256, 256)} <= {t for t, n, g in zip(tiles, count, got) if g["grid"] < n}
+    # More workgroups than the 256 that stay: the divided tiles' launch, as halves and as quarters.
+    parts = {(g["grid"] - 256) // (n % 256) for t, n, g in zip(tiles, count, got) if t == (256, 256) and g["grid"] > 256}
+    assert parts == {2, 4}
+
+
+# Shapes of groups for every tile of 64 rows and more, with a workgroup for each
+# tile and with workgroups that go through several.
+GROUPED = [(1, 6615, 68, 400, 4), (1, 7191, 129, 144, 2), (1, 862, 1201, 272, 78), (1, 4301, 392, 128, 71),
+           (1, 3698, 1170, 144, 49), (1, 1158, 7078, 128, 21), (1, 4051, 1805, 288, 66), (1, 7309, 2014, 416, 2),
+           (1, 6435, 2432, 128, 2), (1, 2358, 6584, 144, 1), (2, 6222, 33, 144, 6), (2, 7043, 33, 144, 48),
+           (2, 2457, 407, 272, 77), (2, 5320, 199, 128, 51), (2, 1461, 1344, 144, 28), (2, 989, 3873, 128, 20),
+           (2, 3305, 1193, 272, 53), (2, 942, 7243, 416, 1), (2, 3696, 2272, 128, 2), (2, 4726, 1543, 144, 3)]
+
+
+def test_grouped_shapes_take_every_tile():
+    seen = set()
+    for mats, M, N, K, E in GROUPED:
+        g = q4.gemm_i8_geometry(mats, M, N, K, E)
+        most = (M // g["tile_rows"] + E) * -(-N // g["tile_cols"])
+        seen.add((mats, g["tile_rows"], g["tile_cols"] * mats, "each" if g["grid"] == most else
+                  "several" if g["grid"] < most else "divided"))
+    want = {(m, *t, k) for m in (1, 2) for t in ((64, 128), (128, 128), (128, 256)) for k in ("each", "several")}
+    want |= {(m, *t) for m in (1, 2) for t in ((64, 64, "each"), (256, 256, "each"), (256, 256, "divided"))}
+    assert want <= seen, want - seen
+
+
+@pytest.mark.parametrize("mats,M,N,K,E", GROUPED)
+def test_grouped_in_every_tile(mats, M, N, K, E):
+    """Uneven groups, some empty, with rows before the first and behind the last."""
+    rng = np.random.default_rng(M)
+    share = rng.uniform(0.05, 1, E) ** 2
+    share[rng.random(E) < 0.2] = 0
+    share[E // 2] += 0.3
+    off = 3 + np.concatenate([[0], np.cumsum(rng.multinomial(M - 8, share / share.sum()))])
+    a, sa = codes(1, M, K), small_scales(3, K, M)
+    gate, up = [(codes(s, E, N, K), small_scales(s + 1, K, E, N)) for s in (2, 5)]
+    out = torch.full((M, N), 7.0, device=DEV)
+    o = torch.tensor(off, dtype=torch.int32, device=DEV)
+    if mats == 2:
+        q4.gemm_i8_grouped_swiglu(dev(a), dev(sa), tuple(map(dev, gate)), tuple(map(dev, up)), o, out=out)
+    else:
+        q4.gemm_i8_grouped(dev(a), dev(sa), *map(dev, gate), o, out=out)
+    got = out.cpu().numpy().astype(np.float64)
+    for e, lo, hi in i8.groups(off):
+        g, u = (gate[0][e], gate[1][e]), (up[0][e], up[1][e])
+        want, bound = i8.swiglu(a[lo:hi], sa[lo:hi], g, u) if mats == 2 else i8.gemm(a[lo:hi], sa[lo:hi], *g)
+        assert (np.abs(got[lo:hi] - want) <= i8.tolerance(want, bound, "f32")).all(), f"expert {e}"
+    assert (got[:off[0]] == 7).all() and (got[off[-1]:] == 7).all()
