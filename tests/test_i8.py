@@ -229,3 +229,96 @@ def test_oracle_swiglu_and_bias_worked_values():
     y, _ = i8.gemm(a, sa, *g, bias=np.array([10], dtype=np.float32))
     assert y[0, 0] == 13
     assert i8.groups([0, 2, 2, 5]) == [(0, 0, 2), (2, 2, 5)]
+
+
+# ---------------------------------------------------------------- the bounds, against fp32 arithmetic
+
+F = np.float32
+
+
+def fp32_product(a, sa, w, sw):
+    """The steps of include/q4i8.h: the exact sum, converted, times a_scales, times w_scales."""
+    acc = (a.astype(np.int64) @ w.astype(np.int64).T).astype(F)
+    return acc * sa[:, None] * sw[None, :]
+
+
+def fp32_swiglu(g, u):
+    """silu(g) * u in fp32 as the header defines it, far gates through e^g in two halves."""
+    with np.errstate(over="ignore", invalid="ignore", under="ignore"):
+        near = g * (F(1) / (F(1) + np.exp2(-g * F(np.log2(np.e))))) * u
+        half = np.exp2(g * F(np.log2(np.e) / 2))
+        return np.where(g < F(-87), g * half * u * half, near)
+
+
+def inside(got, want, bound, t="f32"):
+    """Whether each value is inside what the GPU's are held to."""
+    return np.abs(got.astype(np.float64) - want) <= i8.tolerance(want, bound, t)
+
+
+def bound_problem(seed=1, M=9, N=200, K=912):
+    rng = np.random.default_rng(seed)
+    a, wg, wu = (rng.integers(-128, 128, (r, K), dtype=np.int8) for r in (M, N, N))
+    sa, sg, su = ((rng.uniform(0.5, 2, r) / (74 * K ** 0.25)).astype(F) for r in (M, N, N))
+    return a, sa, (wg, sg * F(4)), (wu, su), (rng.standard_normal(N) * 3).astype(F)
+
+
+def test_bounds_hold_fp32_steps_and_little_more():
+    a, sa, gate, up, bias = bound_problem()
+    p = fp32_product(a, sa, *gate)
+    want, bound = i8.gemm(a, sa, *gate)
+    assert inside(p, want, bound).all()
+    assert np.max(np.abs(p - want) / bound) > 0.1
+    want, bound = i8.gemm(a, sa, *gate, bias=bias)
+    assert inside(p + bias, want, bound).all()
+    # One rounding fewer: the last product and the addition in one step.
+    one = ((a.astype(np.int64) @ gate[0].astype(np.int64).T).astype(F) * sa[:, None]).astype(np.float64)
+    assert inside((one * gate[1].astype(np.float64) + bias).astype(F), want, bound).all()
+    want, bound = i8.swiglu(a, sa, gate, up)
+    y = fp32_swiglu(p, fp32_product(a, sa, *up))
+    assert inside(y, want, bound).all()
+    assert np.max(np.abs(y - want) / bound) > 0.1
+
+
+def test_bounds_refuse_mistakes():
+    """What is computed a little wrongly is outside, in most places and not only in one."""
+    a, sa, gate, up, bias = bound_problem()
+    p, u = fp32_product(a, sa, *gate), fp32_product(a, sa, *up)
+    want, bound = i8.gemm(a, sa, *gate, bias=bias)
+    for name, y in {"P in fp16": p.astype(np.float16).astype(F) + bias, "no bias": p,
+                    "the next column's bias": p + np.roll(bias, 1),
+                    "the next row's scale": fp32_product(a, np.roll(sa, 1), *gate) + bias,
+                    "the next column's scale": fp32_product(a, sa, gate[0], np.roll(gate[1], 1)) + bias,
+                    "one product less": fp32_product(a[:, :-1], sa, gate[0][:, :-1], gate[1]) + bias,
+                    "scales in fp16": fp32_product(a, sa.astype(np.float16).astype(F), *gate) + bias}.items():
+        assert inside(y, want, bound).mean() < 0.1, name
+    want, bound = i8.swiglu(a, sa, gate, up)
+    for name, y in {"gate and up exchanged": fp32_swiglu(u, p), "g in fp16": fp32_swiglu(p.astype(np.float16).astype(F), u),
+                    "u in fp16": fp32_swiglu(p, u.astype(np.float16).astype(F)),
+                    "no silu": p * u, "sigmoid": p / (F(1) + np.exp(-F(1.702) * p)) * u}.items():
+        assert inside(y, want, bound).mean() < 0.1, name
+    # The exponential, where it has a say: its half step of 2^-12 or more times its weight 1 / (1 + e^g) > 0.1.
+    near = np.abs(p + 1) < 3
+    y = p * (F(1) / (F(1) + np.exp(np.where(near, -p, 0)).astype(np.float16).astype(F))) * u
+    assert inside(y, want, bound)[near].mean() < 0.1
+
+
+@pytest.mark.parametrize("size", [2.0 ** 110, 1e-3])
+def test_bounds_of_far_gates(size):
+    """Gates from -174 to 174, with up products that bring silu's small values back or do not."""
+    g = np.linspace(-128, 127, 256).astype(np.int8)[:, None]
+    one, scale = np.ones((1, 1), dtype=np.int8), np.array([1.36], dtype=F)
+    sa, up = np.ones(256, dtype=F), (one, np.array([size], dtype=F))
+    a = np.concatenate([g, np.ones_like(g)], axis=1)
+    gate, up = (np.array([[1, 0]], dtype=np.int8), scale), (np.array([[0, 1]], dtype=np.int8), up[1])
+    want, bound = i8.swiglu(a, sa, gate, up)
+    v, u = fp32_product(a, sa, *gate), fp32_product(a, sa, *up)
+    y = fp32_swiglu(v, u)
+    assert inside(y, want, bound).all()
+    # The bound that q4i8.h gives.
+    rel = np.where(v < 0, 5.2 * np.abs(v) + 17, 17).astype(np.float64) * i8.U * np.abs(want)
+    assert (bound <= rel + np.abs(u.astype(np.float64)) * (v < -174) * 2.0 ** -244 + 2.0 ** -149).all()
+    if size > 1:
+        with np.errstate(over="ignore", under="ignore"):
+            lost = v * np.where(F(1) + np.exp(-v) < 2.0 ** 126, F(1) / (F(1) + np.exp(-v)), F(0)) * u
+        far = (v < -87.4)[:, 0]
+        assert not inside(lost, want, bound)[far].any() and inside(lost, want, bound)[~far].all()
