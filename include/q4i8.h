@@ -14,7 +14,8 @@
  * to fp32 once, multiplied by a_scales[m], then by w_scales[n], in fp32, and
  * rounded to the output type once, at the end: for values inside the range
  * of fp32 and of the output type each product is within 3.1 * 2^-24 of
- * itself before that last rounding.  A scale that is Inf or NaN makes its
+ * itself before that last rounding (with a bias, the sum is rounded once
+ * more).  A scale that is Inf or NaN makes its
  * row or column Inf or NaN as fp32 arithmetic does.
  *
  * Conventions are those of q4gemv.h: device pointers owned by the caller,

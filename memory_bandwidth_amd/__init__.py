@@ -4,8 +4,9 @@ Every function has the name of the C entry point it calls and only marshals
 arguments: it checks dtypes, shapes, contiguity and device, passes raw device
 pointers and torch's current HIP stream, and raises Q4Error on a non-zero
 status.  (The 8-bit calls do so in C++, by the module _bind_i8.)  All arithmetic
-runs in the library's HIP kernels; there is no other implementation here.  Importing this module without the built library works
-(so CPU-only tooling can inspect it), but every call then raises.
+runs in the library's HIP kernels; there is no other implementation here.
+Importing this module without the built library works (so CPU-only tooling can
+inspect it), but every call then raises; without _bind_i8 the 8-bit ones do.
 
 Storage format (see include/q4gemv.h): x float32 [M, K]; wq uint8 [N, K/2]
 (two codes per byte, low nibble = even k); scales float16 or uint16 [N, K/g]
@@ -522,8 +523,8 @@ def _i8_refuse_pair(a, a_scales, gate, up, offsets, grouped, out, dtype) -> None
 def quant_i8(x: torch.Tensor, out: tuple | None = None) -> tuple[torch.Tensor, torch.Tensor]:
     """(codes int8 [M, K], scales float32 [M]) of x [M, K], float32, float16 or
     bfloat16: scales[m] = max|x[m]| / 127 and codes = x / scales to the nearest
-    integer.  K is a multiple of 16.  A row with an Inf or a NaN gets the scale
-    NaN and zero codes."""
+    integer.  K is a multiple of 16, M below 2^22.  A row with an Inf or a NaN
+    gets the scale NaN and zero codes."""
     codes, scales = (None, None) if out is None else out
     got = (_bind or _load_bind()).quant(x, codes, scales)
     if type(got) is tuple:

@@ -409,7 +409,7 @@ __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_i8_block(Args p) {
         return l;
     };
 
-    // Loads: this wavefront brings an eighth of the rows of a and of w.
+    // Loads: this wavefront brings 1 / W of the rows of a and of w.
     // SWI: its weight rows are all gate or all up.
     const int8_t *wbase = SWI && wave * LW / 2 % FW >= FW / 2 ? p.w[1] : p.w[0];
     __amdgpu_buffer_rsrc_t ra, rw;
@@ -843,23 +843,26 @@ enum Kernel { kFew8, kFew16, kFew32, kFew32x32, kFew64, kTile64, kTile128, kTile
 
 // The kernel for a call's sizes.  Up to 8 rows the weights' stream decides.
 // Above that, each kernel's time is estimated, with constants fitted to
-// measured shapes: the tiles to 320 (33 to 8192 rows, N 64 to 14336, K 256 to
-// 14336, one matrix and two), in us a tile, us a step, and how far more tiles
-// than CUs stretch it; tiles that have a CU to themselves come in whole rounds.
+// measured shapes (up to six matrices in turn, so that small ones came from the
+// cache): the tiles to 320 (33 to 8192 rows, N 64 to 14336, K 256 to 14336, one
+// matrix and two), in us a tile, us a step, and how far more tiles than CUs
+// stretch it; tiles that have a CU to themselves come in whole rounds.
 // The kernels of few rows to 1070 (9 to 3000 rows): us a unit of a wavefront
 // alone and for each of the CU's, and, as they read weights past the L2 again
 // for every row tile, us a MB of weights.  The choice is on average 1.2%
-// behind the best of the nine there.  64 x 4096 x 14336 takes 21.2 us in tiles
+// behind the best of the nine there, but now and then far more: 512 x 4096 x
+// 14336 goes to 128 x 128, 68.0 us, and takes 54.9 in 64 x 128.  64 x 4096 x 14336 takes 21.2 us in tiles
 // of 32 x 32, 26.4 in 32 x 16, 28.4 in 64 x 32, 36.7 in 64 x 64; at 128 rows
 // these are 32.9, 41.3, 26.8 and 36.3.
 // Groups go by their average rows, their sizes being known to the GPU alone.
-// Measured over 64 experts of 2 x 2816 x 1024, at 4, 32 and 128 rows each: 16
-// rows a tile 73, 133, - us, 64 rows 69, 82, 133, 128 rows 72, 90, 115, 256
-// rows 103, 119, 145.  Over 8 experts of 4096 x 14336, at 256 rows each:
-// 128 rows a tile 218 us, 256 rows 192; of 2 x 4096 x 4096, at 512 rows 168
-// and 174, at 2048 535 and 504.  Where that leaves CUs idle, the estimates
-// decide, a group ending inside a tile half way: 769 rows over 3 experts of
-// 643 x 3648 take 12.1 us in tiles of 64 x 64, 30.3 in 128 x 256.  Over 220
+// Measured with uneven groups, as a router makes them, over 64 experts of 2 x
+// 2816 x 1024, at 4, 32 and 128 rows on average: 16 rows a tile 49, 97, 248 us,
+// 64 rows 63, 87, 138, 128 x 256 64, 91, 116, 256 rows 87, 116, 153.  Over 8
+// experts of 4096 x 14336, at 256 rows: 128 x 256 226 us, 256 rows 187 (135 and
+// 154 where all have 256); of 2 x 4096 x 4096, at 512 rows 168 and 165, at 2048
+// 558 and 501.  Where that leaves CUs idle, the estimates decide, a group ending
+// inside a tile half way: 769 rows over 3 experts of 643 x 3648 take 11.7 us in
+// tiles of 64 x 64, 30.1 in 128 x 256.  Over 220
 // calls (2 to 128 experts, 0.5 to 300 rows each) the choice is on average 2.7%
 // behind the best.
 Kernel choose(const Args &p, int mats) {

@@ -826,7 +826,8 @@ def test_bias_takes_every_tile():
     # Workgroups that go through several tiles, with one matrix's bias past 512 scales and below.
     assert {(128, 128), (128, 256), (256, 256)} <= {t for t, n, g in zip(tiles, count, got) if g["grid"] < n}
     # More workgroups than the 256 that stay: the divided tiles' launch, as halves and as quarters.
-    parts = {(g["grid"] - 256) // (n % 256) for t, n, g in zip(tiles, count, got) if t == (256, 256) and g["grid"] > 256}
+    parts = {(g["grid"] - 256) // (n % 256) for t, n, g in zip(tiles, count, got)
+             if t == (256, 256) and g["grid"] > 256}
     assert parts == {2, 4}
 
 

@@ -292,7 +292,8 @@ def test_bounds_refuse_mistakes():
                     "scales in fp16": fp32_product(a, sa.astype(np.float16).astype(F), *gate) + bias}.items():
         assert inside(y, want, bound).mean() < 0.1, name
     want, bound = i8.swiglu(a, sa, gate, up)
-    for name, y in {"gate and up exchanged": fp32_swiglu(u, p), "g in fp16": fp32_swiglu(p.astype(np.float16).astype(F), u),
+    for name, y in {"gate and up exchanged": fp32_swiglu(u, p),
+                    "g in fp16": fp32_swiglu(p.astype(np.float16).astype(F), u),
                     "u in fp16": fp32_swiglu(p, u.astype(np.float16).astype(F)),
                     "no silu": p * u, "sigmoid": p / (F(1) + np.exp(-F(1.702) * p)) * u}.items():
         assert inside(y, want, bound).mean() < 0.1, name
