@@ -235,6 +235,9 @@ __device__ __forceinline__ void finish(const Args &p, const i32x4_t (&acc)[FM][S
                 v[c] = (float)acc[i][c >> 2][c & 3] * s * w[0][c] + w[1][c];
             }
         }
+        // Far gates are rare, and without one this costs nothing that shows (8192 x
+        // 2 x 4096 x 512 46.9 us, 47.1 without the branch); one formula that holds
+        // for all gates took 49.5 against 45.5 there.
         if (SWI && __builtin_expect(least < kFar, 0)) {
 #pragma unroll
             for (int c = 0; c < C; ++c) {
