@@ -38,6 +38,10 @@ EXPORTS = ("gemv_q4", "gemv_q4_ws", "gemv_q4_workspace_size", "gemv_q4_static", 
 EXPORTS_I8 = ("quant_i8", "gemm_i8", "gemm_i8_swiglu", "gemm_i8_grouped", "gemm_i8_grouped_swiglu",
               "gemm_i8_geometry")
 
+# Exported C symbols, in the order include/q4f8.h declares them.
+EXPORTS_F8 = ("quant_f8", "quant_f8_block", "gemm_f8", "gemm_f8_swiglu", "gemm_f8_swiglu_backward",
+              "gemm_f8_geometry")
+
 # Element types of include/q4i8.h.
 I8_F32, I8_F16, I8_BF16 = 0, 1, 2
 I8_TYPES = {torch.float32: I8_F32, torch.float16: I8_F16, torch.bfloat16: I8_BF16}
@@ -98,7 +102,14 @@ def lib() -> ctypes.CDLL:
     L.gemm_i8_grouped.argtypes = [P, P, P, P, P, P, I, I, I, I, I, P]
     L.gemm_i8_grouped_swiglu.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, I, P]
     L.gemm_i8_geometry.argtypes = [I, I, I, I, I, IP, IP, IP, IP]
-    for f in EXPORTS_I8:
+    Q = ctypes.c_int64
+    L.quant_f8.argtypes = [P, I, P, P, Q, Q, I, I, P]
+    L.quant_f8_block.argtypes = [P, I, P, P, P, P, I, I, P]
+    L.gemm_f8.argtypes = [P, P, Q, Q, I, P, P, P, P, I, I, I, I, P]
+    L.gemm_f8_swiglu.argtypes = [P, P, Q, Q, I, P, P, P, P, P, I, I, I, I, P]
+    L.gemm_f8_swiglu_backward.argtypes = [P, I, P, P, Q, Q, I, P, P, P, P, P, I, I, I, I, P]
+    L.gemm_f8_geometry.argtypes = [I, I, I, I, I, IP, IP, IP, IP]
+    for f in EXPORTS_I8 + EXPORTS_F8:
         getattr(L, f).restype = ctypes.c_int
     L.q4_strerror.argtypes = [I]
     L.q4_strerror.restype = ctypes.c_char_p
@@ -460,6 +471,7 @@ def _load_bind():
                            "run `python -m memory_bandwidth_amd.build` again")
     _bind_i8.init(getattr(torch._C, "_cuda_getCurrentRawStream", None),
                   *(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in EXPORTS_I8[:5]))
+    _bind_i8.init_f8(*(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in EXPORTS_F8[:5]))
     _bind = _bind_i8
     return _bind
 
@@ -603,4 +615,175 @@ def gemm_i8_geometry(matrices: int, M: int, N: int, K: int, groups: int = 0) -> 
     grid is the workgroups of all launches, the tile that of the first."""
     vals = [ctypes.c_int() for _ in range(4)]
     _check("gemm_i8_geometry", lib().gemm_i8_geometry(matrices, M, groups, N, K, *[ctypes.byref(v) for v in vals]))
+    return dict(zip(("tile_rows", "tile_cols", "grid", "block"), (v.value for v in vals)))
+
+
+# ---------------------------------------------------------------- 8-bit floating point
+#
+# Codes are torch.float8_e4m3fn; a scale stands for 128 values of a row, or for a
+# block of 128 x 128.
+
+_F8 = torch.float8_e4m3fn
+
+
+def _blocks(n):
+    return None if n is None else -(-n // 128)
+
+
+def _f8_check(tensors: dict, strided: str) -> None:
+    """_i8_check, where the tensor named `strided` may have any strides."""
+    t, dtypes, shape = tensors.get(strided, (None, None, None))
+    if isinstance(t, torch.Tensor) and t.layout == torch.strided:
+        tensors[strided] = (t.new_empty(t.shape), dtypes, shape)
+    _i8_check(tensors)
+
+
+def _f8_check_product(a, a_scales, w, w_scales, bias, dtype, out, width=1, dh=None) -> None:
+    if dtype not in I8_TYPES:
+        raise TypeError(f"dtype must be float32, float16 or bfloat16, got {dtype}")
+    M, N, K = _size(a, 0), _size(w, 0), _size(a, 1)
+    rows = _blocks(M) if _size(a_scales, 0) == _blocks(M) else M
+    tensors = {"a": (a, (_F8,), (None, None)), "a_scales": (a_scales, (_F32,), (rows, _blocks(K))),
+               "w": (w, (_F8,), (N, K)), "w_scales": (w_scales, (_F32,), (_blocks(N), _blocks(K)))}
+    if bias is not None:
+        tensors["bias"] = (bias, (_F32,), (N,))
+    if dh is not None:
+        tensors["dh"] = (dh[0], _X_TYPES, (M, N))
+    if out is not None:
+        tensors["out"] = (out, (dtype,), (M, None if N is None else width * N))
+    _f8_check(tensors, "a_scales")
+
+
+def _f8_refuse_product(*args) -> None:
+    _f8_check_product(*args)
+    raise ValueError("unsupported arguments")
+
+
+def _f8_refuse_pair(a, a_scales, gate, up, dtype, out, width=1, dh=None) -> None:
+    for w, w_scales in (gate, up):
+        if not isinstance(w, torch.Tensor) or not isinstance(w_scales, torch.Tensor):
+            raise TypeError("gate and up must each be (weights, scales), two torch.Tensors")
+    if gate[0].shape != up[0].shape:
+        raise ValueError(f"gate and up must have one shape, got {list(gate[0].shape)} and {list(up[0].shape)}")
+    for w, w_scales in (gate, up):
+        _f8_check_product(a, a_scales, w, w_scales, None, dtype, out, width, dh)
+    raise ValueError("unsupported arguments")
+
+
+def _f8_refuse_input(x, given: dict, rows: bool) -> None:
+    _need(x, "x", _X_TYPES)
+    if x.dim() != 2:
+        raise ValueError(f"x must be [rows, columns], got {list(x.shape)}")
+    _f8_check({"x": (x, _X_TYPES, (None, None)), **given}, "scales" if rows else "")
+    raise ValueError("unsupported arguments")
+
+
+def quant_f8(x: torch.Tensor, out: tuple | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+    """(codes float8_e4m3fn [M, K], scales float32 [M, ceil(K / 128)]) of x [M, K], float32,
+    float16 or bfloat16: a scale is the largest magnitude of its 128 values / 448, a
+    code the e4m3 value nearest to x / scale.  K is a multiple of 16, M below
+    2^22.  A block with an Inf or a NaN gets the scale NaN and zero codes.
+
+    New scales lie block by block (their .t() is contiguous), as the products read
+    them best; scales given with out may have any strides."""
+    codes, scales = (None, None) if out is None else out
+    got = (_bind or _load_bind()).quant_f8(x, codes, scales)
+    if type(got) is tuple:
+        return got
+    if got is None:
+        shape = (_size(x, 0), _size(x, 1))
+        _f8_refuse_input(x, {} if out is None else {
+            "codes": (codes, (_F8,), shape), "scales": (scales, (_F32,), (shape[0], _blocks(shape[1])))}, True)
+    raise Q4Error("quant_f8", got)
+
+
+def quant_f8_block(x: torch.Tensor, layout: str = "rows", out: tuple | None = None) -> tuple:
+    """x [R, C] (float32, float16 or bfloat16, C a multiple of 16) to codes with
+    a scale for each 128 x 128 block, by quant_f8's rule.  By layout:
+
+      "rows"     (codes [R, C], scales [ceil(R / 128), ceil(C / 128)])
+      "columns"  (codes [C, R16], scales [ceil(C / 128), ceil(R / 128)]) of the transpose, R16 = R
+                 rounded up to a multiple of 16 and the codes behind R zero
+      "both"     all four, from one pass
+
+    The codes of a value are the same in both."""
+    if layout not in ("rows", "columns", "both"):
+        raise ValueError(f"layout must be 'rows', 'columns' or 'both', got {layout!r}")
+    as_is, turned = layout != "columns", layout != "rows"
+    names = ("codes", "scales") * as_is + ("codes_t", "scales_t") * turned
+    if out is not None and len(out) != len(names):
+        raise ValueError(f"out must be ({', '.join(names)})")
+    given = dict(zip(names, out)) if out is not None else {}
+    got = (_bind or _load_bind()).quant_block_f8(
+        x, as_is, turned, *(given.get(n) for n in ("codes", "scales", "codes_t", "scales_t")))
+    if type(got) is tuple:
+        return got
+    if got is None:
+        R, C = _size(x, 0) or 0, _size(x, 1) or 0
+        shapes = {"codes": (R, C), "scales": (_blocks(R), _blocks(C)), "codes_t": (C, -(-R // 16) * 16),
+                  "scales_t": (_blocks(C), _blocks(R))}
+        _f8_refuse_input(x, {n: (t, (_F8,) if n.startswith("codes") else (_F32,), shapes[n])
+                             for n, t in given.items()}, False)
+    raise Q4Error("quant_f8_block", got)
+
+
+def gemm_f8(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
+            bias: torch.Tensor | None = None, dtype=torch.float32,
+            out: torch.Tensor | None = None) -> torch.Tensor:
+    """y[M, N] = dequant(a)[M, K] . dequant(w)[N, K]^T (+ bias[N]).
+
+    a and w float8_e4m3fn; a_scales float32 [M, ceil(K / 128)], of any strides, or
+    one for each block of 128 rows too, [ceil(M / 128), ceil(K / 128)]; w_scales
+    float32 [ceil(N / 128), ceil(K / 128)]; bias float32.  y is of `dtype`
+    (float32, float16 or bfloat16).  K is a multiple of 16.  For float32 the
+    products are exact and their sums of fp32's accuracy; for 16 bits the matrix
+    cores' 8-bit products are used, which are twice as fast and whose rounding
+    (include/q4f8.h) is below that of the output."""
+    y = (_bind or _load_bind()).gemm_f8(a, a_scales, w, w_scales, bias, dtype, out)
+    if y is None:
+        _f8_refuse_product(a, a_scales, w, w_scales, bias, dtype, out)
+    if type(y) is int:
+        raise Q4Error("gemm_f8", y)
+    return y
+
+
+def gemm_f8_swiglu(a: torch.Tensor, a_scales: torch.Tensor, gate: tuple, up: tuple,
+                   dtype=torch.float32, out: torch.Tensor | None = None) -> torch.Tensor:
+    """y = silu(g) * u with g, u the gemm_f8 of a with gate and up, each (w, w_scales); neither is stored."""
+    (wg, sg), (wu, su) = gate, up
+    y = (_bind or _load_bind()).swiglu_f8(a, a_scales, wg, sg, wu, su, dtype, out)
+    if y is None:
+        _f8_refuse_pair(a, a_scales, gate, up, dtype, out)
+    if type(y) is int:
+        raise Q4Error("gemm_f8_swiglu", y)
+    return y
+
+
+def gemm_f8_swiglu_backward(dh: torch.Tensor, a: torch.Tensor, a_scales: torch.Tensor, gate: tuple, up: tuple,
+                            dtype=torch.float32, out: torch.Tensor | None = None) -> torch.Tensor:
+    """The gradients of gemm_f8_swiglu's g and u, side by side: d [M, 2 N] for dh [M, N],
+    the gradient of y (float32, float16 or bfloat16).
+
+    g and u are computed again.  The gradient of the activations is d . [Wg; Wu] and
+    that of [Wg; Wu] is d^T . x, both gemm_f8 of d's codes: of quant_f8(d) with the
+    weights' quant_f8_block(.., "columns"), and of quant_f8_block(d, "columns") with
+    quant_f8_block(x, "columns")."""
+    (wg, sg), (wu, su) = gate, up
+    d = None if dh is None else \
+        (_bind or _load_bind()).swiglu_backward_f8(dh, a, a_scales, wg, sg, wu, su, dtype, out)
+    if d is None:
+        _f8_refuse_pair(a, a_scales, gate, up, dtype, out, 2, (dh,))
+    if type(d) is int:
+        raise Q4Error("gemm_f8_swiglu_backward", d)
+    return d
+
+
+def gemm_f8_geometry(matrices: int, M: int, N: int, K: int, dtype=torch.float32) -> dict:
+    """Launch geometry of the products for a shape and output type (host-only, needs no
+    GPU): matrices is 2 for the gated forms.  grid is the workgroups of all
+    launches, the tile that of the first."""
+    if dtype not in I8_TYPES:
+        raise TypeError(f"dtype must be float32, float16 or bfloat16, got {dtype}")
+    vals = [ctypes.c_int() for _ in range(4)]
+    _check("gemm_f8_geometry", lib().gemm_f8_geometry(matrices, I8_TYPES[dtype], M, N, K, *[ctypes.byref(v) for v in vals]))
     return dict(zip(("tile_rows", "tile_cols", "grid", "block"), (v.value for v in vals)))

@@ -25,7 +25,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libq4gemv.so")
 BIND = os.path.join(HERE, "_bind_i8" + sysconfig.get_config_var("EXT_SUFFIX"))
 SOURCES = ["api.cpp", "gemv_q4.hip", "gemv_f32.hip", "dequant_q4.hip", "probes.hip", "gemv_blocks.hip",
-           "scan2.hip", "quant_i8.hip", "gemm_i8.hip"]
+           "scan2.hip", "quant_i8.hip", "gemm_i8.hip", "quant_f8.hip", "gemm_f8.hip"]
+BIND_SOURCES = ["bind_i8.cpp", "bind_f8.cpp"]
 ARCH = "gfx950"
 
 # Packed-FP32 instructions stay off: the code never asks for them and the
@@ -61,15 +62,15 @@ def _compile_bind() -> str:
            f'-DBUILT_FOR_TORCH="{torch.__version__}"',
            "-I", os.path.join(ROOT, "include"), "-I", os.path.join(top, "include"),
            "-I", os.path.join(top, "include", "torch", "csrc", "api", "include"),
-           "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "bind_i8.cpp"), "-o", out,
+           "-I", sysconfig.get_paths()["include"], *(os.path.join(CSRC, s) for s in BIND_SOURCES), "-o", out,
            "-L", os.path.join(top, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
            f"-Wl,-rpath,{os.path.join(top, 'lib')}"]
     try:
         r = subprocess.run(cmd, capture_output=True, text=True)
     except FileNotFoundError as e:
-        raise RuntimeError("g++, which compiles bind_i8.cpp, is not installed") from e
+        raise RuntimeError("g++, which compiles bind_i8.cpp and bind_f8.cpp, is not installed") from e
     if r.returncode != 0:
-        raise RuntimeError(f"g++ failed for bind_i8.cpp:\n{r.stdout}\n{r.stderr}")
+        raise RuntimeError(f"g++ failed for bind_i8.cpp and bind_f8.cpp:\n{r.stdout}\n{r.stderr}")
     return out
 
 

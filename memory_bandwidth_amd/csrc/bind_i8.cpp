@@ -7,65 +7,20 @@
 // current stream.  It returns the output, None where an argument is not what
 // it must be (the caller then finds out which, and raises), or the entry
 // point's error status.
-#include <torch/csrc/Dtype.h>
-#include <torch/csrc/Exceptions.h>
-#include <torch/csrc/autograd/python_variable.h>
-
-#include <ATen/ATen.h>
-#include <c10/core/DeviceGuard.h>
-
-#include <climits>
-
-#include "q4i8.h"
+#include "bind.h"
 
 namespace {
 
-// The entry points, from the loaded library, and torch's lookup of a device's
-// current stream.
+using namespace q4py;
+
+// The entry points, from the loaded library.
 struct {
     decltype(&quant_i8) quant;
     decltype(&gemm_i8) gemm;
     decltype(&gemm_i8_swiglu) swiglu;
     decltype(&gemm_i8_grouped) grouped;
     decltype(&gemm_i8_grouped_swiglu) grouped_swiglu;
-    PyObject *stream_of;
 } g;
-
-const at::Tensor *tensor(PyObject *o) { return THPVariable_Check(o) ? &THPVariable_Unpack(o) : nullptr; }
-
-// A contiguous tensor of a type and shape on a device of the GPUs.
-bool is(const at::Tensor *t, at::ScalarType type, int dev, at::IntArrayRef shape) {
-    return t && t->scalar_type() == type && t->is_cuda() && t->get_device() == dev && t->sizes() == shape &&
-           t->is_contiguous();
-}
-
-int type_code(at::ScalarType t) {
-    return t == at::kFloat ? I8_F32 : t == at::kHalf ? I8_F16 : t == at::kBFloat16 ? I8_BF16 : -1;
-}
-
-bool fits_int(int64_t v) { return v <= INT_MAX; }
-
-// A device made current for a call, and its current stream.
-struct OnDevice {
-    c10::DeviceGuard guard;
-    void *stream = nullptr;
-    bool fine = false;
-    explicit OnDevice(const at::Tensor &t) : guard(t.device()) {
-        PyObject *d = PyLong_FromLong(t.get_device());
-        PyObject *s = d ? PyObject_CallFunctionObjArgs(g.stream_of, d, nullptr) : nullptr;
-        Py_XDECREF(d);
-        if (!s) return;
-        stream = PyLong_AsVoidPtr(s);
-        Py_DECREF(s);
-        fine = !PyErr_Occurred();
-    }
-};
-
-// Python may run meanwhile: allocating and launching can wait for the GPU.
-struct NoGil {
-    PyThreadState *state = PyEval_SaveThread();
-    ~NoGil() { PyEval_RestoreThread(state); }
-};
 
 // What all products share: the rows, the output's type and the output.
 struct Rows {
@@ -105,15 +60,6 @@ int64_t experts(const Rows &r, const at::Tensor *offsets) {
     const int64_t E = offsets->size(0) - 1;
     return is(offsets, at::kInt, r.dev, {E + 1}) ? E : -1;
 }
-
-PyObject *finish(int status, PyObject *given, const at::Tensor &y) {
-    if (status != Q4_OK) return PyLong_FromLong(status);
-    if (given != Py_None) return Py_NewRef(given);
-    return THPVariable_Wrap(y);
-}
-
-template <typename T>
-T *ptr(const at::Tensor *t) { return static_cast<T *>(t->data_ptr()); }
 
 // gemm(a, a_scales, w, w_scales, bias, offsets, dtype, out): offsets None for
 // a product without groups.
@@ -213,16 +159,16 @@ PyObject *quant(PyObject *, PyObject *const *args, Py_ssize_t n) {
 
 // init(stream_of, addresses): the entry points in the order of g.
 PyObject *init(PyObject *, PyObject *args) {
-    PyObject *stream_of;
+    PyObject *lookup;
     unsigned long long a[5];
-    if (!PyArg_ParseTuple(args, "OKKKKK", &stream_of, a, a + 1, a + 2, a + 3, a + 4)) return nullptr;
+    if (!PyArg_ParseTuple(args, "OKKKKK", &lookup, a, a + 1, a + 2, a + 3, a + 4)) return nullptr;
     g.quant = reinterpret_cast<decltype(g.quant)>(a[0]);
     g.gemm = reinterpret_cast<decltype(g.gemm)>(a[1]);
     g.swiglu = reinterpret_cast<decltype(g.swiglu)>(a[2]);
     g.grouped = reinterpret_cast<decltype(g.grouped)>(a[3]);
     g.grouped_swiglu = reinterpret_cast<decltype(g.grouped_swiglu)>(a[4]);
-    Py_INCREF(stream_of);
-    Py_XSETREF(g.stream_of, stream_of);
+    Py_INCREF(lookup);
+    Py_XSETREF(stream_of, lookup);
     Py_RETURN_NONE;
 }
 
@@ -240,6 +186,7 @@ PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_bind_i8", nullptr, -1, kMethods,
 PyMODINIT_FUNC PyInit__bind_i8() {
     PyObject *m = PyModule_Create(&kModule);
     // What the tensors' layout here is that of.
-    if (m && PyModule_AddStringConstant(m, "torch", BUILT_FOR_TORCH) < 0) Py_CLEAR(m);
+    if (m && (PyModule_AddFunctions(m, kF8Methods) < 0 || PyModule_AddStringConstant(m, "torch", BUILT_FOR_TORCH) < 0))
+        Py_CLEAR(m);
     return m;
 }

@@ -1,0 +1,919 @@
+// gemm_f8.hip -- products of e4m3 activations and weights with a scale for each
+// block of 128, for gfx950 (see q4f8.h):
+//
+//     P[m, n] = sum_b sa[m, b] sw[n / 128, b] sum_{k in block b} a[m, k] w[n, k]
+//
+// plain, as a gated block of two matrices, and that block's backward pass.
+//
+// A block's sum is what a step of 128 bytes makes: one matrix instruction of
+// 16 x 16 x 128 (or four of 16 x 16 x 32) from zero, then a fused multiply-add
+// by the scales into the sums, 4 values a lane.  The weights are the first
+// operand, so that a lane holds one row m, and one factor sa sw serves
+// all its values of a step: a wavefront's columns lie in one block of 128.
+//
+// Two ways to multiply:
+//   fp8   v_mfma_f32_16x16x128_f8f6f4.  It brings the products of eight
+//         consecutive k to the exponent of the largest and drops what is below
+//         2^-13 of that: 1.5 * 2^-16 of the result (normal codes; measured
+//         against float64).  For outputs of 16 bits.  From registers, with the
+//         multiply-adds, 3670 TFLOP/s (4420 without them).
+//   f16   v_cvt_scalef32_pk_f16_fp8, which is exact, and
+//         v_mfma_f32_16x16x32_f16, whose sums are within 2^-26 (same codes).
+//         For float32 outputs, and for few rows, where the weights' stream decides.
+//         1860 TFLOP/s, conversions and all.
+#include "q4_common.h"
+#include "q4f8.h"
+#include "q4_tiles.h"
+
+#include <algorithm>
+
+namespace {
+
+using namespace q4;
+
+typedef int i32x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+
+enum Mode { kPlain, kGated, kBackward };
+
+struct Args {
+    const uint8_t *a;
+    const float *sa;
+    int64_t sa_m, sa_k;
+    int sa_shift;              // 0: a row of scales for each row, 7: for each block of 128
+    const uint8_t *w[2];       // one matrix, or gate and up
+    const float *sw[2];
+    const float *bias;
+    const void *dh;
+    void *y;
+    int dh_type, y_type, M, N, K;
+    int tiles_m, tiles_n;      // kHalves, kQuarters: of the tiles that are divided
+    Part part;
+    bool once;                 // the weights' stream is more than a cache would keep
+    bool share;                // several row tiles read the same weights
+};
+
+// A lane's 32 bytes of a fragment (16 rows of 128): chunks lane / 16 and lane /
+// 16 + 4 of row lane % 16.  Which k they are is the same for both operands.
+struct Raw { i32x4_t lo, hi; };
+
+template <bool F16> struct Operand;
+template <> struct Operand<false> {
+    i32x8_t v;
+    __device__ __forceinline__ void set(const Raw &r) {
+        v = i32x8_t{r.lo[0], r.lo[1], r.lo[2], r.lo[3], r.hi[0], r.hi[1], r.hi[2], r.hi[3]};
+    }
+};
+template <> struct Operand<true> {
+    f16x8_t v[4];
+    __device__ __forceinline__ static f16x8_t wide(int a, int b) {
+        const f16x2_t p = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.f, false);
+        const f16x2_t q = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.f, true);
+        const f16x2_t r = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.f, false);
+        const f16x2_t s = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.f, true);
+        return f16x8_t{p[0], p[1], q[0], q[1], r[0], r[1], s[0], s[1]};
+    }
+    __device__ __forceinline__ void set(const Raw &r) {
+        v[0] = wide(r.lo[0], r.lo[1]);
+        v[1] = wide(r.lo[2], r.lo[3]);
+        v[2] = wide(r.hi[0], r.hi[1]);
+        v[3] = wide(r.hi[2], r.hi[3]);
+    }
+};
+
+// Sums of one block: 16 weight rows by 16 rows, from zero.
+__device__ __forceinline__ f32x4_t block_sum(const Operand<false> &w, const Operand<false> &x) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w.v, x.v, f32x4_t{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4_t block_sum(const Operand<true> &w, const Operand<true> &x) {
+    f32x4_t t = {0, 0, 0, 0};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) t = __builtin_amdgcn_mfma_f32_16x16x32_f16(w.v[q], x.v[q], t, 0, 0, 0);
+    return t;
+}
+
+// Adds a block's sums times their scales.
+__device__ __forceinline__ void add_scaled(f32x4_t &acc, const f32x4_t &t, float s) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) acc[r] = __builtin_fmaf(t[r], s, acc[r]);
+}
+
+// A scale that all lanes read alike, through the scalar cache.  A vector load
+// would wait behind the ring's.
+typedef const float __attribute__((address_space(4))) uniform_float;
+__device__ __forceinline__ float uniform_load(const float *p) {
+    return *reinterpret_cast<uniform_float *>(reinterpret_cast<uintptr_t>(p));
+}
+
+// Reads the run of C columns from n on of a row of dh, zero past N.
+template <int C>
+__device__ __forceinline__ void load_run(const void *base, int type, size_t at, int n, int N, float (&v)[C]) {
+    const bool whole = n + C <= N;
+    if (type == I8_F32) {
+        const float *p = static_cast<const float *>(base) + at;
+        if (whole) {
+#pragma unroll
+            for (int c = 0; c < C; c += 4) {
+                const u32x4_t r = *reinterpret_cast<const u32x4_at4_t *>(p + c);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) { const uint32_t b = r[i]; v[c + i] = __builtin_bit_cast(float, b); }
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < C; ++c) v[c] = n + c < N ? p[c] : 0.f;
+        }
+        return;
+    }
+    const uint16_t *p = static_cast<const uint16_t *>(base) + at;
+    uint32_t b[C / 2];
+    if (whole) {
+#pragma unroll
+        for (int c = 0; c < C / 2; c += 2) {
+            const u32x2_t r = *reinterpret_cast<const u32x2_at2_t *>(p + 2 * c);
+            b[c] = r[0], b[c + 1] = r[1];
+        }
+    } else {
+#pragma unroll
+        for (int c = 0; c < C / 2; ++c)
+            b[c] = (n + 2 * c < N ? (uint32_t)p[2 * c] : 0u) | (n + 2 * c + 1 < N ? (uint32_t)p[2 * c + 1] << 16 : 0u);
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const uint32_t h = b[c / 2] >> (16 * (c & 1)) & 0xFFFFu;
+        v[c] = type == I8_F16 ? (float)__builtin_bit_cast(_Float16, (uint16_t)h) : __builtin_bit_cast(float, h << 16);
+    }
+}
+
+// The gradients of h = silu(g) u for g and u, with s = 1 / (1 + e^-g):
+//     dg = dh u s (1 + g (1 - s)),   du = dh g s
+// From e = e^-|g|, which never overflows: of s and 1 - s one is 1 / (1 + e) and
+// the other e / (1 + e).  Below kFar, where e is no normal number, s = e^g to the
+// last bit, taken in two halves around the other factors as far_silu does.
+__device__ __forceinline__ void gated_gradient(float dh, float g, float u, float &dg, float &du) {
+    const float e = __expf(-__builtin_fabsf(g)), big = __builtin_amdgcn_rcpf(1.f + e), small = e * big;
+    const float s = g < 0.f ? small : big, r = g < 0.f ? big : small;
+    dg = dh * (u * (s * __builtin_fmaf(g, r, 1.f)));
+    du = dh * (g * s);
+}
+__device__ __forceinline__ void far_gated_gradient(float dh, float g, float u, float &dg, float &du) {
+    const float half = __builtin_amdgcn_exp2f(0.72134752044f * g);
+    dg = (1.f + g) * half * u * (half * dh);
+    du = g * half * (half * dh);
+}
+
+// Writes a wavefront's sums.  acc[i][..]: rows row0 + 16 i + lane % 16 of the
+// tile; over its fragments a lane holds the C columns from n on (of two
+// matrices, C of gate in the first half of the fragments, C of up in the second).
+template <int FM, int C, Mode MODE>
+__device__ __forceinline__ void finish(const Args &p, const f32x4_t (&acc)[FM][MODE == kPlain ? C / 4 : C / 2], int m0,
+                                       int rows, const float *bias, int row0, int n, int lane) {
+    float add[C];
+    if constexpr (MODE == kPlain) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) add[c] = bias ? bias[c] : 0.f;
+    }
+    if (n >= p.N) return;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+        const int r = row0 + i * 16 + (lane & 15);
+        if (r >= rows) continue;
+        const size_t m = (size_t)(m0 + r);
+        if constexpr (MODE == kPlain) {
+            float v[C];
+#pragma unroll
+            for (int c = 0; c < C; ++c) v[c] = acc[i][c >> 2][c & 3] + add[c];
+            store_run<C>(p.y, p.y_type, m * p.N + n, n, p.N, v);
+        } else {
+            constexpr int UP = C / 4;                    // fragments of gate
+            float least = 0.f;
+#pragma unroll
+            for (int c = 0; c < C; ++c) least = __builtin_fminf(least, acc[i][c >> 2][c & 3]);
+            if constexpr (MODE == kGated) {
+                float v[C];
+#pragma unroll
+                for (int c = 0; c < C; ++c) v[c] = silu(acc[i][c >> 2][c & 3]) * acc[i][UP + (c >> 2)][c & 3];
+                if (__builtin_expect(least < kFar, 0)) {         // rare, and then of no account
+#pragma unroll
+                    for (int c = 0; c < C; ++c) {
+                        const float g = acc[i][c >> 2][c & 3];
+                        if (g < kFar) v[c] = far_silu(g, acc[i][UP + (c >> 2)][c & 3]);
+                    }
+                }
+                store_run<C>(p.y, p.y_type, m * p.N + n, n, p.N, v);
+            } else {
+                float dg[C], du[C];
+                load_run<C>(p.dh, p.dh_type, m * p.N + n, n, p.N, dg);
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    const float dh = dg[c], g = acc[i][c >> 2][c & 3], u = acc[i][UP + (c >> 2)][c & 3];
+                    gated_gradient(dh, g, u, dg[c], du[c]);
+                    if (__builtin_expect(least < kFar, 0) && g < kFar) far_gated_gradient(dh, g, u, dg[c], du[c]);
+                }
+                store_run<C>(p.y, p.y_type, m * 2 * p.N + n, n, p.N, dg);
+                store_run<C>(p.y, p.y_type, m * 2 * p.N + p.N + n, n, p.N, du);
+            }
+        }
+    }
+}
+
+// Loads of the scales of 64 rows for a block: from row `row` on of the tile at
+// m0, at `voff` = scale_offset, to LDS.
+__device__ __forceinline__ uint32_t scale_offset(const Args &p, int m0, int row) {
+    return (uint32_t)(((m0 + row) >> p.sa_shift) - (m0 >> p.sa_shift)) * (uint32_t)p.sa_m * 4u;
+}
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t scale_rsrc(const Args &p, int m0, int rows, int kb) {
+    return rsrc_of(p.sa + (int64_t)(m0 >> p.sa_shift) * p.sa_m + kb * p.sa_k, scale_offset(p, m0, rows - 1) + 4u);
+}
+__device__ __forceinline__ void load_scale(__amdgpu_buffer_rsrc_t r, char *to, uint32_t voff) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t)to, 4, voff, 0, 0, 0);
+}
+
+// ---------------------------------------------------------------- tiles
+//
+// A tile of BM rows and BW weight rows (of two matrices: BW / 2 of each) by WM x
+// WN wavefronts, or by G groups of as many that share out K: group g takes
+// every G-th block of 128, and the groups' sums meet in LDS at the end.  Steps
+// of G blocks pass through a ring of D stages in LDS, loaded straight from
+// memory (buffer loads to LDS, 1 KiB an instruction: eight rows of 128 bytes,
+// the lanes' chunk order making the swizzle), with the rows' scales behind
+// them.
+//
+// Of a wavefront's two sets of fragments the smaller one is held for the
+// step, and the larger one streams past it, R fragments on their way from LDS:
+//
+//     fragment s:  read fragment s + R - 1,  products of s with all held ones
+//     s = S-R+1:   wait for step t + 1 in LDS and for this step's reads,
+//                  barrier, load step t + D over step t; from here on what is
+//                  read belongs to step t + 1
+//     s = S-1:     each held fragment is read anew behind its last product
+//
+// so there is one barrier a step, with products on either side of it.  The
+// last D steps of a tile load the first D of the workgroup's next tile (one
+// gridDim.x further), which arrive while this one is stored.  A last step
+// that K does not fill is taken as the last 128 bytes of the rows, with the
+// activations already used set to zero; every address stays inside the rows.
+// Rows past the tile's end repeat its last row, and their results are not stored.
+template <int BM, int BW, int G>
+constexpr int slice_bytes() { return (BM + BW) * BK + BM * 4; }
+
+template <int BM, int BW, int WM, int WN, int G, int D, Mode MODE, bool F16>
+__global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_f8_block(Args p) {
+    constexpr bool TWO = MODE != kPlain;
+    constexpr int FM = BM / WM / 16, FW = BW / WN / 16, BN = TWO ? BW / 2 : BW, MATS = TWO ? 2 : 1;
+    constexpr int W = WM * WN;                                           // wavefronts of a group
+    constexpr int LX = BM / 8 / W, LW = BW / 8 / W, LOADS = LX + LW + 1; // load instructions of one of them and step
+    constexpr int SLICE = slice_bytes<BM, BW, G>(), STAGE = G * SLICE;
+    constexpr bool SX = FM >= FW;                                        // the rows' fragments stream
+    constexpr int S = SX ? FM : FW, H = SX ? FW : FM, R = S == 8 ? 3 : 2;
+    static_assert(S % R == 0 || S % R == R - 1, "the next step's first fragments take places that are free");
+    static_assert(S >= 2 && BM % 64 == 0 && BM <= W * 64, "every row's scale comes by one instruction a wavefront");
+    extern __shared__ __align__(16) char lds[];
+    const int tid = threadIdx.x, lane = tid & 63, all_waves = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wave = all_waves % W, group = all_waves / W;
+    const int wm = wave / WN, wn = wave % WN;
+    const int KB = (p.K + BK - 1) / BK, steps = (KB + G - 1) / G;
+    const int all = p.tiles_m * p.tiles_n, whole = whole_rounds(all);
+    struct Place { int m0, rows, n0; };
+    auto place = [&](int id, Place &at) {
+        const int b = p.part >= kHalves ? whole + (id >> (p.part - kHalves + 1)) : id;
+        int tm, tn;
+        if (b >= (p.part == kWhole ? whole : all) || !tile_of(b, p.tiles_m, p.tiles_n, tm, tn)) return false;
+        const int bm = p.part >= kHalves ? 2 * BM : BM;
+        at.m0 = tm * bm;
+        at.n0 = tn * BN;
+        if (p.part >= kHalves) {
+            at.m0 += (id & 1) * BM;
+            if (p.part == kQuarters) at.n0 = (2 * tn + (id >> 1 & 1)) * BN;
+        }
+        at.rows = min(BM, p.M - at.m0);
+        return at.rows > 0 && at.n0 < p.N;
+    };
+    int id = blockIdx.x;
+    Place cur;
+    if (!place(id, cur)) return;
+
+    // In the largest tiles, what a tile's start and end compute from the lane is
+    // computed anew each time: kept, it takes registers that the fragments need.
+    auto lane_anew = [&]() {
+        int l = tid & 63;
+        if constexpr (FM * FW >= 32) asm volatile("" : "+v"(l));
+        return l;
+    };
+
+    // Loads: this wavefront brings 1 / W of the rows of a and of w, and 64 rows' scales.
+    // Of two matrices, its weight rows are all gate or all up.
+    const uint8_t *wbase = TWO && wave * LW / 2 % FW >= FW / 2 ? p.w[1] : p.w[0];
+    __amdgpu_buffer_rsrc_t ra, rw;
+    uint32_t va[LX], vw[LW], vs;
+    int m0_next;
+    auto aim = [&](const Place &at) {
+        const int lane = lane_anew();
+        const int rows = at.rows, cols = min(BN, p.N - at.n0), chunk = ((lane & 7) ^ (lane >> 3)) << 4;
+        ra = rsrc_of(p.a + (size_t)at.m0 * p.K, (uint32_t)rows * p.K);
+        rw = rsrc_of(wbase + (size_t)at.n0 * p.K, (uint32_t)cols * p.K);
+        m0_next = at.m0;
+        vs = scale_offset(p, at.m0, min(wave * 64 % BM + lane, rows - 1));
+#pragma unroll
+        for (int i = 0; i < LX; ++i)
+            va[i] = (uint32_t)min((wave * LX + i) * 8 + (lane >> 3), rows - 1) * p.K + chunk;
+#pragma unroll
+        for (int i = 0; i < LW; ++i) {
+            // Row r belongs to wavefront column c, its fragment j, row q of it.
+            const int r = (wave * LW + i) * 8 + (lane >> 3), c = r / (16 * FW), j = r / 16 % FW, q = r & 15;
+            const int n = TWO ? c * (8 * FW) + frag_row<FW / 2>(j % (FW / 2), q) : c * (16 * FW) + frag_row<FW>(j, q);
+            vw[i] = (uint32_t)min(n, cols - 1) * p.K + chunk;
+        }
+    };
+    auto load = [&](int slot, int t) {
+        char *to = lds + slot * STAGE + group * SLICE, *at = to + wave * 1024;
+        const int kb = min(t * G + group, KB - 1), koff = min((t * G + group) * BK, p.K - BK);
+#pragma unroll
+        for (int i = 0; i < LX; ++i) load16(ra, at + (wave * (LX - 1) + i) * 1024, va[i], koff);
+#pragma unroll
+        for (int i = 0; i < LW; ++i) load16(rw, at + (BM / 8 + wave * (LW - 1) + i) * 1024, vw[i], koff);
+        load_scale(scale_rsrc(p, m0_next, BM, kb), to + (BM + BW) * BK + wave * 64 % BM * 4, vs);
+    };
+
+    // Fragment reads: lane l takes row l % 16, chunks l / 16 and l / 16 + 4
+    // (which flips bit 6 of the swizzled address).
+    const int fr = (lane & 15) * BK + (((lane >> 4) ^ (lane & 7)) << 4);
+    const int xat = wm * (16 * FM) * BK, wat = (BM + wn * (16 * FW)) * BK;
+    const int sat = (BM + BW) * BK + (wm * (16 * FM) + (lane & 15)) * 4;
+    // Chunks of this group's last block that others have used; all eight: it has none.
+    const int used = max(0, ((steps - 1) * G + group + 1) * 8 - (p.K >> 4));
+    f32x4_t acc[FM][FW];
+    Raw held[H], ring[R];
+    float scale_x[SX ? R : H];                         // of the rows of ring[] or held[]
+    auto read = [&](int at) {
+        const char *from = lds + group * SLICE + at;
+        Raw r;
+        r.lo = *reinterpret_cast<const i32x4_t *>(from + fr);
+        r.hi = *reinterpret_cast<const i32x4_t *>(from + (fr ^ 64));
+        return r;
+    };
+    auto read_x = [&](int slot, int i, bool cut, Raw &r, float &s) {
+        r = read(slot * STAGE + xat + i * 16 * BK);
+        s = *reinterpret_cast<const float *>(lds + group * SLICE + slot * STAGE + sat + i * 64);
+        if (cut) {
+            if ((lane >> 4) < used) r.lo = i32x4_t{0, 0, 0, 0};
+            if ((lane >> 4) + 4 < used) r.hi = i32x4_t{0, 0, 0, 0};
+            if (used >= 8) s = 0.f;
+        }
+    };
+    auto read_stream = [&](int slot, int q, bool cut) {
+        if constexpr (SX) read_x(slot, q, cut, ring[q % R], scale_x[q % R]);
+        else ring[q % R] = read(slot * STAGE + wat + q * 16 * BK);
+    };
+    auto read_held = [&](int slot, int h, bool cut) {
+        if constexpr (SX) held[h] = read(slot * STAGE + wat + h * 16 * BK);
+        else read_x(slot, h, cut, held[h], scale_x[h]);
+    };
+    auto barrier = [&]() {       // and this wavefront's LDS reads are done
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    // The weights' scales of a step, for this wavefront's columns.
+    float sw[MATS];
+    const float *swp[MATS];
+    auto scales_of = [&](const Place &at) {
+        const int nb = min(at.n0 + wn * (TWO ? 8 * FW : 16 * FW), p.N - 1) >> 7;
+#pragma unroll
+        for (int s = 0; s < MATS; ++s) swp[s] = p.sw[s] + (size_t)nb * KB;
+    };
+    auto load_sw = [&](float (&to)[MATS], int t) {
+#pragma unroll
+        for (int s = 0; s < MATS; ++s) to[s] = uniform_load(swp[s] + min(t * G + group, KB - 1));
+    };
+    // The bias of a tile's columns goes behind the ring, 64 of them a wavefront:
+    // fetched at the end, it would cost a trip to memory there.
+    float *biases = reinterpret_cast<float *>(lds + D * STAGE);
+    auto load_bias = [&](const Place &at, float *to) {
+        if (TWO || !p.bias) return;
+        const int q = all_waves * 64, col = at.n0 + q + lane_anew();
+        if (q < BN) load4(p.bias + min(col, p.N - 1), to + q);
+    };
+    auto after = [](int slot) { return slot + 1 == D ? 0 : slot + 1; };
+
+    // One step: its products, and the first reads of the next (none where it is
+    // the tile's last).  `arrive` waits for step t + 1 and `bring` loads into
+    // this step's place.
+    auto step = [&](int t, int slot, bool cut, bool cut_next, bool last, auto arrive, auto bring) {
+        const int next = after(slot);
+        float sw_next[MATS];
+        load_sw(sw_next, t + 1);
+        Operand<F16> kept[H];
+#pragma unroll
+        for (int h = 0; h < H; ++h) kept[h].set(held[h]);
+        float factor[SX ? 1 : H][MATS];
+        if constexpr (!SX) {
+#pragma unroll
+            for (int h = 0; h < H; ++h)
+#pragma unroll
+                for (int s = 0; s < MATS; ++s) factor[h][s] = scale_x[h] * sw[s];
+        }
+#pragma unroll
+        for (int q = 0; q < S; ++q) {
+            if (q == S - R + 1) {
+                arrive();
+                barrier();
+                bring();
+#pragma unroll
+                for (int s = 0; s < MATS; ++s) asm volatile("" : "+s"(sw_next[s]));      // has come with the LDS reads
+            }
+            Operand<F16> passing;
+            passing.set(ring[q % R]);
+            if constexpr (SX) {
+#pragma unroll
+                for (int s = 0; s < MATS; ++s) factor[0][s] = scale_x[q % R] * sw[s];
+            }
+            if (q + R - 1 < S) read_stream(slot, q + R - 1, cut);
+            else if (!last) read_stream(next, q + R - 1 - S, cut_next);
+            f32x4_t sum[H];
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                sum[h] = SX ? block_sum(kept[h], passing) : block_sum(passing, kept[h]);
+                if (q == S - 1 && !last) read_held(next, h, cut_next);
+            }
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                const int i = SX ? q : h, j = SX ? h : q;
+                add_scaled(acc[i][j], sum[h], factor[SX ? 0 : h][TWO && j >= FW / 2 ? 1 : 0]);
+            }
+        }
+#pragma unroll
+        for (int s = 0; s < MATS; ++s) sw[s] = sw_next[s];
+    };
+
+    aim(cur);
+    scales_of(cur);
+    int side = 0;                // of the two places for the bias
+    load_bias(cur, biases);
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+        if (d < steps) load(d, d);
+    wait_batches<LOADS, D - 1>(steps - 1);
+    barrier();
+    for (int slot = 0;;) {
+        const bool one = steps == 1;
+#pragma unroll
+        for (int q = 0; q < R - 1; ++q) read_stream(slot, q, one);
+#pragma unroll
+        for (int h = 0; h < H; ++h) read_held(slot, h, one);
+        load_sw(sw, 0);
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FW; ++j) acc[i][j] = f32x4_t{0, 0, 0, 0};
+        int t = 0;
+        for (; t + D < steps; ++t) {
+            step(t, slot, false, false, false, [] { wait_loads<(D - 2) * LOADS>(); }, [&] { load(slot, t + D); });
+            slot = after(slot);
+        }
+        // The last D steps load the next tile's first.
+        Place nxt = cur;
+        const bool more = G == 1 && steps >= D && place(id + (int)gridDim.x, nxt);
+        if (more) aim(nxt);
+        for (; t < steps; ++t) {
+            step(t, slot, t + 1 == steps, t + 2 == steps, t + 1 == steps,
+                 [&] {
+                     if (more) wait_loads<(D - 2) * LOADS>();
+                     else wait_batches<LOADS, D - 2>(steps - t - 2);
+                 },
+                 [&] {
+                     if (!more) return;
+                     if (t + D == steps) load_bias(nxt, biases + (side ^ 1) * BN);
+                     load(slot, t + D - steps);
+                 });
+            slot = after(slot);
+        }
+        constexpr int C = TWO ? 2 * FW : 4 * FW;      // consecutive columns of a lane
+        const int lane = lane_anew();
+        const int col = wn * (4 * C) + (lane >> 4) * C;
+        const float *bias = !TWO && p.bias ? biases + side * BN + col : nullptr;
+        if constexpr (G == 1) {
+            finish<FM, C, MODE>(p, acc, cur.m0, cur.rows, bias, wm * (16 * FM), cur.n0 + col, lane);
+        } else {
+            // The groups' sums meet in the ring's place, and group g finishes
+            // rows g, g + G, .. of the fragments.
+            static_assert(G * W * FM * FW * 1024 <= D * STAGE, "the sums fit the ring");
+            __syncthreads();
+            f32x4_t *part = reinterpret_cast<f32x4_t *>(lds) + wave * (FM * FW * 64) + lane;
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int j = 0; j < FW; ++j) part[(group * W * FM * FW + i * FW + j) * 64] = acc[i][j];
+            __syncthreads();
+            for (int i = group; i < FM; i += G) {
+                f32x4_t sum[1][FW] = {};
+#pragma unroll
+                for (int g = 0; g < G; ++g)
+#pragma unroll
+                    for (int j = 0; j < FW; ++j) sum[0][j] += part[(g * W * FM * FW + i * FW + j) * 64];
+                finish<1, C, MODE>(p, sum, cur.m0, cur.rows, bias, wm * (16 * FM) + i * 16, cur.n0 + col, lane);
+            }
+            return;
+        }
+        if (!more) return;
+        id += gridDim.x;
+        cur = nxt;
+        scales_of(cur);
+        side ^= 1;
+    }
+}
+
+// ---------------------------------------------------------------- few rows
+//
+// Tiles of 8 NX rows: what counts is the bytes in flight, and that every CU
+// has its share of them.  A wavefront takes FN strips of 16 weight rows (of
+// each matrix) and every KS-th block of 128; KS wavefronts of a workgroup
+// meet in LDS at the end.  Its blocks pass through a ring of D slots of its own
+// in LDS, loaded straight from memory eight rows of 128 bytes an instruction,
+// the rows' scales behind them, the next block issued as soon as a slot has
+// been read: no barrier, and D - 1 blocks in flight while one is multiplied.
+// Blocks past K repeat the row's last 16 bytes against activations of zero.
+constexpr int kFewDepth = 2;
+
+template <int NX, int FN, Mode MODE, int W>
+__global__ __launch_bounds__(W * 64) void gemm_f8_few(Args p, int ks_log2) {
+    constexpr int FM = (NX + 1) / 2, BM = 8 * NX, MATS = MODE == kPlain ? 1 : 2, FW = FN * MATS;
+    constexpr int D = kFewDepth, LOADS = 2 * FW + NX + 1;               // load instructions of a block
+    constexpr int SLOT = (2 * FW + 2 * FM) * 1024 + 256;                // whole fragments, the last may be half loaded
+    extern __shared__ __align__(16) char lds[];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int KS = 1 << ks_log2, ks = wave & (KS - 1);
+    // Row tiles that read the same weights lie side by side on one XCD, so that
+    // its L2 brings them once; others take the XCDs in turn.
+    int tm = (int)blockIdx.x / p.tiles_n, tn = (int)blockIdx.x - tm * p.tiles_n;
+    if (p.share) {
+        const int id = eighth_of(blockIdx.x, p.tiles_m * p.tiles_n);
+        if (id < 0) return;
+        tn = id / p.tiles_m;
+        tm = id - tn * p.tiles_m;
+    }
+    const int m0 = tm * BM, rows = min(BM, p.M - m0);
+    const int n0 = (tn * (W >> ks_log2) + (wave >> ks_log2)) * (16 * FN);
+    const int kc = p.K >> 4, KB = (kc + 7) >> 3;
+    const int g = lane >> 4, r = lane & 15;
+    f32x4_t acc[FM][FW] = {};
+    // The bias of the lane's columns, fetched before the ring's loads: at the end
+    // it would cost a trip to memory.
+    constexpr int C = 4 * FN;
+    const int n = n0 + g * C;
+    float bias[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) bias[c] = MODE == kPlain && p.bias ? p.bias[min(n + c, p.N - 1)] : 0.f;
+
+    if (n0 < p.N) {
+        char *ring = lds + wave * (D * SLOT);
+        const int cols = min(16 * FN, p.N - n0);
+        const __amdgpu_buffer_rsrc_t rx = rsrc_of(p.a + (size_t)m0 * p.K, (uint32_t)rows * p.K);
+        __amdgpu_buffer_rsrc_t rw[MATS];
+        const float *swp[MATS];
+#pragma unroll
+        for (int s = 0; s < MATS; ++s) {
+            rw[s] = rsrc_of(p.w[s] + (size_t)n0 * p.K, (uint32_t)cols * p.K);
+            swp[s] = p.sw[s] + (size_t)(n0 >> 7) * KB;
+        }
+        uint32_t vx[NX], vw[2 * FN];
+#pragma unroll
+        for (int i = 0; i < NX; ++i) vx[i] = (uint32_t)min(i * 8 + (lane >> 3), rows - 1) * p.K;
+#pragma unroll
+        for (int i = 0; i < 2 * FN; ++i) {
+            const int q = (i & 1) * 8 + (lane >> 3);               // row of fragment i / 2
+            vw[i] = (uint32_t)min(frag_row<FN>(i >> 1, q), cols - 1) * p.K;
+        }
+        const uint32_t vs = scale_offset(p, m0, min(lane, rows - 1));
+        const int chunk = (lane & 7) ^ (lane >> 3);
+        auto load = [&](int slot, int u) {
+            char *at = ring + slot * SLOT;
+            const uint32_t k = (uint32_t)min(u * 8 + chunk, kc - 1) << 4;
+#pragma unroll
+            for (int s = 0; s < MATS; ++s)
+#pragma unroll
+                for (int i = 0; i < 2 * FN; ++i) {
+                    char *to = at + (s * 2 * FN + i) * 1024;
+                    if (p.once) load16<true>(rw[s], to, vw[i] + k, 0);
+                    else load16(rw[s], to, vw[i] + k, 0);
+                }
+#pragma unroll
+            for (int i = 0; i < NX; ++i)
+                load16(rx, at + (2 * FW + i) * 1024, vx[i] + k, 0);
+            load_scale(scale_rsrc(p, m0, BM, u), at + SLOT - 256, vs);
+        };
+        const int fr = r * BK + ((g ^ (r & 7)) << 4);
+        auto products = [&](int slot, int u, const float (&sw)[MATS]) {
+            const char *at = ring + slot * SLOT;
+            auto read = [&](int f) {
+                Raw v;
+                v.lo = *reinterpret_cast<const i32x4_t *>(at + f * 2048 + fr);
+                v.hi = *reinterpret_cast<const i32x4_t *>(at + f * 2048 + (fr ^ 64));
+                return v;
+            };
+            Operand<true> w[FW];
+#pragma unroll
+            for (int j = 0; j < FW; ++j) w[j].set(read(j));
+#pragma unroll
+            for (int i = 0; i < FM; ++i) {
+                Raw v = read(FW + i);
+                const float s = *reinterpret_cast<const float *>(at + SLOT - 256 + (i * 16 + r) * 4);
+                if (u * 8 + 8 > kc) {
+                    if (u * 8 + g >= kc) v.lo = i32x4_t{0, 0, 0, 0};
+                    if (u * 8 + 4 + g >= kc) v.hi = i32x4_t{0, 0, 0, 0};
+                }
+                Operand<true> x;
+                x.set(v);
+#pragma unroll
+                for (int j = 0; j < FW; ++j) add_scaled(acc[i][j], block_sum(w[j], x), s * sw[j / FN]);
+            }
+        };
+        int left = (KB - ks + KS - 1) >> ks_log2, u = ks, slot = 0;      // this wavefront's blocks
+        float sw[MATS], sw_next[MATS];
+        auto load_sw = [&](float (&to)[MATS], int u) {
+#pragma unroll
+            for (int s = 0; s < MATS; ++s) to[s] = uniform_load(swp[s] + min(u, KB - 1));
+        };
+        load_sw(sw, u);
+#pragma unroll
+        for (int d = 0; d < D; ++d)
+            if (d < left) load(d, ks + d * KS);
+        for (; left > 0; --left, u += KS) {
+            load_sw(sw_next, u + KS);
+            if (left >= D) wait_loads<(D - 1) * LOADS>();
+            else wait_loads<0>();
+            products(slot, u, sw);
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");      // the slot has been read
+            if (left > D) load(slot, u + D * KS);
+            if (++slot == D) slot = 0;
+#pragma unroll
+            for (int s = 0; s < MATS; ++s) sw[s] = sw_next[s];
+        }
+    }
+    if (KS > 1) {
+        // Every wavefront has read its ring: the partial sums take its place.
+        __syncthreads();
+        f32x4_t *part = reinterpret_cast<f32x4_t *>(lds) + lane;
+        if (ks > 0) {
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int j = 0; j < FW; ++j) part[(wave * FM * FW + i * FW + j) * 64] = acc[i][j];
+        }
+        __syncthreads();
+        if (ks > 0) return;
+        for (int k = 1; k < KS; ++k)
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+                for (int j = 0; j < FW; ++j) acc[i][j] += part[((wave + k) * FM * FW + i * FW + j) * 64];
+    }
+    finish<FM, C, MODE>(p, acc, m0, rows, bias, 0, n, lane);
+}
+
+constexpr int kMaxRows = 1 << 24;
+constexpr int kMaxK = 131056;
+
+bool elem_aligned(const void *y, int type) { return q4::aligned(y, type == I8_F32 ? 4 : 2); }
+
+// Where a call's launches go: to the stream, or into a report of their plan,
+// with the first one's tile and all workgroups.
+struct Report { int rows, cols; int64_t grid; int block; };
+struct Target { hipStream_t stream; Report *report; };
+
+int planned(const Target &to, int rows, int cols, int64_t grid, int block) {
+    Report &r = *to.report;
+    if (!r.grid) r = {rows, cols, 0, block};
+    r.grid += grid;
+    return Q4_OK;
+}
+
+// Wavefronts on one strip's K (log2) and in a workgroup of a few-rows kernel
+// of bm rows: as many share K as it takes for 1536 wavefronts, 6 for each CU,
+// while each has a block.
+struct Split { int64_t tiles, strips; int log2, waves; };
+Split split_of(const Args &p, int bm, int cols, int most) {
+    Split s = {tiles_of(p.M, bm), tiles_of(p.N, cols), 0, most};
+    const int64_t units = tiles_of(p.K, BK);
+    while ((2 << s.log2) <= most && (units >> s.log2) > 1 && (s.tiles * s.strips) << s.log2 < 1536) ++s.log2;
+    const int64_t eights = most == 8 ? s.tiles * tiles_of(s.strips, 8 >> s.log2) : 0;
+    if (s.log2 < 3 && (eights < kCUs / 2 || eights > kCUs)) s.waves = 4;
+    return s;
+}
+
+template <int NX, int FN, Mode MODE, int W>
+int launch_few(Args p, const Split &s, const Target &to) {
+    constexpr int FM = (NX + 1) / 2, FW = MODE == kPlain ? FN : 2 * FN, kLds = W * kFewDepth * ((2 * FW + 2 * FM) * 1024 + 256);
+    p.share = s.tiles > 1;
+    p.once = p.K % 64 == 0 && !p.share && (int64_t)(MODE == kPlain ? 1 : 2) * p.N * p.K > (int64_t)64 << 20;
+    p.tiles_m = (int)s.tiles;
+    p.tiles_n = (int)tiles_of(s.strips, W >> s.log2);
+    const int64_t grid = s.tiles * p.tiles_n;
+    if (grid * (W * 64) > kMaxThreads) return Q4_EINVAL;
+    if (to.report) return planned(to, 8 * NX, (W >> s.log2) * 16 * FN, grid, W * 64);
+    gemm_f8_few<NX, FN, MODE, W><<<(unsigned)grid, W * 64, kLds, to.stream>>>(p, s.log2);
+    return q4::launch_status();
+}
+
+template <int NX, int FN, Mode MODE, int MOST = 8>
+int launch_few(const Args &p, const Target &to) {
+    const Split s = split_of(p, 8 * NX, 16 * FN, MOST);
+    if constexpr (MOST == 8)
+        if (s.waves == 8) return launch_few<NX, FN, MODE, 8>(p, s, to);
+    return launch_few<NX, FN, MODE, 4>(p, s, to);
+}
+
+template <int BM, int BW, int WM, int WN, int G, int D, Mode MODE, bool F16>
+int launch_block(Args p, const Target &to) {
+    constexpr int kBN = MODE == kPlain ? BW : BW / 2;
+    constexpr int kLds = D * G * slice_bytes<BM, BW, G>() + 2 * kBN * 4;
+    constexpr int kThreads = WM * WN * G * 64;
+    static_assert(kLds <= 160 * 1024, "the ring fits");
+    p.tiles_m = (int)tiles_of(p.M, (p.part >= kHalves ? 2 : 1) * BM);
+    p.tiles_n = (int)tiles_of(p.N, (p.part == kQuarters ? 2 : 1) * kBN);
+    int64_t grid = (int64_t)p.tiles_m * p.tiles_n;
+    if (grid > 1 << 30) return Q4_EINVAL;
+    if (p.part == kWhole) grid = whole_rounds((int)grid);
+    if (p.part >= kHalves) grid = (grid - whole_rounds((int)grid)) << (p.part - kHalves + 1);
+    // Workgroups that stay and go through the tiles, each loading its next one
+    // while it finishes the last.
+    const int64_t steps = tiles_of(p.K, BK);
+    if (G == 1 && p.part < kHalves && steps >= D && steps <= 64)
+        grid = std::min<int64_t>(grid, kCUs * (160 * 1024 / kLds));
+    else if (grid * kThreads > kMaxThreads) return Q4_EINVAL;
+    if (to.report) return planned(to, BM, kBN, grid, kThreads);
+    gemm_f8_block<BM, BW, WM, WN, G, D, MODE, F16><<<(unsigned)grid, kThreads, kLds, to.stream>>>(p);
+    return q4::launch_status();
+}
+
+enum Kernel { kFew8, kFew16, kFew32, kFew32x32, kFew64, kTile64, kTile128, kTileWide, kTile256, kTileDeep, kKernels };
+
+// The kernel for a call's sizes, by estimated times.
+Kernel choose(const Args &p, int mats) {
+    const int64_t steps = tiles_of(p.K, BK);
+    const bool f16 = p.y_type == I8_F32;
+    if (p.M <= 8) return kFew8;
+    if (p.K < BK) return p.M <= 16 ? kFew16 : kFew32;
+    auto tiles = [&](int bm, int bw) { return tiles_of(p.M, bm) * tiles_of(p.N, bw / mats); };
+    auto rounds = [&](int bm, int bw) { return (double)((tiles(bm, bw) + kCUs - 1) / kCUs); };
+    // Tiles a CU, 1 where there are fewer, and the time of one alone or of one among others.
+    auto each = [&](int64_t t, double one, double many) { return t <= kCUs ? one : (double)t / kCUs * many; };
+    auto few = [&](int bm, int cols, int most, double start, double unit, double shared, double first) {
+        const Split s = split_of(p, bm, cols, most);
+        const int64_t tm = tiles_of(p.M, bm), wgs = tm * tiles_of(s.strips, s.waves >> s.log2);
+        const double a_unit = std::max(unit, shared * (double)(tiles_of(wgs, kCUs) * s.waves));
+        const double mb = (double)mats * p.N * p.K * 1e-6;
+        return std::max(start + a_unit * (first + (double)tiles_of(steps, 1 << s.log2)),
+                        0.32 * mb * (1. + 0.4 * (double)(tm - 1)) - 1.5);
+    };
+    const bool two = mats == 2;
+    double cost[kKernels];
+    cost[kFew8] = few(8, 16, 8, -0.5, 0.15, two ? 0.050 : 0.031, 0.81);
+    cost[kFew16] = few(16, 16, 8, -0.7, 0.24, two ? 0.099 : 0.043, 0.5);
+    cost[kFew32] = few(32, 16, 8, -0.4, 0.30, two ? 0.154 : 0.11, 0.74);
+    cost[kFew32x32] = few(32, 32, 8, -0.23, 0.33, 0.14, 0.56);       // with one matrix
+    cost[kFew64] = few(64, two ? 16 : 32, 4, 0.74, 0.63, 0.25, 0.75);
+    cost[kTileDeep] = each(tiles(64, 64), 0.67 + steps * 0.38, 0.78 + steps * 0.40);
+    cost[kTile64] = std::max(1.0, (double)tiles(64, 128) / kCUs * 1.2) * (0.67 + steps * 0.42);
+    cost[kTile128] = each(tiles(128, 128), 2.25 + steps * 0.46, 0.63 + steps * 0.78);
+    cost[kTileWide] = rounds(128, 256) * (6.54 + steps * (f16 ? 1.2 : 0.75));
+    const int64_t t256 = tiles(256, 256), left = t256 % kCUs;
+    const double divided = left > kQuartersMost ? 6.54 + steps * 0.75 : left ? 2.25 + steps * 0.46 : 0.;
+    cost[kTile256] = t256 < kCUs || left > kRestMost ? rounds(256, 256) * (8.0 + steps * 1.33)
+                                                     : (double)(t256 / kCUs) * (8.0 + steps * 1.33) + divided;
+    Kernel best = kFew8;
+    for (Kernel k : {kFew16, kFew32, kFew32x32, kFew64, kTileDeep, kTile64, kTile128, kTileWide, kTile256})
+        if (cost[k] < cost[best] && !(two && k == kFew32x32) && !(f16 && k == kTile256)) best = k;
+    return best;
+}
+
+template <Mode MODE, bool F16>
+int launch(const Args &p, Kernel k, const Target &to) {
+    constexpr bool TWO = MODE != kPlain;
+    // Two workgroups share a CU with a ring of two stages; where there is only
+    // one for each CU, it takes four.
+    auto alone = [&](int bm, int bw) { return tiles_of(p.M, bm) * tiles_of(p.N, TWO ? bw / 2 : bw) <= kCUs; };
+    // Two matrices halve the columns of a lane's run: four rows of wavefronts
+    // then store whole lines.
+    constexpr int kM = TWO ? 4 : 2, kN = TWO ? 2 : 4;
+    switch (k) {
+    case kFew8: return launch_few<1, 1, MODE>(p, to);
+    case kFew16: return launch_few<2, 1, MODE>(p, to);
+    case kFew32: return launch_few<4, 1, MODE>(p, to);
+    case kFew32x32: return launch_few<4, TWO ? 1 : 2, MODE>(p, to);
+    case kFew64: return launch_few<8, TWO ? 1 : 2, MODE, 4>(p, to);
+    case kTile64: return launch_block<64, 128, 2, 4, 1, 3, MODE, F16>(p, to);
+    case kTileDeep:
+        if (alone(64, 64)) return launch_block<64, 64, 2, 2, 2, 4, MODE, F16>(p, to);
+        return launch_block<64, 64, 2, 2, 2, 2, MODE, F16>(p, to);
+    case kTile128:
+        if (alone(128, 128)) return launch_block<128, 128, kM, kN, 1, 4, MODE, F16>(p, to);
+        return launch_block<128, 128, kM, kN, 1, 2, MODE, F16>(p, to);
+    case kTileWide: return launch_block<128, 256, kM, kN, 1, 3, MODE, F16>(p, to);
+    default:
+        if constexpr (F16) return Q4_EINVAL;         // not chosen
+        else {
+            // Whole rounds, then the tiles that are left, divided.
+            Args q = p;
+            const int64_t all = tiles_of(p.M, 256) * tiles_of(p.N, TWO ? 128 : 256), left = all % kCUs;
+            if (all >= kCUs && left && left <= kRestMost) q.part = kWhole;
+            if (int st = launch_block<256, 256, kM, kN, 1, 2, MODE, false>(q, to)) return st;
+            if (q.part == kAll) return Q4_OK;
+            if (left > kQuartersMost) {
+                q.part = kHalves;
+                return launch_block<128, 256, kM, kN, 1, 3, MODE, false>(q, to);
+            }
+            q.part = kQuarters;
+            return launch_block<128, 128, kM, kN, 1, 4, MODE, false>(q, to);
+        }
+    }
+}
+
+int launch(const Args &p, Mode mode, const Target &to) {
+    const Kernel k = choose(p, mode == kPlain ? 1 : 2);
+    const bool f16 = p.y_type == I8_F32;
+    switch (mode) {
+    case kPlain: return f16 ? launch<kPlain, true>(p, k, to) : launch<kPlain, false>(p, k, to);
+    case kGated: return f16 ? launch<kGated, true>(p, k, to) : launch<kGated, false>(p, k, to);
+    default: return f16 ? launch<kBackward, true>(p, k, to) : launch<kBackward, false>(p, k, to);
+    }
+}
+
+bool type_ok(int t) { return t == I8_F32 || t == I8_F16 || t == I8_BF16; }
+
+int check_sizes(const Args &p) {
+    if (p.M < 0 || p.M > kMaxRows || p.N < 0 || p.N > kMaxRows || p.K < 16 || p.K % 16 || p.K > kMaxK)
+        return Q4_EINVAL;
+    if (tiles_of(p.M, 16) * tiles_of(p.N, 16) > 0x7FFFFFFFll) return Q4_EINVAL;
+    return type_ok(p.y_type) ? Q4_OK : Q4_EINVAL;
+}
+
+int run(Args p, int a_block, Mode mode, void *stream) {
+    if (int st = check_sizes(p)) return st;
+    if (a_block != 1 && a_block != 128) return Q4_EINVAL;
+    if (p.sa_m < 0 || p.sa_m > (1 << 20) || p.sa_k < 0 || p.sa_k > (1ll << 31)) return Q4_EINVAL;
+    if (mode == kBackward && !type_ok(p.dh_type)) return Q4_EINVAL;
+    if (p.M == 0 || p.N == 0) return Q4_OK;
+    if (!p.a || !p.sa || !p.w[0] || !p.sw[0] || !p.y) return Q4_ENULL;
+    if (mode != kPlain && (!p.w[1] || !p.sw[1])) return Q4_ENULL;
+    if (mode == kBackward && !p.dh) return Q4_ENULL;
+    if (!q4::aligned(p.a, 16) || !q4::aligned(p.w[0], 16) || !q4::aligned(p.w[1], 16) || !q4::aligned(p.sa, 4) ||
+        !q4::aligned(p.sw[0], 4) || !q4::aligned(p.sw[1], 4) || !q4::aligned(p.bias, 4) ||
+        !elem_aligned(p.y, p.y_type) || !elem_aligned(p.dh, p.dh_type))
+        return Q4_EALIGN;
+    if (int st = q4::check_device()) return st;
+    p.sa_shift = a_block == 128 ? 7 : 0;
+    return launch(p, mode, {static_cast<hipStream_t>(stream), nullptr});
+}
+
+Args args_of(const uint8_t *a, const float *sa, int64_t sm, int64_t sk, const uint8_t *w0, const float *s0,
+             const uint8_t *w1, const float *s1, void *y, int y_type, int M, int N, int K) {
+    Args p = {};
+    p.a = a, p.sa = sa, p.sa_m = sm, p.sa_k = sk;
+    p.w[0] = w0, p.w[1] = w1, p.sw[0] = s0, p.sw[1] = s1;
+    p.y = y, p.y_type = y_type, p.M = M, p.N = N, p.K = K;
+    return p;
+}
+
+}  // namespace
+
+extern "C" int gemm_f8(const uint8_t *a, const float *a_scales, int64_t stride_m, int64_t stride_k, int a_block,
+                       const uint8_t *w, const float *w_scales, const float *bias, void *y, int y_type, int M, int N,
+                       int K, void *stream) {
+    Args p = args_of(a, a_scales, stride_m, stride_k, w, w_scales, nullptr, nullptr, y, y_type, M, N, K);
+    p.bias = bias;
+    return run(p, a_block, kPlain, stream);
+}
+
+extern "C" int gemm_f8_swiglu(const uint8_t *a, const float *a_scales, int64_t stride_m, int64_t stride_k, int a_block,
+                              const uint8_t *w_gate, const float *scales_gate, const uint8_t *w_up,
+                              const float *scales_up, void *y, int y_type, int M, int N, int K, void *stream) {
+    return run(args_of(a, a_scales, stride_m, stride_k, w_gate, scales_gate, w_up, scales_up, y, y_type, M, N, K),
+               a_block, kGated, stream);
+}
+
+extern "C" int gemm_f8_swiglu_backward(const void *dh, int dh_type, const uint8_t *a, const float *a_scales,
+                                       int64_t stride_m, int64_t stride_k, int a_block, const uint8_t *w_gate,
+                                       const float *scales_gate, const uint8_t *w_up, const float *scales_up, void *d,
+                                       int y_type, int M, int N, int K, void *stream) {
+    Args p = args_of(a, a_scales, stride_m, stride_k, w_gate, scales_gate, w_up, scales_up, d, y_type, M, N, K);
+    p.dh = dh, p.dh_type = dh_type;
+    return run(p, a_block, kBackward, stream);
+}
+
+extern "C" int gemm_f8_geometry(int matrices, int y_type, int M, int N, int K, int *tile_rows, int *tile_cols,
+                                int *grid, int *block) {
+    Args p = {};
+    p.M = M, p.N = N, p.K = K, p.y_type = y_type;
+    if (matrices != 1 && matrices != 2) return Q4_EINVAL;
+    if (int st = check_sizes(p)) return st;
+    Report r = {};
+    if (M > 0 && N > 0)
+        if (int st = launch(p, matrices == 1 ? kPlain : kGated, {nullptr, &r})) return st;
+    if (tile_rows) *tile_rows = r.rows;
+    if (tile_cols) *tile_cols = r.cols;
+    if (grid) *grid = (int)r.grid;
+    if (block) *block = r.block;
+    return Q4_OK;
+}

@@ -1,0 +1,600 @@
+"""GPU parity of the operators of 8-bit floating point against the 64-bit
+oracle, through the Python binding.
+
+Quantisers are compared exactly.  Products are compared in two ways: on codes
+and scales whose every sum is a short binary number, where the result has to
+be the rounded one exactly, at every size and tile; and on quantised normal
+values, held to the bounds that include/q4f8.h gives plus half a step of the
+output's type.
+"""
+
+import threading
+
+import numpy as np
+import pytest
+import torch
+
+import memory_bandwidth_amd as q4
+from oracle import f8
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+TYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+F8 = torch.float8_e4m3fn
+
+
+def dev(a):
+    t = torch.from_numpy(np.ascontiguousarray(a)).to(DEV)
+    return t.view(F8) if t.dtype == torch.uint8 else t
+
+
+def pair(m):
+    return dev(m[0]), dev(m[1])
+
+
+def by_block(scales):
+    """Scales on the GPU as quant_f8 lays them out."""
+    return dev(scales.T).t()
+
+
+def bits(t):
+    return t.view(torch.uint8).cpu().numpy() if t.dtype == F8 else t.cpu().numpy()
+
+
+# ---------------------------------------------------------------- quantisers
+
+def values_of(seed, M, K, t):
+    x = torch.from_numpy(np.random.default_rng(seed).standard_normal((M, K)).astype(np.float32))
+    x[:, 5] *= 11
+    return x.to(TYPES[t])
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("M,K", [(1, 16), (3, 48), (65, 128), (7, 896), (33, 1040), (2, 4096), (17, 272), (5, 14336),
+                                 (1, 131056), (1030, 272), (2100, 1936)])
+def test_quant(t, M, K):
+    x = values_of(M * K, M, K, t)
+    c, s = q4.quant_f8(x.to(DEV))
+    cw, sw = f8.quant(x.double().numpy())
+    assert np.array_equal(bits(s), sw)
+    assert np.array_equal(f8.decode(bits(c)), f8.decode(cw))
+    assert s.t().is_contiguous()
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("R,C", [(1, 16), (3, 48), (128, 128), (127, 144), (129, 896), (260, 272), (16, 4096), (1000, 400),
+                                 (145, 1040), (2, 131056)])
+@pytest.mark.parametrize("layout", ["rows", "columns", "both"])
+def test_quant_block(t, R, C, layout):
+    x = values_of(R * C, R, C, t)
+    got = q4.quant_f8_block(x.to(DEV), layout=layout)
+    cw, sw = f8.quant(x.double().numpy(), 128)
+    want = {"rows": (cw, sw), "columns": f8.turned(cw, sw), "both": (cw, sw, *f8.turned(cw, sw))}[layout]
+    assert len(got) == len(want)
+    for g, w in zip(got, want):
+        assert tuple(g.shape) == w.shape
+        same = np.array_equal(f8.decode(bits(g)), f8.decode(w)) if g.dtype == F8 else np.array_equal(bits(g), w)
+        assert same
+
+
+def special(t):
+    K = 400
+    rng = np.random.default_rng(9)
+    x = np.zeros((14, K), dtype=np.float32)
+    x[0] = rng.choice(f8.MIDDLES, K)                       # scale 1 where a block holds 448: ties
+    x[0, ::128] = 448
+    x[1] = -rng.choice(f8.MIDDLES, K) * 0.75
+    x[1, ::128] = 448 * 0.75
+    x[3] = rng.standard_normal(K)
+    x[3, 100] = np.inf
+    x[4] = rng.standard_normal(K)
+    x[4, K - 1] = np.nan
+    x[5, 0] = -np.inf
+    x[6] = rng.standard_normal(K) * 1e-6
+    x[7] = rng.standard_normal(K) * 100
+    x[8, 17] = 2.0 ** -24                                  # alone in its row
+    x[9] = 1.0
+    x[10, K - 1] = -3.0
+    x[11] = rng.standard_normal(K) * 2.0 ** rng.integers(-20, 3, K)
+    x[12] = rng.choice([0.0, -0.0, 1.0], K)
+    x[13] = rng.choice(f8.VALUES[:127], K)
+    if t == "f32":
+        x[6] = rng.integers(-9, 10, K) * 2.0 ** -149       # subnormal
+        x[7] = rng.standard_normal(K) * 8e37
+        x[8] = rng.choice(f8.MIDDLES, K) * 2.0 ** -126     # scale 2^-126, ties
+        x[8, 1] = 448 * 2.0 ** -126
+    return torch.from_numpy(x).to(TYPES[t])
+
+
+@pytest.mark.parametrize("t", TYPES)
+def test_quant_ties_and_special_blocks(t):
+    x = special(t)
+    c, s = q4.quant_f8(x.to(DEV))
+    cw, sw = f8.quant(x.double().numpy())
+    assert np.array_equal(bits(s), sw, equal_nan=True)
+    assert np.array_equal(f8.decode(bits(c)), f8.decode(cw))
+    c, s, ct, st = q4.quant_f8_block(x.to(DEV), layout="both")
+    cw, sw = f8.quant(x.double().numpy(), 128)
+    for g, w in zip((c, s, ct, st), (cw, sw, *f8.turned(cw, sw))):
+        assert np.array_equal(f8.decode(bits(g)) if g.dtype == F8 else bits(g), f8.decode(w) if w.dtype == np.uint8 else w,
+                              equal_nan=True)
+    # Each special row as a block of its own.
+    for r in range(x.shape[0]):
+        c, s = q4.quant_f8_block(x[r:r + 1].to(DEV))
+        cw, sw = f8.quant(x[r:r + 1].double().numpy(), 128)
+        assert np.array_equal(bits(s), sw, equal_nan=True) and np.array_equal(f8.decode(bits(c)), f8.decode(cw)), r
+
+
+def test_quant_near_ties():
+    """Quotients within a few ulp of every middle, on both sides and on it, for many scales."""
+    rng = np.random.default_rng(4)
+    rows = []
+    for _ in range(200):
+        s = np.float32(rng.uniform(0.5, 1) * 2.0 ** rng.integers(-30, 30))
+        x = (rng.choice(f8.MIDDLES, 128) * np.float64(s)).astype(np.float32)
+        x = (x.view(np.int32) + rng.integers(-2, 3, 128).astype(np.int32)).view(np.float32) * rng.choice([-1, 1], 128)
+        x[0] = np.float32(448) * s
+        rows.append(x.astype(np.float32))
+    x = np.stack(rows)
+    c, got = q4.quant_f8(dev(x))
+    cw, sw = f8.quant(x.astype(np.float64))
+    assert np.array_equal(bits(got), sw) and np.array_equal(f8.decode(bits(c)), f8.decode(cw))
+
+
+def test_quant_outputs_given():
+    """Scales of any strides; codes and scales inside larger buffers, which keep what is around them."""
+    M, K = 37, 400
+    x = values_of(3, M, K, "bf16")
+    cw, sw = f8.quant(x.double().numpy())
+    codes = torch.zeros(M + 2, K, dtype=torch.uint8, device=DEV).view(F8)
+    for scales in (torch.full((M, 4), 7.0, device=DEV), torch.full((M, 9), 7.0, device=DEV)[:, 2:6],
+                   torch.full((4, 3 * M), 7.0, device=DEV).t()[::3]):
+        c, s = q4.quant_f8(x.to(DEV), out=(codes[1:M + 1], scales))
+        assert c.data_ptr() == codes[1].data_ptr() and s is scales
+        assert np.array_equal(bits(s), sw) and np.array_equal(f8.decode(bits(c)), f8.decode(cw))
+        assert not bits(codes)[[0, M + 1]].any()
+    wide = torch.full((M, 9), 7.0, device=DEV)
+    q4.quant_f8(x.to(DEV), out=(codes[1:M + 1], wide[:, 2:6]))
+    assert (wide[:, :2] == 7).all() and (wide[:, 6:] == 7).all()
+    cw, sw = f8.quant(x.double().numpy(), 128)
+    out = (torch.empty(M, K, dtype=F8, device=DEV), torch.empty(1, 4, device=DEV), torch.empty(K, 48, dtype=F8, device=DEV),
+           torch.empty(4, 1, device=DEV))
+    got = q4.quant_f8_block(x.to(DEV), layout="both", out=out)
+    assert all(g.data_ptr() == o.data_ptr() for g, o in zip(got, out))
+    for g, w in zip(got, (cw, sw, *f8.turned(cw, sw))):
+        assert np.array_equal(f8.decode(bits(g)) if g.dtype == F8 else bits(g), f8.decode(w) if w.dtype == np.uint8 else w)
+
+
+def test_empty():
+    z = lambda *s, **k: torch.zeros(*s, device=DEV, **k)                 # noqa: E731
+    c, s = q4.quant_f8(z(0, 64))
+    assert tuple(c.shape) == (0, 64) and tuple(s.shape) == (0, 1)
+    got = q4.quant_f8_block(z(0, 64), layout="both")
+    assert [tuple(t.shape) for t in got] == [(0, 64), (0, 1), (64, 0), (1, 0)]
+    a, w, sw = z(0, 64).to(F8), z(5, 64).to(F8), z(1, 1)
+    assert tuple(q4.gemm_f8(a, z(0, 1), w, sw).shape) == (0, 5)
+    assert tuple(q4.gemm_f8_swiglu_backward(z(0, 5), a, z(0, 1), (w, sw), (w, sw)).shape) == (0, 10)
+
+
+# ---------------------------------------------------------------- products, exactly
+#
+# Codes of 0, +-1, +-2, +-4 and scales that are one of two powers of two: products
+# and their sums are whole multiples of one unit below 2^24 of it, and the
+# products of eight are within 2^4 of each other, so that no step rounds.
+
+SMALL = np.array([0x00, 0x38, 0xB8, 0x40, 0xC0, 0x48, 0xC8], dtype=np.uint8)
+
+
+def short_codes(seed, *shape):
+    return np.random.default_rng(seed).choice(SMALL, shape)
+
+
+def short_scales(seed, rows, K, unit):
+    return (np.random.default_rng(seed).choice([1.0, 2.0], (rows, f8.blocks(K))) * unit).astype(np.float32)
+
+
+def unit(K):
+    """A power of two that brings sums of K products near 1, from both scales."""
+    return 2.0 ** -round(np.log2(K) / 4 + 1.5)
+
+
+def short_problem(M, N, K, tall=1, mats=1, seed=1):
+    u = unit(K)
+    a = short_codes(seed, M, K), short_scales(seed + 1, M if tall == 1 else f8.blocks(M), K, u)
+    return a, [(short_codes(seed + 2 + i, N, K), short_scales(seed + 5 + i, f8.blocks(N), K, u)) for i in range(mats)]
+
+
+def spread_on_gpu(codes, scales, tall):
+    s = scales.double().repeat_interleave(128, 1)[:, :codes.shape[1]].repeat_interleave(tall, 0)[:codes.shape[0]]
+    return codes.double() * s
+
+
+def exact_on_gpu(a, sa, w, sw):
+    """P in float64, exact for these inputs."""
+    tall = 1 if sa.shape[0] == a.shape[0] else 128
+    return spread_on_gpu(a, sa, tall) @ spread_on_gpu(w, sw, 128).t()
+
+
+def same(y, want, label):
+    bad = (y != want.to(y.dtype)).nonzero()
+    assert not len(bad), f"{label}: {len(bad)} of {y.numel()} differ, first at {bad[0].tolist()}"
+
+
+GEMM = [(1, 1, 16), (1, 17, 48), (1, 896, 896), (1, 300, 4096), (2, 64, 128), (3, 129, 144), (8, 1000, 1040),
+        (15, 33, 4096), (16, 16, 64), (17, 257, 272), (31, 130, 14336), (32, 512, 2816), (48, 100, 912),
+        (64, 64, 128), (65, 127, 256), (100, 896, 4864), (128, 256, 1024), (129, 300, 1040), (200, 333, 2064),
+        (256, 256, 256), (257, 511, 528), (300, 1024, 896), (511, 520, 4112), (700, 777, 1296), (1025, 1030, 400),
+        (2049, 260, 144), (260, 4100, 208), (40, 70, 32)]
+LARGE = [(64, 4100, 2064), (500, 2050, 2064), (330, 4870, 912), (1090, 5000, 528), (3775, 1827, 1056),
+         (3984, 3781, 656), (2900, 5050, 528), (4100, 4100, 272), (5000, 300, 4112), (64, 3999, 4112),
+         (230, 3313, 400), (36, 1373, 32), (126, 2093, 6016), (64, 4090, 14336), (128, 3990, 4112),
+         (4300, 4100, 2064), (4096, 5300, 2000), (8200, 4097, 1040), (2304, 2560, 9216), (2518, 2391, 2528), (3808, 1469, 2208)]
+
+
+@pytest.mark.parametrize("M,N,K", GEMM + LARGE)
+@pytest.mark.parametrize("t", TYPES)
+def test_gemm_exact(M, N, K, t):
+    (a, sa), [w] = short_problem(M, N, K)
+    args = dev(a), by_block(sa), *pair(w)
+    same(q4.gemm_f8(*args, dtype=TYPES[t]), exact_on_gpu(*args), f"{M} {N} {K}")
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 77, 256), (5, 64, 400), (40, 520, 144), (130, 64, 1024), (257, 300, 656),
+                                   (600, 515, 400), (1300, 2100, 272), (4300, 4100, 528)])
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+def test_gemm_scales_of_row_blocks_and_bias(M, N, K, t):
+    (a, sa), [w] = short_problem(M, N, K, tall=128)
+    b = (np.random.default_rng(5).integers(-64, 65, N) / 16).astype(np.float32)
+    args = dev(a), dev(sa), *pair(w)
+    same(q4.gemm_f8(*args, bias=dev(b), dtype=TYPES[t]), exact_on_gpu(*args) + dev(b).double(), f"{M} {N} {K}")
+
+
+@pytest.mark.parametrize("M,N,K", [(3, 40, 656), (40, 200, 656), (70, 520, 272), (600, 515, 400)])
+def test_gemm_strides_of_scales(M, N, K):
+    (a, sa), [w] = short_problem(M, N, K)
+    KB = sa.shape[1]
+    want = exact_on_gpu(dev(a), dev(sa), *pair(w))
+    wide = torch.full((M, KB + 5), float("nan"), device=DEV)
+    wide[:, 2:2 + KB] = dev(sa)
+    apart = torch.full((3 * KB, 2 * M), float("nan"), device=DEV)
+    apart[1::3, ::2] = dev(sa).t()
+    one = torch.full((KB,), 0.5, device=DEV).expand(M, KB)
+    for s in (dev(sa), wide[:, 2:2 + KB], apart[1::3, ::2].t()):
+        same(q4.gemm_f8(dev(a), s, *pair(w)), want, str(s.stride()))
+        same(q4.gemm_f8(dev(a), s, *pair(w), dtype=torch.bfloat16), want, str(s.stride()))
+    same(q4.gemm_f8(dev(a), one, *pair(w)), exact_on_gpu(dev(a), one.contiguous(), *pair(w)), "one row for all")
+
+
+@pytest.mark.parametrize("M,N", [(1, 5), (20, 18), (70, 70), (300, 260)])
+@pytest.mark.parametrize("t", ["f32", "f16"])
+def test_gemm_longest(M, N, t):
+    K = 131056
+    (a, sa), [w] = short_problem(M, N, K)
+    args = dev(a), by_block(sa), *pair(w)
+    same(q4.gemm_f8(*args, dtype=TYPES[t]), exact_on_gpu(*args), f"{M} {N}")
+
+
+def test_sizes_take_every_tile():
+    for t, tiles in ((torch.float32, {(8,), (16,), (32,), (64, 32), (64, 64), (64, 128), (128, 128), (128, 256)}),
+                     (torch.bfloat16, {(8,), (16,), (32,), (64, 32), (64, 64), (64, 128), (128, 128), (128, 256),
+                                       (256, 256)})):
+        got = [q4.gemm_f8_geometry(1, *s, dtype=t) for s in GEMM + LARGE]
+        seen = {(g["tile_rows"], g["tile_cols"]) for g in got} | {(g["tile_rows"],) for g in got}
+        assert tiles <= seen, tiles - seen
+        # Both kinds of launch: a workgroup for each tile, and workgroups that go through several.
+        many = [g["grid"] < -(-s[0] // g["tile_rows"]) * -(-s[1] // g["tile_cols"]) for g, s in zip(got, GEMM + LARGE)]
+        assert any(many) and not all(many)
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("M,N", [(1, 40), (5, 64), (70, 72), (300, 264)])
+@pytest.mark.parametrize("skew", [0, 1])
+def test_gemm_out_in_a_larger_buffer(t, M, N, skew):
+    """Outputs that start off a 16-byte border, with guards on both sides."""
+    (a, sa), [w] = short_problem(M, N, 160)
+    args = dev(a), by_block(sa), *pair(w)
+    buf = torch.full((M * N + 32,), 7.0, dtype=TYPES[t], device=DEV)
+    out = buf[8 + skew:8 + skew + M * N].view(M, N)
+    y = q4.gemm_f8(*args, dtype=TYPES[t], out=out)
+    assert y.data_ptr() == out.data_ptr()
+    same(y, exact_on_gpu(*args), f"{M} {N}")
+    assert (buf[:8 + skew] == 7).all() and (buf[8 + skew + M * N:] == 7).all()
+
+
+# ---------------------------------------------------------------- gates, on exact products
+
+GATED = [(1, 1, 16), (1, 896, 896), (4, 300, 4096), (16, 65, 144), (30, 1000, 1040), (64, 32, 128), (100, 130, 2816),
+         (257, 200, 528), (520, 515, 1296), (64, 2100, 2064), (300, 1000, 2064), (200, 2320, 912), (1060, 2500, 528),
+         (2593, 1533, 800), (2365, 3095, 432), (1500, 4100, 400), (96, 999, 4112), (67, 3422, 368), (40, 1100, 1040),
+         (40, 499, 8208), (40, 1373, 48), (100, 1789, 6160), (4300, 2050, 2064), (4096, 2650, 2000), (8200, 2049, 1040)]
+
+
+def gated_problem(M, N, K, size=4.0):
+    """a, gate, up and their exact products g (some beyond +-8 * size) and u, float64 on the host."""
+    (a, sa), [gate, up] = short_problem(M, N, K, mats=2)
+    gate = gate[0], gate[1] * np.float32(size)
+    g, u = (exact_on_gpu(dev(a), dev(sa), *pair(m)).cpu().numpy() for m in (gate, up))
+    return (dev(a), by_block(sa)), pair(gate), pair(up), g, u
+
+
+def check(y, want, bound, t, label):
+    got = y.float().cpu().numpy().astype(np.float64)
+    tol = f8.tolerance(want, bound, t)
+    bad = ~(np.abs(got - want) <= tol)
+    assert not bad.any(), (f"{label}: {int(bad.sum())} of {bad.size} outside, first at {np.argwhere(bad)[0]}, worst "
+                           f"{np.nanmax(np.abs(got - want) / tol):.3g} of the tolerance")
+
+
+@pytest.mark.parametrize("M,N,K", GATED)
+@pytest.mark.parametrize("t", TYPES)
+def test_swiglu(M, N, K, t):
+    a, gate, up, g, u = gated_problem(M, N, K)
+    check(q4.gemm_f8_swiglu(*a, gate, up, dtype=TYPES[t]), *f8.gated(g, 0, u, 0), t, f"{M} {N} {K}")
+
+
+@pytest.mark.parametrize("M,N,K", GATED)
+@pytest.mark.parametrize("t,td", [("f32", "bf16"), ("f16", "f32"), ("bf16", "f16"), ("bf16", "bf16")])
+def test_swiglu_backward(M, N, K, t, td):
+    a, gate, up, g, u = gated_problem(M, N, K)
+    dh = torch.from_numpy(np.random.default_rng(3).standard_normal((M, N)).astype(np.float32)).to(TYPES[td])
+    d = q4.gemm_f8_swiglu_backward(dh.to(DEV), *a, gate, up, dtype=TYPES[t])
+    check(d, *f8.gradient(dh.double().numpy(), g, 0, u, 0), t, f"{M} {N} {K}")
+
+
+@pytest.mark.parametrize("M,N,K", [(3, 40, 64), (70, 150, 256)])
+def test_far_gates(M, N, K):
+    """Gates far to both sides: silu(g) -> g and -> 0 with its small values, no NaN."""
+    a, gate, up, g, u = gated_problem(M, N, K, size=64.0)
+    assert (g < -87).any() and (g < -174).any() and (g > 100).any()
+    up = up[0], up[1] * 2.0 ** 60
+    u = u * 2.0 ** 60
+    check(q4.gemm_f8_swiglu(*a, gate, up), *f8.gated(g, 0, u, 0), "f32", "forward")
+    dh = np.random.default_rng(3).standard_normal((M, N)).astype(np.float32)
+    check(q4.gemm_f8_swiglu_backward(dev(dh), *a, gate, up), *f8.gradient(dh.astype(np.float64), g, 0, u, 0), "f32",
+          "backward")
+
+
+@pytest.mark.parametrize("M,N", [(3, 40), (70, 72), (300, 264)])
+@pytest.mark.parametrize("skew", [0, 1])
+def test_swiglu_backward_in_larger_buffers(M, N, skew):
+    """dh and d that start off a 16-byte border, with guards around d."""
+    a, gate, up, g, u = gated_problem(M, N, 160)
+    dh = torch.from_numpy(np.random.default_rng(3).standard_normal(M * N + 1).astype(np.float32)).bfloat16().to(DEV)
+    dh = dh[skew:skew + M * N].view(M, N)
+    buf = torch.full((2 * M * N + 32,), 7.0, dtype=torch.bfloat16, device=DEV)
+    out = buf[8 + skew:8 + skew + 2 * M * N].view(M, 2 * N)
+    d = q4.gemm_f8_swiglu_backward(dh, *a, gate, up, dtype=torch.bfloat16, out=out)
+    assert d.data_ptr() == out.data_ptr()
+    check(d, *f8.gradient(dh.double().cpu().numpy(), g, 0, u, 0), "bf16", f"{M} {N}")
+    assert (buf[:8 + skew] == 7).all() and (buf[8 + skew + 2 * M * N:] == 7).all()
+
+
+# ---------------------------------------------------------------- quantised values
+
+REAL = [(1, 300, 4096), (7, 129, 144), (33, 520, 912), (100, 896, 2816), (200, 333, 2064), (300, 1024, 896),
+        (600, 515, 1296), (1500, 1100, 528)]
+
+
+def real_problem(M, N, K, mats=1, tall=1):
+    rng = np.random.default_rng(M + N + K)
+    x = rng.standard_normal((M, K)) * np.where(rng.random(K) < 0.02, 8, 1)
+    return f8.quant(x, tall), [f8.quant(rng.standard_normal((N, K)) * K ** -0.5, 128) for _ in range(mats)]
+
+
+@pytest.mark.parametrize("M,N,K", REAL)
+@pytest.mark.parametrize("t", TYPES)
+def test_gemm_of_quantised_values(M, N, K, t):
+    (a, sa), [w] = real_problem(M, N, K)
+    y = q4.gemm_f8(dev(a), by_block(sa), *pair(w), dtype=TYPES[t])
+    check(y, *f8.product(a, sa, *w, t == "f32"), t, f"{M} {N} {K}")
+    # Few steps of the type in all: a mistake that the bound of single values
+    # would let pass shows in their mean square.  Rounding to a type is off by
+    # 0.3 steps in this mean, a step half an epsilon to one; the 8-bit unit by less than
+    # 2^-13 of the largest of eight for each product, which for normal codes is 2^-15.
+    want = f8.product(a, sa, *w, True)[0]
+    off = y.double().cpu().numpy() - want
+    rms = np.sqrt((off ** 2).mean() / (want ** 2).mean())
+    assert rms < 0.5 * torch.finfo(TYPES[t]).eps + (2.0 ** -20 if t == "f32" else 2.0 ** -14)
+
+
+@pytest.mark.parametrize("M,N,K", REAL)
+@pytest.mark.parametrize("t", TYPES)
+def test_gates_of_quantised_values(M, N, K, t):
+    (a, sa), [gate, up] = real_problem(M, N, K, 2)
+    g, eg = f8.product(a, sa, *gate, t == "f32")
+    u, eu = f8.product(a, sa, *up, t == "f32")
+    args = dev(a), by_block(sa), pair(gate), pair(up)
+    check(q4.gemm_f8_swiglu(*args, dtype=TYPES[t]), *f8.gated(g, eg, u, eu), t, "forward")
+    dh = np.random.default_rng(3).standard_normal((M, N)).astype(np.float32)
+    check(q4.gemm_f8_swiglu_backward(dev(dh), *args, dtype=TYPES[t]),
+          *f8.gradient(dh.astype(np.float64), g, eg, u, eu), t, "backward")
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+@pytest.mark.parametrize("M", [1, 9, 40, 100, 600])
+def test_rows_do_not_mix(M, t):
+    """NaN and infinite scales and NaN codes stay in their rows and columns, and zero rows are zero."""
+    N, K = 150, 400
+    (a, sa), [w] = short_problem(M, N, K)
+    a, w0 = a.copy(), w[0].copy()
+    a[M // 2] = 0
+    w0[3, 7] = 0x7F
+    sa = sa.copy()
+    sa[M - 1, 2] = np.nan
+    y = q4.gemm_f8(dev(a), by_block(sa), dev(w0), dev(w[1]), dtype=TYPES[t]).float().cpu().numpy()
+    with np.errstate(invalid="ignore"):
+        want = f8.values(a, sa) @ f8.values(w0, w[1]).T
+    assert np.array_equal(np.isnan(y), np.isnan(want))
+    assert np.isnan(y[M - 1]).all() and np.isnan(y[:, 3]).all()
+    if M > 1:
+        assert not y[M // 2][np.arange(N) != 3].any()
+    # The last, short block's scale infinite in a row.
+    sa[M - 1, 2] = 1
+    sa[M - 1, 3] = np.inf
+    y = q4.gemm_f8(dev(a), by_block(sa), dev(w[0]), dev(w[1]), dtype=TYPES[t]).float().cpu().numpy()
+    last = f8.decode(a)[M - 1, 384:] @ f8.decode(w[0])[:, 384:].T          # its sums: infinite, or 0 * Inf
+    assert np.array_equal(np.isinf(y[M - 1]), last != 0) and np.array_equal(np.isnan(y[M - 1]), last == 0)
+    assert np.isfinite(y[:M - 1]).all()
+
+
+# ---------------------------------------------------------------- a layer's step
+
+def step(x, dy, gate, up, down):
+    """A feed-forward layer's training step as a program writes it; gate, up [F, D] and down [D, F] in bf16."""
+    w13 = torch.cat([gate, up])
+    F, D = gate.shape
+    FB = F // 128
+    w, sw, wt, swt = q4.quant_f8_block(w13, layout="both")
+    w2, s2, w2t, s2t = q4.quant_f8_block(down, layout="both")
+    a, sa = q4.quant_f8(x)
+    pairs = (w[:F], sw[:FB]), (w[F:], sw[FB:])
+    h = q4.gemm_f8_swiglu(a, sa, *pairs, dtype=torch.bfloat16)
+    y = q4.gemm_f8(*q4.quant_f8(h), w2, s2, dtype=torch.bfloat16)
+    dh = q4.gemm_f8(*q4.quant_f8(dy), w2t, s2t, dtype=torch.bfloat16)
+    d = q4.gemm_f8_swiglu_backward(dh, a, sa, *pairs, dtype=torch.bfloat16)
+    dx = q4.gemm_f8(*q4.quant_f8(d), wt, swt, dtype=torch.bfloat16)
+    turn = lambda v: q4.quant_f8_block(v, layout="columns")              # noqa: E731
+    dw13 = q4.gemm_f8(*turn(d), *turn(x))
+    dw2 = q4.gemm_f8(*turn(dy), *turn(h))
+    return y, dx, dw13, dw2
+
+
+def step_problem(T, D, F, seed=1):
+    rng = np.random.default_rng(seed)
+    make = lambda *s, size=1.0: torch.from_numpy((rng.standard_normal(s) * size).astype(np.float32)).bfloat16()  # noqa: E731
+    return (make(T, D), make(T, D, size=0.01), make(F, D, size=D ** -0.5), make(F, D, size=D ** -0.5),
+            make(D, F, size=F ** -0.5))
+
+
+@pytest.mark.parametrize("T,D,F", [(1, 128, 128), (77, 256, 384), (600, 896, 640)])
+def test_training_step(T, D, F):
+    """Against autograd in float64.  Each e4m3 rounding is off by 2^-4 of a value at most, 2^-5.8 in the mean
+    square; a gradient is reached through six of them, none enlarged much: below 0.1 of its size."""
+    tensors = step_problem(T, D, F)
+    got = step(*(t.to(DEV) for t in tensors))
+    x, dy, gate, up, down = (t.double() for t in tensors)
+    for t in (x, gate, up, down):
+        t.requires_grad_()
+    g = x @ gate.t()
+    y = (g * torch.sigmoid(g) * (x @ up.t())) @ down.t()
+    y.backward(dy)
+    for name, v, want in (("y", got[0], y.detach()), ("dx", got[1], x.grad), ("dw13", got[2], torch.cat([gate.grad, up.grad])),
+                          ("dw2", got[3], down.grad)):
+        assert tuple(v.shape) == tuple(want.shape)
+        assert ((v.double().cpu() - want).norm() / want.norm()).item() < 0.1, name
+
+
+def test_gradient_against_differences():
+    """d is the slope of sum(dh y) in the products' results: by differences of the library's own forward pass along
+    up's scales and gate's, which scale u and g."""
+    M, N, K = 40, 60, 272
+    a, gate, up, g, u = gated_problem(M, N, K, 1.0)
+    dh = np.random.default_rng(3).standard_normal((M, N)).astype(np.float32)
+    d = q4.gemm_f8_swiglu_backward(dev(dh), *a, gate, up).double().cpu().numpy()
+    h = 2.0 ** -9                                   # scales times 1 +- h are exact; g and u move by h of themselves
+    for i, v in ((0, g), (1, u)):
+        ys = []
+        for f in (1 + h, 1 - h):
+            pairs = (gate[0], gate[1] * f) if i == 0 else gate, (up[0], up[1] * f) if i == 1 else up
+            ys.append(q4.gemm_f8_swiglu(*a, *pairs).double().cpu().numpy())
+        slope = (ys[0] - ys[1]) * dh / (2 * h)
+        # Differences: third derivatives of silu are below 0.6, so that h^2 g^3 |u dh| / 6 is left out and the
+        # two values' own errors, 17 + 5 |g| steps of 2^-24 each, are divided by h.
+        tol = h * h * np.abs(g ** 3 * u * dh) * (i == 0) + (40 + 12 * np.abs(g)) * f8.U * np.abs(dh * (np.abs(ys[0]) + 1e-30)) / h
+        tol += 2.0 ** -18 * np.abs(d[:, N * i:N * i + N] * v) + 1e-30
+        assert (np.abs(slope - d[:, N * i:N * i + N] * v) <= tol).all()
+
+
+# ---------------------------------------------------------------- streams, graphs, threads
+
+@pytest.mark.parametrize("T", [1, 20, 300])
+def test_captured_step_is_the_eager_one(T):
+    D, F = 256, 384
+    problems = [[t.to(DEV) for t in step_problem(T, D, F, seed)] for seed in (1, 2, 3)]
+    eager = [[t.clone() for t in step(*p)] for p in problems]
+    held = [t.clone() for t in problems[0]]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step(*held)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(*held)
+    for i in (0, 1, 2, 0):
+        for h, p in zip(held, problems[i]):
+            h.copy_(p)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(g, e) for g, e in zip(got, eager[i]))
+        step(*problems[(i + 1) % 3])
+
+
+def test_two_graphs_and_streams_at_once():
+    """Two captured products replayed on two streams, neither of which has a workspace to share."""
+    cases = []
+    for seed in (1, 2):
+        (a, sa), [w] = short_problem(100, 700, 912, seed=seed)
+        args = dev(a), by_block(sa), *pair(w)
+        want = exact_on_gpu(*args)
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            y = q4.gemm_f8(*args, dtype=torch.bfloat16)
+        cases.append((torch.cuda.Stream(), graph, y, want, args))
+    for _ in range(3):
+        for stream, graph, *_ in cases:
+            with torch.cuda.stream(stream):
+                graph.replay()
+        torch.cuda.synchronize()
+        for _, _, y, want, _ in cases:
+            same(y, want, "graph")
+            y.zero_()
+        torch.cuda.synchronize()
+
+
+def test_calls_from_threads():
+    problems = [short_problem(m, 300, 400, seed=m) for m in (1, 20, 90, 300)]
+    args = [(dev(a), by_block(sa), *pair(w)) for (a, sa), [w] in problems]
+    want = [exact_on_gpu(*p) for p in args]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(20):
+                y = q4.gemm_f8(*args[i])
+                torch.cuda.current_stream().synchronize()
+                if not torch.equal(y, want[i].float()):
+                    wrong.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
+def test_refusals_on_the_device():
+    (a, sa), [w] = short_problem(4, 40, 64)
+    a, sa, (wc, ws) = dev(a), dev(sa), pair(w)
+    dh = torch.zeros(4, 40, device=DEV)
+    bad = [(ValueError, lambda: q4.gemm_f8(a, sa[:3], wc, ws)), (ValueError, lambda: q4.gemm_f8(a, sa, wc, ws[:, :0])),
+           (ValueError, lambda: q4.gemm_f8(a[:, ::2], sa, wc, ws)), (ValueError, lambda: q4.gemm_f8(a, sa, wc[:, :48], ws)),
+           (ValueError, lambda: q4.gemm_f8(a, sa, wc, ws, bias=dh[0, :3])), (TypeError, lambda: q4.gemm_f8(a, sa.half(), wc, ws)),
+           (ValueError, lambda: q4.gemm_f8(a, sa.cpu(), wc, ws)), (ValueError, lambda: q4.gemm_f8(a, sa, wc, ws, out=dh[:, :3])),
+           (TypeError, lambda: q4.gemm_f8(a, sa, wc, ws, dtype=torch.float16, out=dh)),
+           (ValueError, lambda: q4.gemm_f8_swiglu(a, sa, (wc, ws), (wc[:20], ws))),
+           (ValueError, lambda: q4.gemm_f8_swiglu_backward(dh[:3], a, sa, (wc, ws), (wc, ws))),
+           (ValueError, lambda: q4.gemm_f8_swiglu_backward(dh, a, sa, (wc, ws), (wc, ws), out=dh)),
+           (TypeError, lambda: q4.gemm_f8_swiglu_backward(None, a, sa, (wc, ws), (wc, ws))),
+           (TypeError, lambda: q4.gemm_f8_swiglu_backward(dh.double(), a, sa, (wc, ws), (wc, ws))),
+           (ValueError, lambda: q4.quant_f8(dh[:, ::2])), (ValueError, lambda: q4.quant_f8(dh[0])),
+           (ValueError, lambda: q4.quant_f8(dh[:, :16].contiguous(), out=(a[:, :16], sa))),
+           (ValueError, lambda: q4.quant_f8_block(dh[:, :16].contiguous(), out=(a,))),
+           (q4.Q4Error, lambda: q4.quant_f8(dh)), (q4.Q4Error, lambda: q4.quant_f8_block(dh))]      # 40 columns
+    for i, (kind, fn) in enumerate(bad):
+        with pytest.raises(kind):
+            fn()
+            print("not refused:", i)
