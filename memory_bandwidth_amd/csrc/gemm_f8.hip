@@ -255,8 +255,13 @@ __device__ __forceinline__ void load_scale(__amdgpu_buffer_rsrc_t r, char *to, u
 // that K does not fill is taken as the last 128 bytes of the rows, with the
 // activations already used set to zero; every address stays inside the rows.
 // Rows past the tile's end repeat its last row, and their results are not stored.
-template <int BM, int BW, int G>
-constexpr int slice_bytes() { return (BM + BW) * BK + BM * 4; }
+//
+// Scales: wavefront v < BM / 64 brings those of 64 rows, the next one (two, with
+// two matrices) those of the columns, a lane 16 of them.  They pass through LDS
+// as well: read through the scalar cache they would make every wait for an LDS
+// read a wait for all.
+template <int BM, int BW, bool TWO>
+constexpr int slice_bytes() { return (BM + BW) * BK + BM * 4 + (TWO ? 512 : 256); }
 
 template <int BM, int BW, int WM, int WN, int G, int D, Mode MODE, bool F16>
 __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_f8_block(Args p) {
@@ -264,11 +269,11 @@ __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_f8_block(Args p) {
     constexpr int FM = BM / WM / 16, FW = BW / WN / 16, BN = TWO ? BW / 2 : BW, MATS = TWO ? 2 : 1;
     constexpr int W = WM * WN;                                           // wavefronts of a group
     constexpr int LX = BM / 8 / W, LW = BW / 8 / W, LOADS = LX + LW + 1; // load instructions of one of them and step
-    constexpr int SLICE = slice_bytes<BM, BW, G>(), STAGE = G * SLICE;
+    constexpr int SLICE = slice_bytes<BM, BW, TWO>(), STAGE = G * SLICE;
     constexpr bool SX = FM >= FW;                                        // the rows' fragments stream
-    constexpr int S = SX ? FM : FW, H = SX ? FW : FM, R = S == 8 ? 3 : 2;
+    constexpr int S = SX ? FM : FW, H = SX ? FW : FM, R = 2;
     static_assert(S % R == 0 || S % R == R - 1, "the next step's first fragments take places that are free");
-    static_assert(S >= 2 && BM % 64 == 0 && BM <= W * 64, "every row's scale comes by one instruction a wavefront");
+    static_assert(S >= 2 && BM % 64 == 0 && BM / 64 + MATS <= W, "one instruction a wavefront brings all scales");
     extern __shared__ __align__(16) char lds[];
     const int tid = threadIdx.x, lane = tid & 63, all_waves = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wave = all_waves % W, group = all_waves / W;
@@ -307,23 +312,34 @@ __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_f8_block(Args p) {
     const uint8_t *wbase = TWO && wave * LW / 2 % FW >= FW / 2 ? p.w[1] : p.w[0];
     __amdgpu_buffer_rsrc_t ra, rw;
     uint32_t va[LX], vw[LW], vs;
-    int m0_next;
+    // This wavefront's scales: those of a matrix's columns, or of 64 rows.
+    const int mat = wave - BM / 64;
+    const bool of_columns = mat >= 0 && mat < MATS;
+    const int scales_at = (BM + BW) * BK + (of_columns ? BM * 4 + mat * 256 : wave * 64 % BM * 4);
+    const int64_t scale_step = of_columns ? 1 : p.sa_k;
+    const float *scale_base;
     auto aim = [&](const Place &at) {
         const int lane = lane_anew();
         const int rows = at.rows, cols = min(BN, p.N - at.n0), chunk = ((lane & 7) ^ (lane >> 3)) << 4;
         ra = rsrc_of(p.a + (size_t)at.m0 * p.K, (uint32_t)rows * p.K);
         rw = rsrc_of(wbase + (size_t)at.n0 * p.K, (uint32_t)cols * p.K);
-        m0_next = at.m0;
-        vs = scale_offset(p, at.m0, min(wave * 64 % BM + lane, rows - 1));
+        if (of_columns) {
+            const int nb = at.n0 >> 7;
+            scale_base = (mat == 0 ? p.sw[0] : p.sw[1]) + (size_t)nb * KB;
+            vs = (uint32_t)((min(at.n0 + lane * 16, p.N - 1) >> 7) - nb) * (uint32_t)KB * 4u;
+        } else {
+            scale_base = p.sa + (int64_t)(at.m0 >> p.sa_shift) * p.sa_m;
+            vs = scale_offset(p, at.m0, min(wave * 64 % BM + lane, rows - 1));
+        }
 #pragma unroll
         for (int i = 0; i < LX; ++i)
-            va[i] = (uint32_t)min((wave * LX + i) * 8 + (lane >> 3), rows - 1) * p.K + chunk;
+            va[i] = __umul24(min((wave * LX + i) * 8 + (lane >> 3), rows - 1), p.K) + chunk;
 #pragma unroll
         for (int i = 0; i < LW; ++i) {
             // Row r belongs to wavefront column c, its fragment j, row q of it.
             const int r = (wave * LW + i) * 8 + (lane >> 3), c = r / (16 * FW), j = r / 16 % FW, q = r & 15;
             const int n = TWO ? c * (8 * FW) + frag_row<FW / 2>(j % (FW / 2), q) : c * (16 * FW) + frag_row<FW>(j, q);
-            vw[i] = (uint32_t)min(n, cols - 1) * p.K + chunk;
+            vw[i] = __umul24(min(n, cols - 1), p.K) + chunk;
         }
     };
     auto load = [&](int slot, int t) {
@@ -333,7 +349,7 @@ __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_f8_block(Args p) {
         for (int i = 0; i < LX; ++i) load16(ra, at + (wave * (LX - 1) + i) * 1024, va[i], koff);
 #pragma unroll
         for (int i = 0; i < LW; ++i) load16(rw, at + (BM / 8 + wave * (LW - 1) + i) * 1024, vw[i], koff);
-        load_scale(scale_rsrc(p, m0_next, BM, kb), to + (BM + BW) * BK + wave * 64 % BM * 4, vs);
+        load_scale(rsrc_of(scale_base + kb * scale_step, 0xFFFFFFFFu), to + scales_at, vs);
     };
 
     // Fragment reads: lane l takes row l % 16, chunks l / 16 and l / 16 + 4
@@ -353,22 +369,29 @@ __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_f8_block(Args p) {
         r.hi = *reinterpret_cast<const i32x4_t *>(from + (fr ^ 64));
         return r;
     };
-    auto read_x = [&](int slot, int i, bool cut, Raw &r, float &s) {
+    auto read_x = [&](int slot, int i, Raw &r, float &s) {
         r = read(slot * STAGE + xat + i * 16 * BK);
         s = *reinterpret_cast<const float *>(lds + group * SLICE + slot * STAGE + sat + i * 64);
-        if (cut) {
-            if ((lane >> 4) < used) r.lo = i32x4_t{0, 0, 0, 0};
-            if ((lane >> 4) + 4 < used) r.hi = i32x4_t{0, 0, 0, 0};
-            if (used >= 8) s = 0.f;
-        }
     };
-    auto read_stream = [&](int slot, int q, bool cut) {
-        if constexpr (SX) read_x(slot, q, cut, ring[q % R], scale_x[q % R]);
+    auto read_stream = [&](int slot, int q) {
+        if constexpr (SX) read_x(slot, q, ring[q % R], scale_x[q % R]);
         else ring[q % R] = read(slot * STAGE + wat + q * 16 * BK);
     };
-    auto read_held = [&](int slot, int h, bool cut) {
+    auto read_held = [&](int slot, int h) {
         if constexpr (SX) held[h] = read(slot * STAGE + wat + h * 16 * BK);
-        else read_x(slot, h, cut, held[h], scale_x[h]);
+        else read_x(slot, h, held[h], scale_x[h]);
+    };
+    // The last step's activations that other steps have used are cleared by the
+    // wavefront that has loaded them, once they have come.
+    auto clear_used = [&](int slot) {
+        const int lane = lane_anew();
+        char *to = lds + slot * STAGE + group * SLICE;
+        if (((lane & 7) ^ (lane >> 3)) < used) {
+#pragma unroll
+            for (int i = 0; i < LX; ++i)
+                *reinterpret_cast<i32x4_t *>(to + (wave * LX + i) * 1024 + lane * 16) = i32x4_t{0, 0, 0, 0};
+        }
+        if (used >= 8 && !of_columns) *reinterpret_cast<float *>(to + scales_at + lane * 4) = 0.f;
     };
     auto barrier = [&]() {       // and this wavefront's LDS reads are done
         __builtin_amdgcn_sched_barrier(0);
@@ -377,15 +400,11 @@ __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_f8_block(Args p) {
     };
     // The weights' scales of a step, for this wavefront's columns.
     float sw[MATS];
-    const float *swp[MATS];
-    auto scales_of = [&](const Place &at) {
-        const int nb = min(at.n0 + wn * (TWO ? 8 * FW : 16 * FW), p.N - 1) >> 7;
+    const int swat = (BM + BW) * BK + BM * 4 + wn * (TWO ? FW / 2 : FW) * 4;
+    auto read_sw = [&](int slot) {
 #pragma unroll
-        for (int s = 0; s < MATS; ++s) swp[s] = p.sw[s] + (size_t)nb * KB;
-    };
-    auto load_sw = [&](float (&to)[MATS], int t) {
-#pragma unroll
-        for (int s = 0; s < MATS; ++s) to[s] = uniform_load(swp[s] + min(t * G + group, KB - 1));
+        for (int s = 0; s < MATS; ++s)
+            sw[s] = *reinterpret_cast<const float *>(lds + slot * STAGE + group * SLICE + swat + s * 256);
     };
     // The bias of a tile's columns goes behind the ring, 64 of them a wavefront:
     // fetched at the end, it would cost a trip to memory there.
@@ -397,98 +416,106 @@ __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_f8_block(Args p) {
     };
     auto after = [](int slot) { return slot + 1 == D ? 0 : slot + 1; };
 
-    // One step: its products, and the first reads of the next (none where it is
-    // the tile's last).  `arrive` waits for step t + 1 and `bring` loads into
-    // this step's place.
-    auto step = [&](int t, int slot, bool cut, bool cut_next, bool last, auto arrive, auto bring) {
+    // One step: its products, and the first reads of the next (past a tile's last
+    // step they are not used).  A sum is added two products late, so that it
+    // has left the matrix cores by then; a step's last two behind the next one's
+    // first.  `arrive` waits for step t + 1 and `bring` loads into this step's place.
+    constexpr int ALL = S * H;
+    static_assert(ALL % 4 == 0 && H >= 2, "places of sums and factors repeat with the steps");
+    f32x4_t sum[4];
+    float factor[2][SX ? 1 : H][MATS];                 // scales of the products of even and odd fragments
+    auto add = [&](int n) {                            // sum n of a step; -2, -1: of the one before
+        const int at = n < 0 ? n + ALL : n, q = at / H, h = at % H, i = SX ? q : h, j = SX ? h : q;
+        add_scaled(acc[i][j], sum[at % 4], factor[q & 1][SX ? 0 : h][TWO && j >= FW / 2 ? 1 : 0]);
+    };
+    auto step = [&](int t, int slot, auto arrive, auto bring) {
         const int next = after(slot);
-        float sw_next[MATS];
-        load_sw(sw_next, t + 1);
         Operand<F16> kept[H];
 #pragma unroll
         for (int h = 0; h < H; ++h) kept[h].set(held[h]);
-        float factor[SX ? 1 : H][MATS];
-        if constexpr (!SX) {
-#pragma unroll
-            for (int h = 0; h < H; ++h)
-#pragma unroll
-                for (int s = 0; s < MATS; ++s) factor[h][s] = scale_x[h] * sw[s];
-        }
 #pragma unroll
         for (int q = 0; q < S; ++q) {
             if (q == S - R + 1) {
+                // Additions stay on this side of the branches: moved behind them, all
+                // their sums would have to be kept.
+#pragma unroll
+                for (int i = 0; i < FM; ++i)
+#pragma unroll
+                    for (int j = 0; j < FW; ++j) asm volatile("" : "+v"(acc[i][j]));
                 arrive();
                 barrier();
                 bring();
-#pragma unroll
-                for (int s = 0; s < MATS; ++s) asm volatile("" : "+s"(sw_next[s]));      // has come with the LDS reads
             }
             Operand<F16> passing;
             passing.set(ring[q % R]);
-            if constexpr (SX) {
 #pragma unroll
-                for (int s = 0; s < MATS; ++s) factor[0][s] = scale_x[q % R] * sw[s];
-            }
-            if (q + R - 1 < S) read_stream(slot, q + R - 1, cut);
-            else if (!last) read_stream(next, q + R - 1 - S, cut_next);
-            f32x4_t sum[H];
+            for (int h = 0; h < (SX ? 1 : H); ++h)
 #pragma unroll
-            for (int h = 0; h < H; ++h) {
-                sum[h] = SX ? block_sum(kept[h], passing) : block_sum(passing, kept[h]);
-                if (q == S - 1 && !last) read_held(next, h, cut_next);
-            }
+                for (int s = 0; s < MATS; ++s) factor[q & 1][h][s] = scale_x[SX ? q % R : h] * sw[s];
+            if (q + R - 1 < S) read_stream(slot, q + R - 1);
+            else read_stream(next, q + R - 1 - S);
 #pragma unroll
             for (int h = 0; h < H; ++h) {
-                const int i = SX ? q : h, j = SX ? h : q;
-                add_scaled(acc[i][j], sum[h], factor[SX ? 0 : h][TWO && j >= FW / 2 ? 1 : 0]);
+                sum[(q * H + h) % 4] = SX ? block_sum(kept[h], passing) : block_sum(passing, kept[h]);
+                add(q * H + h - 2);
+                if (q == S - 1) read_held(next, h);
             }
+            if (q == S - 1) read_sw(next);
+            __builtin_amdgcn_sched_barrier(0);
         }
-#pragma unroll
-        for (int s = 0; s < MATS; ++s) sw[s] = sw_next[s];
     };
 
     aim(cur);
-    scales_of(cur);
     int side = 0;                // of the two places for the bias
     load_bias(cur, biases);
 #pragma unroll
     for (int d = 0; d < D; ++d)
         if (d < steps) load(d, d);
     wait_batches<LOADS, D - 1>(steps - 1);
+    if (steps == 1 && used) clear_used(0);
     barrier();
     for (int slot = 0;;) {
-        const bool one = steps == 1;
 #pragma unroll
-        for (int q = 0; q < R - 1; ++q) read_stream(slot, q, one);
+        for (int q = 0; q < R - 1; ++q) read_stream(slot, q);
 #pragma unroll
-        for (int h = 0; h < H; ++h) read_held(slot, h, one);
-        load_sw(sw, 0);
+        for (int h = 0; h < H; ++h) read_held(slot, h);
+        read_sw(slot);
 #pragma unroll
         for (int i = 0; i < FM; ++i)
 #pragma unroll
             for (int j = 0; j < FW; ++j) acc[i][j] = f32x4_t{0, 0, 0, 0};
-        int t = 0;
-        for (; t + D < steps; ++t) {
-            step(t, slot, false, false, false, [] { wait_loads<(D - 2) * LOADS>(); }, [&] { load(slot, t + D); });
-            slot = after(slot);
-        }
+        sum[2] = sum[3] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+        for (int h = 0; h < (SX ? 1 : H); ++h)
+#pragma unroll
+            for (int s = 0; s < MATS; ++s) factor[1][h][s] = 0.f;
         // The last D steps load the next tile's first.
         Place nxt = cur;
-        const bool more = G == 1 && steps >= D && place(id + (int)gridDim.x, nxt);
-        if (more) aim(nxt);
-        for (; t < steps; ++t) {
-            step(t, slot, t + 1 == steps, t + 2 == steps, t + 1 == steps,
-                 [&] {
-                     if (more) wait_loads<(D - 2) * LOADS>();
-                     else wait_batches<LOADS, D - 2>(steps - t - 2);
-                 },
-                 [&] {
-                     if (!more) return;
-                     if (t + D == steps) load_bias(nxt, biases + (side ^ 1) * BN);
-                     load(slot, t + D - steps);
-                 });
-            slot = after(slot);
+        bool loads = steps > D;
+        for (int t = 0, end = loads ? steps - D : 0;;) {
+            for (; t < end; ++t) {
+                step(t, slot,
+                     [&] {
+                         if (loads) wait_loads<(D - 2) * LOADS>();
+                         else wait_batches<LOADS, D - 2>(steps - t - 2);
+                         if (t + 2 == steps && used) clear_used(after(slot));
+                     },
+                     [&] {
+                         if (loads) load(slot, t + D < steps ? t + D : t + D - steps);
+                     });
+                slot = after(slot);
+            }
+            if (end == steps) break;
+            end = steps;
+            loads = G == 1 && steps >= D && place(id + (int)gridDim.x, nxt);
+            if (loads) {
+                aim(nxt);
+                load_bias(nxt, biases + (side ^ 1) * BN);
+            }
         }
+        const bool more = loads;
+        add(-2);
+        add(-1);
         constexpr int C = TWO ? 2 * FW : 4 * FW;      // consecutive columns of a lane
         const int lane = lane_anew();
         const int col = wn * (4 * C) + (lane >> 4) * C;
@@ -519,7 +546,6 @@ __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_f8_block(Args p) {
         if (!more) return;
         id += gridDim.x;
         cur = nxt;
-        scales_of(cur);
         side ^= 1;
     }
 }
@@ -727,7 +753,7 @@ int launch_few(const Args &p, const Target &to) {
 template <int BM, int BW, int WM, int WN, int G, int D, Mode MODE, bool F16>
 int launch_block(Args p, const Target &to) {
     constexpr int kBN = MODE == kPlain ? BW : BW / 2;
-    constexpr int kLds = D * G * slice_bytes<BM, BW, G>() + 2 * kBN * 4;
+    constexpr int kLds = D * G * slice_bytes<BM, BW, MODE != kPlain>() + 2 * kBN * 4;
     constexpr int kThreads = WM * WN * G * 64;
     static_assert(kLds <= 160 * 1024, "the ring fits");
     p.tiles_m = (int)tiles_of(p.M, (p.part >= kHalves ? 2 : 1) * BM);
