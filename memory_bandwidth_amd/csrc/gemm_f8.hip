@@ -241,13 +241,14 @@ __device__ __forceinline__ void load_scale(__amdgpu_buffer_rsrc_t r, char *to, u
 // them.
 //
 // Of a wavefront's two sets of fragments the smaller one is held for the
-// step, and the larger one streams past it, R fragments on their way from LDS:
+// step, and the larger one streams past it:
 //
-//     fragment s:  read fragment s + R - 1,  products of s with all held ones
-//     s = S-R+1:   wait for step t + 1 in LDS and for this step's reads,
-//                  barrier, load step t + D over step t; from here on what is
-//                  read belongs to step t + 1
-//     s = S-1:     each held fragment is read anew behind its last product
+//     fragments 0 .. S - T - 1:  its products with all held ones, behind them
+//                  reads of fragments to come
+//     barrier:     step t + 1 has come to LDS and this step's reads are done;
+//                  step t + D is loaded over step t
+//     the last T:  for each held fragment its products with them, then the
+//                  read of the next step's
 //
 // so there is one barrier a step, with products on either side of it.  The
 // last D steps of a tile load the first D of the workgroup's next tile (one
@@ -260,6 +261,18 @@ __device__ __forceinline__ void load_scale(__amdgpu_buffer_rsrc_t r, char *to, u
 // two matrices) those of the columns, a lane 16 of them.  They pass through LDS
 // as well: read through the scalar cache they would make every wait for an LDS
 // read a wait for all.
+// Orders what stands between two scheduling barriers: behind each of the
+// products an LDS read and five vector instructions.
+template <int PRODUCTS>
+__device__ __forceinline__ void spread() {
+    if constexpr (PRODUCTS > 0) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);
+        spread<PRODUCTS - 1>();
+    }
+}
+
 template <int BM, int BW, bool TWO>
 constexpr int slice_bytes() { return (BM + BW) * BK + BM * 4 + (TWO ? 512 : 256); }
 
@@ -271,8 +284,9 @@ __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_f8_block(Args p) {
     constexpr int LX = BM / 8 / W, LW = BW / 8 / W, LOADS = LX + LW + 1; // load instructions of one of them and step
     constexpr int SLICE = slice_bytes<BM, BW, TWO>(), STAGE = G * SLICE;
     constexpr bool SX = FM >= FW;                                        // the rows' fragments stream
-    constexpr int S = SX ? FM : FW, H = SX ? FW : FM, R = 2;
-    static_assert(S % R == 0 || S % R == R - 1, "the next step's first fragments take places that are free");
+    constexpr int S = SX ? FM : FW, H = SX ? FW : FM;
+    constexpr int T = S == 8 ? 3 : 1, R = T + 1;                         // of the stream: the last ones, places
+    static_assert(S % R == 0, "the next step's first fragment takes a place that is free");
     static_assert(S >= 2 && BM % 64 == 0 && BM / 64 + MATS <= W, "one instruction a wavefront brings all scales");
     extern __shared__ __align__(16) char lds[];
     const int tid = threadIdx.x, lane = tid & 63, all_waves = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -309,8 +323,9 @@ __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_f8_block(Args p) {
 
     // Loads: this wavefront brings 1 / W of the rows of a and of w, and 64 rows' scales.
     // Of two matrices, its weight rows are all gate or all up.
-    const uint8_t *wbase = TWO && wave * LW / 2 % FW >= FW / 2 ? p.w[1] : p.w[0];
-    __amdgpu_buffer_rsrc_t ra, rw;
+    const uint8_t *w_matrix = TWO && wave * LW / 2 % FW >= FW / 2 ? p.w[1] : p.w[0];
+    const uint8_t *a_base, *w_base;
+    uint32_t a_bytes, w_bytes;
     uint32_t va[LX], vw[LW], vs;
     // This wavefront's scales: those of a matrix's columns, or of 64 rows.
     const int mat = wave - BM / 64;
@@ -321,8 +336,8 @@ __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_f8_block(Args p) {
     auto aim = [&](const Place &at) {
         const int lane = lane_anew();
         const int rows = at.rows, cols = min(BN, p.N - at.n0), chunk = ((lane & 7) ^ (lane >> 3)) << 4;
-        ra = rsrc_of(p.a + (size_t)at.m0 * p.K, (uint32_t)rows * p.K);
-        rw = rsrc_of(wbase + (size_t)at.n0 * p.K, (uint32_t)cols * p.K);
+        a_base = p.a + (size_t)at.m0 * p.K, a_bytes = (uint32_t)rows * p.K;
+        w_base = w_matrix + (size_t)at.n0 * p.K, w_bytes = (uint32_t)cols * p.K;
         if (of_columns) {
             const int nb = at.n0 >> 7;
             scale_base = (mat == 0 ? p.sw[0] : p.sw[1]) + (size_t)nb * KB;
@@ -342,14 +357,20 @@ __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_f8_block(Args p) {
             vw[i] = __umul24(min(n, cols - 1), p.K) + chunk;
         }
     };
-    auto load = [&](int slot, int t) {
-        char *to = lds + slot * STAGE + group * SLICE, *at = to + wave * 1024;
-        const int kb = min(t * G + group, KB - 1), koff = min((t * G + group) * BK, p.K - BK);
-#pragma unroll
-        for (int i = 0; i < LX; ++i) load16(ra, at + (wave * (LX - 1) + i) * 1024, va[i], koff);
-#pragma unroll
-        for (int i = 0; i < LW; ++i) load16(rw, at + (BM / 8 + wave * (LW - 1) + i) * 1024, vw[i], koff);
-        load_scale(rsrc_of(scale_base + kb * scale_step, 0xFFFFFFFFu), to + scales_at, vs);
+    // Load k of a step: `wanted` false makes it one past the end of an empty
+    // array, which no memory is asked for, so that every step has as many.
+    struct Source { __amdgpu_buffer_rsrc_t a, w, scale; char *to; int koff; };
+    auto source = [&](int slot, int t, bool wanted) {
+        const int kb = min(t * G + group, KB - 1);
+        return Source{rsrc_of(a_base, wanted ? a_bytes : 0u), rsrc_of(w_base, wanted ? w_bytes : 0u),
+                      rsrc_of(scale_base + kb * scale_step, wanted ? 0xFFFFFFFFu : 0u), lds + slot * STAGE + group * SLICE,
+                      min((t * G + group) * BK, p.K - BK)};
+    };
+    auto load = [&](const Source &from, int k) {
+        char *at = from.to + (wave * (k < LX ? LX : LW) + (k < LX ? k : BM / 8 + k - LX)) * 1024;
+        if (k < LX) load16(from.a, at, va[k < LX ? k : 0], from.koff);
+        else if (k < LX + LW) load16(from.w, at, vw[k < LX + LW ? k - LX : 0], from.koff);
+        else load_scale(from.scale, from.to + scales_at, vs);
     };
 
     // Fragment reads: lane l takes row l % 16, chunks l / 16 and l / 16 + 4
@@ -417,51 +438,87 @@ __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_f8_block(Args p) {
     auto after = [](int slot) { return slot + 1 == D ? 0 : slot + 1; };
 
     // One step: its products, and the first reads of the next (past a tile's last
-    // step they are not used).  A sum is added two products late, so that it
-    // has left the matrix cores by then; a step's last two behind the next one's
-    // first.  `arrive` waits for step t + 1 and `bring` loads into this step's place.
-    constexpr int ALL = S * H;
-    static_assert(ALL % 4 == 0 && H >= 2, "places of sums and factors repeat with the steps");
+    // step they are not used).  The products of the last T fragments of the stream
+    // come by held fragment, so that each of those is read anew behind T of
+    // them: all at once, behind the last, would have the matrix cores wait for
+    // LDS.  A sum is added two products late, so that it has left the matrix cores
+    // by then; a step's last two behind the next one's first.
+    constexpr int ALL = S * H, MAIN = (S - T) * H;
+    static_assert(ALL % 4 == 0 && H >= 2, "places of sums repeat with the steps");
     f32x4_t sum[4];
-    float factor[2][SX ? 1 : H][MATS];                 // scales of the products of even and odd fragments
+    float factor[4];
+    auto q_of = [](int n) { return n < MAIN ? n / H : S - T + (n - MAIN) % T; };
+    auto h_of = [](int n) { return n < MAIN ? n % H : (n - MAIN) / T; };
     auto add = [&](int n) {                            // sum n of a step; -2, -1: of the one before
-        const int at = n < 0 ? n + ALL : n, q = at / H, h = at % H, i = SX ? q : h, j = SX ? h : q;
-        add_scaled(acc[i][j], sum[at % 4], factor[q & 1][SX ? 0 : h][TWO && j >= FW / 2 ? 1 : 0]);
+        if (n < 0) n += ALL;
+        add_scaled(acc[SX ? q_of(n) : h_of(n)][SX ? h_of(n) : q_of(n)], sum[n % 4], factor[n % 4]);
     };
-    auto step = [&](int t, int slot, auto arrive, auto bring) {
+    auto step = [&](int t, int slot, const Source &from) {
         const int next = after(slot);
-        Operand<F16> kept[H];
+        Operand<F16> kept[H], passing[T];
+        float by[SX ? T : H][MATS];                    // scales of the rows in hand, times those of the columns
+        auto scale = [&](int at, float x) {
 #pragma unroll
-        for (int h = 0; h < H; ++h) kept[h].set(held[h]);
+            for (int s = 0; s < MATS; ++s) by[at][s] = x * sw[s];
+        };
 #pragma unroll
-        for (int q = 0; q < S; ++q) {
-            if (q == S - R + 1) {
-                // Additions stay on this side of the branches: moved behind them, all
-                // their sums would have to be kept.
+        for (int h = 0; h < H; ++h) {
+            kept[h].set(held[h]);
+            if constexpr (!SX) scale(h, scale_x[h]);
+        }
+        auto product = [&](int n, const Operand<F16> &x, int at) {
+            const int q = q_of(n), h = h_of(n), j = SX ? h : q;
+            sum[n % 4] = SX ? block_sum(kept[h], x) : block_sum(x, kept[h]);
+            factor[n % 4] = by[SX ? at : h][TWO && j >= FW / 2 ? 1 : 0];
+            add(n - 2);
+        };
+        // Reads of the stream's fragments run up to R - 1 ahead, at most two a fragment.
+        int ahead = 1;
 #pragma unroll
-                for (int i = 0; i < FM; ++i)
-#pragma unroll
-                    for (int j = 0; j < FW; ++j) asm volatile("" : "+v"(acc[i][j]));
-                arrive();
-                barrier();
-                bring();
-            }
-            Operand<F16> passing;
-            passing.set(ring[q % R]);
-#pragma unroll
-            for (int h = 0; h < (SX ? 1 : H); ++h)
-#pragma unroll
-                for (int s = 0; s < MATS; ++s) factor[q & 1][h][s] = scale_x[SX ? q % R : h] * sw[s];
-            if (q + R - 1 < S) read_stream(slot, q + R - 1);
-            else read_stream(next, q + R - 1 - S);
+        for (int q = 0; q < S - T; ++q) {
+            passing[0].set(ring[q % R]);
+            if constexpr (SX) scale(0, scale_x[q % R]);
 #pragma unroll
             for (int h = 0; h < H; ++h) {
-                sum[(q * H + h) % 4] = SX ? block_sum(kept[h], passing) : block_sum(passing, kept[h]);
-                add(q * H + h - 2);
-                if (q == S - 1) read_held(next, h);
+                product(q * H + h, passing[0], 0);
+                if (h == 0 || h == H / 2) {
+                    if (ahead < min(q + R, S) && (h == 0 || T > 1)) read_stream(slot, ahead++);
+                }
             }
-            if (q == S - 1) read_sw(next);
+            if constexpr (!F16) spread<H>();
             __builtin_amdgcn_sched_barrier(0);
+        }
+        // Additions stay on this side of the branches: moved behind them, all
+        // their sums would have to be kept.
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FW; ++j) asm volatile("" : "+v"(acc[i][j]));
+        wait_loads<(D - 2) * LOADS>();
+        if (t + 2 == steps && used) clear_used(next);
+        barrier();
+#pragma unroll
+        for (int q = S - T; q < S; ++q) {
+            passing[q - S + T].set(ring[q % R]);
+            if constexpr (SX) scale(q - S + T, scale_x[q % R]);
+        }
+        read_stream(next, 0);
+        if constexpr (!F16) __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+#pragma unroll
+            for (int q = 0; q < T; ++q) {
+                const int n = h * T + q;
+                product(MAIN + n, passing[q], q);
+                // The step's loads, spread over these products: a wavefront that
+                // issues many in a row waits for the memory path to take them.
+#pragma unroll
+                for (int k = n * LOADS / (H * T); k < (n + 1) * LOADS / (H * T); ++k) load(from, k);
+                if constexpr (!F16) __builtin_amdgcn_sched_barrier(0);
+            }
+            read_held(next, h);
+            if (h == H - 1) read_sw(next);
+            if constexpr (!F16) __builtin_amdgcn_sched_barrier(0);
         }
     };
 
@@ -469,14 +526,16 @@ __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_f8_block(Args p) {
     int side = 0;                // of the two places for the bias
     load_bias(cur, biases);
 #pragma unroll
-    for (int d = 0; d < D; ++d)
-        if (d < steps) load(d, d);
-    wait_batches<LOADS, D - 1>(steps - 1);
+    for (int d = 0; d < D; ++d) {
+        const Source from = source(d, d, d < steps);
+#pragma unroll
+        for (int k = 0; k < LOADS; ++k) load(from, k);
+    }
+    wait_loads<(D - 1) * LOADS>();
     if (steps == 1 && used) clear_used(0);
     barrier();
     for (int slot = 0;;) {
-#pragma unroll
-        for (int q = 0; q < R - 1; ++q) read_stream(slot, q);
+        read_stream(slot, 0);
 #pragma unroll
         for (int h = 0; h < H; ++h) read_held(slot, h);
         read_sw(slot);
@@ -485,35 +544,23 @@ __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_f8_block(Args p) {
 #pragma unroll
             for (int j = 0; j < FW; ++j) acc[i][j] = f32x4_t{0, 0, 0, 0};
         sum[2] = sum[3] = f32x4_t{0, 0, 0, 0};
-#pragma unroll
-        for (int h = 0; h < (SX ? 1 : H); ++h)
-#pragma unroll
-            for (int s = 0; s < MATS; ++s) factor[1][h][s] = 0.f;
+        factor[2] = factor[3] = 0.f;
         // The last D steps load the next tile's first.
         Place nxt = cur;
-        bool loads = steps > D;
-        for (int t = 0, end = loads ? steps - D : 0;;) {
+        bool more = steps > D;
+        for (int t = 0, end = more ? steps - D : 0;;) {
             for (; t < end; ++t) {
-                step(t, slot,
-                     [&] {
-                         if (loads) wait_loads<(D - 2) * LOADS>();
-                         else wait_batches<LOADS, D - 2>(steps - t - 2);
-                         if (t + 2 == steps && used) clear_used(after(slot));
-                     },
-                     [&] {
-                         if (loads) load(slot, t + D < steps ? t + D : t + D - steps);
-                     });
+                step(t, slot, source(slot, t + D < steps ? t + D : t + D - steps, more));
                 slot = after(slot);
             }
             if (end == steps) break;
             end = steps;
-            loads = G == 1 && steps >= D && place(id + (int)gridDim.x, nxt);
-            if (loads) {
+            more = G == 1 && steps >= D && place(id + (int)gridDim.x, nxt);
+            if (more) {
                 aim(nxt);
                 load_bias(nxt, biases + (side ^ 1) * BN);
             }
         }
-        const bool more = loads;
         add(-2);
         add(-1);
         constexpr int C = TWO ? 2 * FW : 4 * FW;      // consecutive columns of a lane
@@ -526,6 +573,7 @@ __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_f8_block(Args p) {
             // The groups' sums meet in the ring's place, and group g finishes
             // rows g, g + G, .. of the fragments.
             static_assert(G * W * FM * FW * 1024 <= D * STAGE, "the sums fit the ring");
+            wait_loads<0>();
             __syncthreads();
             f32x4_t *part = reinterpret_cast<f32x4_t *>(lds) + wave * (FM * FW * 64) + lane;
 #pragma unroll
@@ -543,7 +591,7 @@ __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_f8_block(Args p) {
             }
             return;
         }
-        if (!more) return;
+        if (!more) return wait_loads<0>();     // LDS is theirs until they have ended
         id += gridDim.x;
         cur = nxt;
         side ^= 1;
