@@ -17,7 +17,7 @@
  *     P[m, n] = sum_b a_scales[m, b] * w_scales[b(n), b] * sum_{k in block b} a[m, k] w[n, k]
  *
  * How far P may be off.  S is the sum of |each product| with its scales.
- *  - float32 outputs, and few rows: products are exact, and the sums of a
+ *  - float32 outputs: products are exact, and the sums of a
  *    block are of fp32's accuracy (within 2^-20 of the sum of their
  *    magnitudes); scales are multiplied and blocks added in fp32.  P is within
  *    (2^-20 + (KB + 3) 2^-24) S.
@@ -27,9 +27,8 @@
  *    7 * 2^-13 times the largest product of each eight (in practice 2^-16 of
  *    the result for values of a normal distribution), where the output's own
  *    rounding is 2^-11 or 2^-8.
- * Which sizes count as few rows is the library's choice, so for 16-bit outputs
- * the last digits of a row may depend on how many others there are.  Scales of
- * Inf or NaN and codes of NaN make what they enter Inf or NaN as fp32
+ * The order of the sums goes with the sizes, so the last digits of a row may
+ * depend on how many others there are.  Scales of Inf or NaN and codes of NaN make what they enter Inf or NaN as fp32
  * arithmetic does.  Products of two scales should be in the normal range of
  * fp32: below it their last bits are lost, above it they are Inf.
  *

@@ -19,8 +19,9 @@
 //         multiply-adds, 3670 TFLOP/s (4420 without them).
 //   f16   v_cvt_scalef32_pk_f16_fp8, which is exact, and
 //         v_mfma_f32_16x16x32_f16, whose sums are within 2^-26 (same codes).
-//         For float32 outputs, and for few rows, where the weights' stream decides.
-//         1860 TFLOP/s, conversions and all.
+//         For float32 outputs.  1860 TFLOP/s, conversions and all: one takes eight
+//         cycles of a SIMD, two values a lane, and each operand of 16 rows is
+//         sixteen of them beside the four products of 16 cycles it enters.
 #include "q4_common.h"
 #include "q4f8.h"
 #include "q4_tiles.h"
@@ -51,6 +52,7 @@ struct Args {
     int dh_type, y_type, M, N, K;
     int tiles_m, tiles_n;      // kHalves, kQuarters: of the tiles that are divided
     Part part;
+    int whole;                 // kWhole: tiles that are taken; else: tiles before those that are divided
     bool once;                 // the weights' stream is more than a cache would keep
     bool share;                // several row tiles read the same weights
 };
@@ -293,12 +295,12 @@ __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_f8_block(Args p) {
     const int wave = all_waves % W, group = all_waves / W;
     const int wm = wave / WN, wn = wave % WN;
     const int KB = (p.K + BK - 1) / BK, steps = (KB + G - 1) / G;
-    const int all = p.tiles_m * p.tiles_n, whole = whole_rounds(all);
+    const int tiles = p.part == kWhole ? p.whole : p.tiles_m * p.tiles_n;
     struct Place { int m0, rows, n0; };
     auto place = [&](int id, Place &at) {
-        const int b = p.part >= kHalves ? whole + (id >> (p.part - kHalves + 1)) : id;
+        const int b = p.part >= kHalves ? p.whole + (id >> (p.part - kHalves + 1)) : id;
         int tm, tn;
-        if (b >= (p.part == kWhole ? whole : all) || !tile_of(b, p.tiles_m, p.tiles_n, tm, tn)) return false;
+        if (b >= tiles || !tile_of(b, p.tiles_m, p.tiles_n, tm, tn)) return false;
         const int bm = p.part >= kHalves ? 2 * BM : BM;
         at.m0 = tm * bm;
         at.n0 = tn * BN;
@@ -610,7 +612,7 @@ __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_f8_block(Args p) {
 // Blocks past K repeat the row's last 16 bytes against activations of zero.
 constexpr int kFewDepth = 2;
 
-template <int NX, int FN, Mode MODE, int W>
+template <int NX, int FN, Mode MODE, bool F16, int W>
 __global__ __launch_bounds__(W * 64) void gemm_f8_few(Args p, int ks_log2) {
     constexpr int FM = (NX + 1) / 2, BM = 8 * NX, MATS = MODE == kPlain ? 1 : 2, FW = FN * MATS;
     constexpr int D = kFewDepth, LOADS = 2 * FW + NX + 1;               // load instructions of a block
@@ -686,7 +688,7 @@ __global__ __launch_bounds__(W * 64) void gemm_f8_few(Args p, int ks_log2) {
                 v.hi = *reinterpret_cast<const i32x4_t *>(at + f * 2048 + (fr ^ 64));
                 return v;
             };
-            Operand<true> w[FW];
+            Operand<F16> w[FW];
 #pragma unroll
             for (int j = 0; j < FW; ++j) w[j].set(read(j));
 #pragma unroll
@@ -697,7 +699,7 @@ __global__ __launch_bounds__(W * 64) void gemm_f8_few(Args p, int ks_log2) {
                     if (u * 8 + g >= kc) v.lo = i32x4_t{0, 0, 0, 0};
                     if (u * 8 + 4 + g >= kc) v.hi = i32x4_t{0, 0, 0, 0};
                 }
-                Operand<true> x;
+                Operand<F16> x;
                 x.set(v);
 #pragma unroll
                 for (int j = 0; j < FW; ++j) add_scaled(acc[i][j], block_sum(w[j], x), s * sw[j / FN]);
@@ -776,7 +778,7 @@ Split split_of(const Args &p, int bm, int cols, int most) {
     return s;
 }
 
-template <int NX, int FN, Mode MODE, int W>
+template <int NX, int FN, Mode MODE, bool F16, int W>
 int launch_few(Args p, const Split &s, const Target &to) {
     constexpr int FM = (NX + 1) / 2, FW = MODE == kPlain ? FN : 2 * FN, kLds = W * kFewDepth * ((2 * FW + 2 * FM) * 1024 + 256);
     p.share = s.tiles > 1;
@@ -786,16 +788,16 @@ int launch_few(Args p, const Split &s, const Target &to) {
     const int64_t grid = s.tiles * p.tiles_n;
     if (grid * (W * 64) > kMaxThreads) return Q4_EINVAL;
     if (to.report) return planned(to, 8 * NX, (W >> s.log2) * 16 * FN, grid, W * 64);
-    gemm_f8_few<NX, FN, MODE, W><<<(unsigned)grid, W * 64, kLds, to.stream>>>(p, s.log2);
+    gemm_f8_few<NX, FN, MODE, F16, W><<<(unsigned)grid, W * 64, kLds, to.stream>>>(p, s.log2);
     return q4::launch_status();
 }
 
-template <int NX, int FN, Mode MODE, int MOST = 8>
+template <int NX, int FN, Mode MODE, bool F16, int MOST = 8>
 int launch_few(const Args &p, const Target &to) {
     const Split s = split_of(p, 8 * NX, 16 * FN, MOST);
     if constexpr (MOST == 8)
-        if (s.waves == 8) return launch_few<NX, FN, MODE, 8>(p, s, to);
-    return launch_few<NX, FN, MODE, 4>(p, s, to);
+        if (s.waves == 8) return launch_few<NX, FN, MODE, F16, 8>(p, s, to);
+    return launch_few<NX, FN, MODE, F16, 4>(p, s, to);
 }
 
 template <int BM, int BW, int WM, int WN, int G, int D, Mode MODE, bool F16>
@@ -808,8 +810,8 @@ int launch_block(Args p, const Target &to) {
     p.tiles_n = (int)tiles_of(p.N, (p.part == kQuarters ? 2 : 1) * kBN);
     int64_t grid = (int64_t)p.tiles_m * p.tiles_n;
     if (grid > 1 << 30) return Q4_EINVAL;
-    if (p.part == kWhole) grid = whole_rounds((int)grid);
-    if (p.part >= kHalves) grid = (grid - whole_rounds((int)grid)) << (p.part - kHalves + 1);
+    if (p.part == kWhole) grid = p.whole;
+    if (p.part >= kHalves) grid = (grid - p.whole) << (p.part - kHalves + 1);
     // Workgroups that stay and go through the tiles, each loading its next one
     // while it finishes the last.
     const int64_t steps = tiles_of(p.K, BK);
@@ -862,36 +864,51 @@ Kernel choose(const Args &p, int mats) {
     return best;
 }
 
+// Tiles come in rounds of `slots`, as many as the chip holds at a time.  Where
+// the last round would have few, it goes to a launch of smaller tiles.
+void split_rounds(Args &p, int64_t all, int slots) {
+    const int64_t left = all % slots;
+    if (all < slots || !left || left > kRestMost) return;
+    p.part = kWhole;
+    p.whole = (int)(all - left);
+}
+
 template <Mode MODE, bool F16>
 int launch(const Args &p, Kernel k, const Target &to) {
     constexpr bool TWO = MODE != kPlain;
-    // Two workgroups share a CU with a ring of two stages; where there is only
-    // one for each CU, it takes four.
+    // Where there is only one workgroup for each CU, its ring has more stages.
     auto alone = [&](int bm, int bw) { return tiles_of(p.M, bm) * tiles_of(p.N, TWO ? bw / 2 : bw) <= kCUs; };
     // Two matrices halve the columns of a lane's run: four rows of wavefronts
     // then store whole lines.
     constexpr int kM = TWO ? 4 : 2, kN = TWO ? 2 : 4;
     switch (k) {
-    case kFew8: return launch_few<1, 1, MODE>(p, to);
-    case kFew16: return launch_few<2, 1, MODE>(p, to);
-    case kFew32: return launch_few<4, 1, MODE>(p, to);
-    case kFew32x32: return launch_few<4, TWO ? 1 : 2, MODE>(p, to);
-    case kFew64: return launch_few<8, TWO ? 1 : 2, MODE, 4>(p, to);
+    case kFew8: return launch_few<1, 1, MODE, F16>(p, to);
+    case kFew16: return launch_few<2, 1, MODE, F16>(p, to);
+    case kFew32: return launch_few<4, 1, MODE, F16>(p, to);
+    case kFew32x32: return launch_few<4, TWO ? 1 : 2, MODE, F16>(p, to);
+    case kFew64: return launch_few<8, TWO ? 1 : 2, MODE, F16, 4>(p, to);
     case kTile64: return launch_block<64, 128, 2, 4, 1, 3, MODE, F16>(p, to);
     case kTileDeep:
         if (alone(64, 64)) return launch_block<64, 64, 2, 2, 2, 4, MODE, F16>(p, to);
         return launch_block<64, 64, 2, 2, 2, 2, MODE, F16>(p, to);
-    case kTile128:
+    case kTile128: {
         if (alone(128, 128)) return launch_block<128, 128, kM, kN, 1, 4, MODE, F16>(p, to);
-        return launch_block<128, 128, kM, kN, 1, 2, MODE, F16>(p, to);
+        // Four wavefronts, of 64 x 64: two workgroups a CU, neither of which
+        // waits at the other's barriers.
+        Args q = p;
+        split_rounds(q, tiles_of(p.M, 128) * tiles_of(p.N, TWO ? 64 : 128), 2 * kCUs);
+        if (int st = launch_block<128, 128, 2, 2, 1, 2, MODE, F16>(q, to)) return st;
+        if (q.part == kAll) return Q4_OK;
+        q.part = kQuarters;
+        return launch_block<64, 64, 2, 2, 2, 4, MODE, F16>(q, to);
+    }
     case kTileWide: return launch_block<128, 256, kM, kN, 1, 3, MODE, F16>(p, to);
     default:
         if constexpr (F16) return Q4_EINVAL;         // not chosen
         else {
-            // Whole rounds, then the tiles that are left, divided.
             Args q = p;
             const int64_t all = tiles_of(p.M, 256) * tiles_of(p.N, TWO ? 128 : 256), left = all % kCUs;
-            if (all >= kCUs && left && left <= kRestMost) q.part = kWhole;
+            split_rounds(q, all, kCUs);
             if (int st = launch_block<256, 256, kM, kN, 1, 2, MODE, false>(q, to)) return st;
             if (q.part == kAll) return Q4_OK;
             if (left > kQuartersMost) {
