@@ -189,7 +189,7 @@ PyObject *quant(PyObject *, PyObject *const *args, Py_ssize_t n) {
     {
         const NoGil no_gil;
         codes = given ? *gc : at::empty({in.rows, in.cols}, in.codes());
-        scales = given ? *gs : at::empty({KB, in.rows}, in.scales()).t();
+        scales = given ? *gs : at::empty_strided({in.rows, KB}, {1, in.rows}, in.scales());
         status = g.quant(in.x->data_ptr(), in.type, static_cast<uint8_t *>(codes.data_ptr()), ptr<float>(&scales),
                          stride_of(scales, 0), stride_of(scales, 1), (int)in.rows, (int)in.cols, on.stream);
     }

@@ -825,39 +825,86 @@ int launch_block(Args p, const Target &to) {
 
 enum Kernel { kFew8, kFew16, kFew32, kFew32x32, kFew64, kTile64, kTile128, kTileWide, kTile256, kTileDeep, kKernels };
 
-// The kernel for a call's sizes, by estimated times.
+// Estimated times, in us.  Tiles: for one, and for a step of it (`many`: where a
+// CU has several, each of them); tiles that have a CU to themselves come in
+// whole rounds.  Few rows: the start, a block of a wavefront alone and for each of
+// the CU's (of two matrices), the blocks that the ring's first wait stands for; and,
+// as the weights are read past the L2 again for every row tile, a MB of them,
+// what each more row tile adds of that, and what the cache takes off.
+struct Linear { double start, step; double at(int64_t steps) const { return start + step * (double)steps; } };
+struct FewCost { double start, block, shared, shared_two, first; };
+struct Costs {
+    FewCost few8, few16, few32, few32x32, few64;
+    double mb, again, off;
+    Linear deep, deep_many;
+    double stretch;            // of 64 x 128 tiles, by tiles a CU
+    Linear tile64, tile128, tile128_many, wide, tile256;
+};
+// Fitted to 1000 calls (9 to 8192 rows, N 64 to 14336, K 128 to 14336, one matrix and
+// two; up to six sets of operands in turn, in a graph), in which the choice is on
+// average 0.6% behind the best kernel for 16-bit outputs and 1.2% for float32,
+// 5% and 7% or more in one of twenty.  Where they decide: 64 x 4096 x 14336
+// takes 21.2 us in tiles of 32 x 32, 26.6 in 32 x 16, 28.8 in 64 x 32 and 39.5 in
+// 64 x 64; at 128 rows these are 32.3, 42.1, 27.3 and 38.1.  1024 x 4096 x 4096
+// takes 25.6 us in 128 x 128, 29.1 in 64 x 128 and 34.3 in 128 x 256, 8192 x
+// 14336 x 4096 413 in 256 x 256, 508 in 128 x 256 and 536 in 128 x 128.
+constexpr Costs kCosts16 = {{-0.344, 0.353, 0.045, 0.057, 0.963},
+                            {-0.680, 0.451, 0.058, 0.084, 0.407},
+                            {-0.502, 0.668, 0.078, 0.133, 0.682},
+                            {-0.231, 0.192, 0.128, 0.128, 1.067},
+                            {0.357, 0.616, 0.181, 0.635, 1.769},
+                            0.184, 0.519, 0.55,
+                            {1.457, 0.380}, {3.787, 0.591},
+                            1.076, {2.484, 0.498}, {2.699, 0.540}, {0.435, 0.537}, {7.803, 0.552}, {2.800, 1.215}};
+constexpr Costs kCosts32 = {{-0.615, 0.142, 0.036, 0.046, 0.912},
+                            {-0.567, 0.240, 0.046, 0.051, 0.395},
+                            {-0.536, 0.306, 0.073, 0.100, 0.373},
+                            {-0.262, 0.316, 0.115, 0.115, 0.348},
+                            {0.757, 0.668, 0.197, 1.015, 2.179},
+                            0.134, 0.651, 1.153,
+                            {0.635, 0.406}, {1.294, 0.752},
+                            0.999, {0.810, 0.558}, {0.878, 0.558}, {2.080, 0.780}, {4.298, 1.488}, {0., 0.}};
+
+// The kernel for a call's sizes: up to 8 rows the weights' stream decides; above,
+// the least estimated time.
 Kernel choose(const Args &p, int mats) {
     const int64_t steps = tiles_of(p.K, BK);
-    const bool f16 = p.y_type == I8_F32;
+    const bool f16 = p.y_type == I8_F32, two = mats == 2;
+    const Costs &c = f16 ? kCosts32 : kCosts16;
     if (p.M <= 8) return kFew8;
     if (p.K < BK) return p.M <= 16 ? kFew16 : kFew32;
     auto tiles = [&](int bm, int bw) { return tiles_of(p.M, bm) * tiles_of(p.N, bw / mats); };
-    auto rounds = [&](int bm, int bw) { return (double)((tiles(bm, bw) + kCUs - 1) / kCUs); };
+    auto rounds = [&](int64_t t) { return (double)((t + kCUs - 1) / kCUs); };
     // Tiles a CU, 1 where there are fewer, and the time of one alone or of one among others.
-    auto each = [&](int64_t t, double one, double many) { return t <= kCUs ? one : (double)t / kCUs * many; };
-    auto few = [&](int bm, int cols, int most, double start, double unit, double shared, double first) {
+    auto each = [&](int64_t t, const Linear &one, const Linear &many) {
+        return t <= kCUs ? one.at(steps) : (double)t / kCUs * many.at(steps);
+    };
+    auto few = [&](int bm, int cols, int most, const FewCost &f) {
         const Split s = split_of(p, bm, cols, most);
         const int64_t tm = tiles_of(p.M, bm), wgs = tm * tiles_of(s.strips, s.waves >> s.log2);
-        const double a_unit = std::max(unit, shared * (double)(tiles_of(wgs, kCUs) * s.waves));
+        const double block = std::max(f.block, (two ? f.shared_two : f.shared) * (double)(tiles_of(wgs, kCUs) * s.waves));
         const double mb = (double)mats * p.N * p.K * 1e-6;
-        return std::max(start + a_unit * (first + (double)tiles_of(steps, 1 << s.log2)),
-                        0.32 * mb * (1. + 0.4 * (double)(tm - 1)) - 1.5);
+        return std::max(f.start + block * (f.first + (double)tiles_of(steps, 1 << s.log2)),
+                        c.mb * mb * (1. + c.again * (double)(tm - 1)) - c.off);
     };
-    const bool two = mats == 2;
     double cost[kKernels];
-    cost[kFew8] = few(8, 16, 8, -0.5, 0.15, two ? 0.050 : 0.031, 0.81);
-    cost[kFew16] = few(16, 16, 8, -0.7, 0.24, two ? 0.099 : 0.043, 0.5);
-    cost[kFew32] = few(32, 16, 8, -0.4, 0.30, two ? 0.154 : 0.11, 0.74);
-    cost[kFew32x32] = few(32, 32, 8, -0.23, 0.33, 0.14, 0.56);       // with one matrix
-    cost[kFew64] = few(64, two ? 16 : 32, 4, 0.74, 0.63, 0.25, 0.75);
-    cost[kTileDeep] = each(tiles(64, 64), 0.67 + steps * 0.38, 0.78 + steps * 0.40);
-    cost[kTile64] = std::max(1.0, (double)tiles(64, 128) / kCUs * 1.2) * (0.67 + steps * 0.42);
-    cost[kTile128] = each(tiles(128, 128), 2.25 + steps * 0.46, 0.63 + steps * 0.78);
-    cost[kTileWide] = rounds(128, 256) * (6.54 + steps * (f16 ? 1.2 : 0.75));
+    cost[kFew8] = few(8, 16, 8, c.few8);
+    cost[kFew16] = few(16, 16, 8, c.few16);
+    cost[kFew32] = few(32, 16, 8, c.few32);
+    cost[kFew32x32] = few(32, 32, 8, c.few32x32);      // with one matrix
+    cost[kFew64] = few(64, two ? 16 : 32, 4, c.few64);
+    cost[kTileDeep] = each(tiles(64, 64), c.deep, c.deep_many);
+    cost[kTile64] = std::max(1.0, (double)tiles(64, 128) / kCUs * c.stretch) * c.tile64.at(steps);
+    const int64_t t128 = tiles(128, 128), left128 = t128 % (2 * kCUs);
+    cost[kTile128] = t128 >= 2 * kCUs && left128 && left128 <= kRestMost
+                         ? (double)(t128 - left128) / kCUs * c.tile128_many.at(steps) +
+                               each(4 * left128, c.deep, c.deep_many)
+                         : each(t128, c.tile128, c.tile128_many);
+    cost[kTileWide] = rounds(tiles(128, 256)) * c.wide.at(steps);
     const int64_t t256 = tiles(256, 256), left = t256 % kCUs;
-    const double divided = left > kQuartersMost ? 6.54 + steps * 0.75 : left ? 2.25 + steps * 0.46 : 0.;
-    cost[kTile256] = t256 < kCUs || left > kRestMost ? rounds(256, 256) * (8.0 + steps * 1.33)
-                                                     : (double)(t256 / kCUs) * (8.0 + steps * 1.33) + divided;
+    const double divided = left > kQuartersMost ? c.wide.at(steps) : left ? c.tile128.at(steps) : 0.;
+    cost[kTile256] = t256 < kCUs || left > kRestMost ? rounds(t256) * c.tile256.at(steps)
+                                                     : (double)(t256 / kCUs) * c.tile256.at(steps) + divided;
     Kernel best = kFew8;
     for (Kernel k : {kFew16, kFew32, kFew32x32, kFew64, kTileDeep, kTile64, kTile128, kTileWide, kTile256})
         if (cost[k] < cost[best] && !(two && k == kFew32x32) && !(f16 && k == kTile256)) best = k;
