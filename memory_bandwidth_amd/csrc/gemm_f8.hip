@@ -830,13 +830,15 @@ enum Kernel { kFew8, kFew16, kFew32, kFew32x32, kFew64, kTile64, kTile128, kTile
 // whole rounds.  Few rows: the start, a block of a wavefront alone and for each of
 // the CU's (of two matrices), the blocks that the ring's first wait stands for; and,
 // as the weights are read past the L2 again for every row tile, a MB of them,
-// what each more row tile adds of that, and what the cache takes off.
+// what each more row tile adds of that, and what the cache takes off.  64 x 64
+// tiles are for where there is one for each CU at most; 32 x 32 and 64 x 32 for one
+// matrix.
 struct Linear { double start, step; double at(int64_t steps) const { return start + step * (double)steps; } };
 struct FewCost { double start, block, shared, shared_two, first; };
 struct Costs {
     FewCost few8, few16, few32, few32x32, few64;
     double mb, again, off;
-    Linear deep, deep_many;
+    Linear deep;
     double stretch;            // of 64 x 128 tiles, by tiles a CU
     Linear tile64, tile128, tile128_many, wide, tile256;
 };
@@ -854,7 +856,7 @@ constexpr Costs kCosts16 = {{-0.344, 0.353, 0.045, 0.057, 0.963},
                             {-0.231, 0.192, 0.128, 0.128, 1.067},
                             {0.357, 0.616, 0.181, 0.635, 1.769},
                             0.184, 0.519, 0.55,
-                            {1.457, 0.380}, {3.787, 0.591},
+                            {1.457, 0.380},
                             1.076, {2.484, 0.498}, {2.699, 0.540}, {0.435, 0.537}, {7.803, 0.552}, {2.800, 1.215}};
 constexpr Costs kCosts32 = {{-0.615, 0.142, 0.036, 0.046, 0.912},
                             {-0.567, 0.240, 0.046, 0.051, 0.395},
@@ -862,7 +864,7 @@ constexpr Costs kCosts32 = {{-0.615, 0.142, 0.036, 0.046, 0.912},
                             {-0.262, 0.316, 0.115, 0.115, 0.348},
                             {0.757, 0.668, 0.197, 1.015, 2.179},
                             0.134, 0.651, 1.153,
-                            {0.635, 0.406}, {1.294, 0.752},
+                            {0.635, 0.406},
                             0.999, {0.810, 0.558}, {0.878, 0.558}, {2.080, 0.780}, {4.298, 1.488}, {0., 0.}};
 
 // The kernel for a call's sizes: up to 8 rows the weights' stream decides; above,
@@ -887,27 +889,29 @@ Kernel choose(const Args &p, int mats) {
         return std::max(f.start + block * (f.first + (double)tiles_of(steps, 1 << s.log2)),
                         c.mb * mb * (1. + c.again * (double)(tm - 1)) - c.off);
     };
+    constexpr double kNever = 1e30;
     double cost[kKernels];
     cost[kFew8] = few(8, 16, 8, c.few8);
     cost[kFew16] = few(16, 16, 8, c.few16);
     cost[kFew32] = few(32, 16, 8, c.few32);
-    cost[kFew32x32] = few(32, 32, 8, c.few32x32);      // with one matrix
-    cost[kFew64] = few(64, two ? 16 : 32, 4, c.few64);
-    cost[kTileDeep] = each(tiles(64, 64), c.deep, c.deep_many);
+    cost[kFew32x32] = two ? kNever : few(32, 32, 8, c.few32x32);
+    cost[kFew64] = two ? kNever : few(64, 32, 4, c.few64);
+    cost[kTileDeep] = tiles(64, 64) <= kCUs ? c.deep.at(steps) : kNever;
     cost[kTile64] = std::max(1.0, (double)tiles(64, 128) / kCUs * c.stretch) * c.tile64.at(steps);
     const int64_t t128 = tiles(128, 128), left128 = t128 % (2 * kCUs);
     cost[kTile128] = t128 >= 2 * kCUs && left128 && left128 <= kRestMost
                          ? (double)(t128 - left128) / kCUs * c.tile128_many.at(steps) +
-                               each(4 * left128, c.deep, c.deep_many)
+                               rounds(4 * left128) * c.deep.at(steps)
                          : each(t128, c.tile128, c.tile128_many);
     cost[kTileWide] = rounds(tiles(128, 256)) * c.wide.at(steps);
     const int64_t t256 = tiles(256, 256), left = t256 % kCUs;
     const double divided = left > kQuartersMost ? c.wide.at(steps) : left ? c.tile128.at(steps) : 0.;
-    cost[kTile256] = t256 < kCUs || left > kRestMost ? rounds(t256) * c.tile256.at(steps)
-                                                     : (double)(t256 / kCUs) * c.tile256.at(steps) + divided;
+    cost[kTile256] = f16                                 ? kNever        // its fragments would not fit
+                     : t256 < kCUs || left > kRestMost ? rounds(t256) * c.tile256.at(steps)
+                                                       : (double)(t256 / kCUs) * c.tile256.at(steps) + divided;
     Kernel best = kFew8;
     for (Kernel k : {kFew16, kFew32, kFew32x32, kFew64, kTileDeep, kTile64, kTile128, kTileWide, kTile256})
-        if (cost[k] < cost[best] && !(two && k == kFew32x32) && !(f16 && k == kTile256)) best = k;
+        if (cost[k] < cost[best]) best = k;
     return best;
 }
 
@@ -932,12 +936,12 @@ int launch(const Args &p, Kernel k, const Target &to) {
     case kFew8: return launch_few<1, 1, MODE, F16>(p, to);
     case kFew16: return launch_few<2, 1, MODE, F16>(p, to);
     case kFew32: return launch_few<4, 1, MODE, F16>(p, to);
-    case kFew32x32: return launch_few<4, TWO ? 1 : 2, MODE, F16>(p, to);
-    case kFew64: return launch_few<8, TWO ? 1 : 2, MODE, F16, 4>(p, to);
+    case kFew32x32:
+    case kFew64:
+        if constexpr (TWO) return Q4_EINVAL;                                    // not chosen
+        else return k == kFew64 ? launch_few<8, 2, MODE, F16, 4>(p, to) : launch_few<4, 2, MODE, F16>(p, to);
     case kTile64: return launch_block<64, 128, 2, 4, 1, 3, MODE, F16>(p, to);
-    case kTileDeep:
-        if (alone(64, 64)) return launch_block<64, 64, 2, 2, 2, 4, MODE, F16>(p, to);
-        return launch_block<64, 64, 2, 2, 2, 2, MODE, F16>(p, to);
+    case kTileDeep: return launch_block<64, 64, 2, 2, 2, 4, MODE, F16>(p, to);
     case kTile128: {
         if (alone(128, 128)) return launch_block<128, 128, kM, kN, 1, 4, MODE, F16>(p, to);
         // Four wavefronts, of 64 x 64: two workgroups a CU, neither of which

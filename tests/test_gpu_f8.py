@@ -225,10 +225,15 @@ GEMM = [(1, 1, 16), (1, 17, 48), (1, 896, 896), (1, 300, 4096), (2, 64, 128), (3
         (64, 64, 128), (65, 127, 256), (100, 896, 4864), (128, 256, 1024), (129, 300, 1040), (200, 333, 2064),
         (256, 256, 256), (257, 511, 528), (300, 1024, 896), (511, 520, 4112), (700, 777, 1296), (1025, 1030, 400),
         (2049, 260, 144), (260, 4100, 208), (40, 70, 32)]
-LARGE = [(64, 4100, 2064), (500, 2050, 2064), (330, 4870, 912), (1090, 5000, 528), (3775, 1827, 1056),
-         (3984, 3781, 656), (2900, 5050, 528), (4100, 4100, 272), (5000, 300, 4112), (64, 3999, 4112),
-         (230, 3313, 400), (36, 1373, 32), (126, 2093, 6016), (64, 4090, 14336), (128, 3990, 4112),
-         (4300, 4100, 2064), (4096, 5300, 2000), (8200, 4097, 1040), (2304, 2560, 9216), (2518, 2391, 2528), (3808, 1469, 2208)]
+# Every kind of launch that the products choose from, for either way to multiply,
+# with rows and columns that end inside tiles and K inside steps: one tile a
+# workgroup and several, last rounds as they are, in halves and in quarters.
+LARGE = [(64, 4100, 2064), (500, 2050, 2064), (3984, 3781, 656), (64, 3999, 4112), (36, 1373, 32), (126, 2093, 6016),
+         (64, 4090, 14336), (128, 3990, 4112), (4300, 4100, 2064), (2304, 2560, 9216), (18, 9303, 800),
+         (36, 8174, 1472), (38, 6292, 9520), (141, 5177, 800), (3065, 116, 1440), (4868, 387, 656), (5390, 659, 288),
+         (7439, 1399, 272), (3692, 4667, 144), (4715, 1794, 304), (8655, 930, 272), (4771, 5846, 272),
+         (5331, 4596, 656), (3083, 5219, 272), (4378, 345, 288), (7290, 193, 272), (6343, 103, 688),
+         (1804, 4310, 1680), (2910, 2761, 400), (2755, 5834, 400)]
 
 
 @pytest.mark.parametrize("M,N,K", GEMM + LARGE)
@@ -274,16 +279,31 @@ def test_gemm_longest(M, N, t):
     same(q4.gemm_f8(*args, dtype=TYPES[t]), exact_on_gpu(*args), f"{M} {N}")
 
 
-def test_sizes_take_every_tile():
-    for t, tiles in ((torch.float32, {(8,), (16,), (32,), (64, 32), (64, 64), (64, 128), (128, 128), (128, 256)}),
-                     (torch.bfloat16, {(8,), (16,), (32,), (64, 32), (64, 64), (64, 128), (128, 128), (128, 256),
-                                       (256, 256)})):
-        got = [q4.gemm_f8_geometry(1, *s, dtype=t) for s in GEMM + LARGE]
-        seen = {(g["tile_rows"], g["tile_cols"]) for g in got} | {(g["tile_rows"],) for g in got}
-        assert tiles <= seen, tiles - seen
-        # Both kinds of launch: a workgroup for each tile, and workgroups that go through several.
-        many = [g["grid"] < -(-s[0] // g["tile_rows"]) * -(-s[1] // g["tile_cols"]) for g, s in zip(got, GEMM + LARGE)]
-        assert any(many) and not all(many)
+def launches(mats, M, N, K, t):
+    """What a call's launches are: the tile, and whether workgroups go through several, or tiles are left and divided."""
+    g = q4.gemm_f8_geometry(mats, M, N, K, dtype=t)
+    r, wide = g["tile_rows"], g["tile_cols"] * mats
+    tiles = -(-M // r) * -(-N // g["tile_cols"])
+    if r <= 32 or (r, wide) == (64, 32):
+        return r, g["block"]
+    slots = 512 if r <= 128 and wide <= 128 else 256
+    left = tiles % slots
+    name = "one each"
+    if wide <= 256 and r in (128, 256) and wide != 2 * r:
+        whole = tiles >= slots and 0 < left <= 128 and tiles > 256
+        name = ("halves" if r == 256 and left > 64 else "quarters") if whole else name
+    return r, wide, "several" if name == "one each" and g["grid"] < tiles else name
+
+
+def test_sizes_take_every_launch():
+    common = {(8, 256), (8, 512), (16, 256), (16, 512), (32, 256), (32, 512), (64, 64, "one each"), (64, 128, "one each"),
+              (128, 128, "one each"), (128, 128, "several"), (128, 128, "quarters"), (128, 256, "one each")}
+    f32 = common | {(64, 128, "several"), (128, 256, "several")}
+    f16 = common | {(256, 256, "one each"), (256, 256, "several"), (256, 256, "halves"), (256, 256, "quarters")}
+    for mats, shapes, more in ((1, GEMM + LARGE, {(64, 256)}), (2, GATED, set())):
+        for t, want in ((torch.float32, f32), (torch.bfloat16, f16)):
+            seen = {launches(mats, *s, t) for s in shapes}
+            assert want | more <= seen, (mats, t, (want | more) - seen)
 
 
 @pytest.mark.parametrize("t", TYPES)
@@ -304,9 +324,11 @@ def test_gemm_out_in_a_larger_buffer(t, M, N, skew):
 # ---------------------------------------------------------------- gates, on exact products
 
 GATED = [(1, 1, 16), (1, 896, 896), (4, 300, 4096), (16, 65, 144), (30, 1000, 1040), (64, 32, 128), (100, 130, 2816),
-         (257, 200, 528), (520, 515, 1296), (64, 2100, 2064), (300, 1000, 2064), (200, 2320, 912), (1060, 2500, 528),
-         (2593, 1533, 800), (2365, 3095, 432), (1500, 4100, 400), (96, 999, 4112), (67, 3422, 368), (40, 1100, 1040),
-         (40, 499, 8208), (40, 1373, 48), (100, 1789, 6160), (4300, 2050, 2064), (4096, 2650, 2000), (8200, 2049, 1040)]
+         (257, 200, 528), (520, 515, 1296), (64, 2100, 2064), (1500, 4100, 400), (96, 999, 4112), (40, 499, 8208),
+         (40, 1373, 48), (100, 1789, 6160), (4300, 2050, 2064), (9, 10, 16), (9, 9, 1056), (17, 9, 16), (4189, 9, 16),
+         (19, 2724, 1040), (33, 6864, 1104), (35, 8135, 5824), (8550, 92, 784), (5390, 330, 288), (7439, 700, 272),
+         (7056, 1172, 144), (4715, 897, 304), (8655, 465, 272), (4771, 2923, 272), (5331, 2298, 656), (3083, 2610, 272),
+         (5470, 151, 320), (1804, 2155, 1680), (2910, 1381, 400), (2755, 2917, 400)]
 
 
 def gated_problem(M, N, K, size=4.0):
