@@ -109,42 +109,47 @@ __device__ __forceinline__ float uniform_load(const float *p) {
     return *reinterpret_cast<uniform_float *>(reinterpret_cast<uintptr_t>(p));
 }
 
-// Reads the run of C columns from n on of a row of dh, zero past N.
-template <int C>
-__device__ __forceinline__ void load_run(const void *base, int type, size_t at, int n, int N, float (&v)[C]) {
+// A run of C columns from n on of a row of dh as it lies there, zero past N: a
+// word a value (WIDE) or two values of 16 bits.
+template <int C, bool WIDE>
+__device__ __forceinline__ void load_run(const void *base, size_t at, int n, int N, uint32_t (&raw)[WIDE ? C : C / 2]) {
     const bool whole = n + C <= N;
-    if (type == I8_F32) {
-        const float *p = static_cast<const float *>(base) + at;
+    if constexpr (WIDE) {
+        const uint32_t *p = static_cast<const uint32_t *>(base) + at;
         if (whole) {
 #pragma unroll
             for (int c = 0; c < C; c += 4) {
                 const u32x4_t r = *reinterpret_cast<const u32x4_at4_t *>(p + c);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) { const uint32_t b = r[i]; v[c + i] = __builtin_bit_cast(float, b); }
+                raw[c] = r[0], raw[c + 1] = r[1], raw[c + 2] = r[2], raw[c + 3] = r[3];
             }
         } else {
 #pragma unroll
-            for (int c = 0; c < C; ++c) v[c] = n + c < N ? p[c] : 0.f;
-        }
-        return;
-    }
-    const uint16_t *p = static_cast<const uint16_t *>(base) + at;
-    uint32_t b[C / 2];
-    if (whole) {
-#pragma unroll
-        for (int c = 0; c < C / 2; c += 2) {
-            const u32x2_t r = *reinterpret_cast<const u32x2_at2_t *>(p + 2 * c);
-            b[c] = r[0], b[c + 1] = r[1];
+            for (int c = 0; c < C; ++c) raw[c] = n + c < N ? p[c] : 0u;
         }
     } else {
+        const uint16_t *p = static_cast<const uint16_t *>(base) + at;
+        if (whole) {
 #pragma unroll
-        for (int c = 0; c < C / 2; ++c)
-            b[c] = (n + 2 * c < N ? (uint32_t)p[2 * c] : 0u) | (n + 2 * c + 1 < N ? (uint32_t)p[2 * c + 1] << 16 : 0u);
+            for (int c = 0; c < C / 2; c += 2) {
+                const u32x2_t r = *reinterpret_cast<const u32x2_at2_t *>(p + 2 * c);
+                raw[c] = r[0], raw[c + 1] = r[1];
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < C / 2; ++c)
+                raw[c] = (n + 2 * c < N ? (uint32_t)p[2 * c] : 0u) |
+                         (n + 2 * c + 1 < N ? (uint32_t)p[2 * c + 1] << 16 : 0u);
+        }
     }
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-        const uint32_t h = b[c / 2] >> (16 * (c & 1)) & 0xFFFFu;
-        v[c] = type == I8_F16 ? (float)__builtin_bit_cast(_Float16, (uint16_t)h) : __builtin_bit_cast(float, h << 16);
+}
+template <bool WIDE>
+__device__ __forceinline__ float value_of(const uint32_t *raw, int type, int c) {
+    if constexpr (WIDE) {
+        const uint32_t b = raw[c];
+        return __builtin_bit_cast(float, b);
+    } else {
+        const uint32_t h = raw[c / 2] >> (16 * (c & 1)) & 0xFFFFu;
+        return type == I8_F16 ? (float)__builtin_bit_cast(_Float16, (uint16_t)h) : __builtin_bit_cast(float, h << 16);
     }
 }
 
@@ -171,6 +176,7 @@ __device__ __forceinline__ void far_gated_gradient(float dh, float g, float u, f
 template <int FM, int C, Mode MODE>
 __device__ __forceinline__ void finish(const Args &p, const f32x4_t (&acc)[FM][MODE == kPlain ? C / 4 : C / 2], int m0,
                                        int rows, const float *bias, int row0, int n, int lane) {
+    constexpr int UP = C / 4;                            // fragments of gate
     float add[C];
     if constexpr (MODE == kPlain) {
 #pragma unroll
@@ -181,43 +187,73 @@ __device__ __forceinline__ void finish(const Args &p, const f32x4_t (&acc)[FM][M
     for (int i = 0; i < FM; ++i) {
         const int r = row0 + i * 16 + (lane & 15);
         if (r >= rows) continue;
-        const size_t m = (size_t)(m0 + r);
+        const size_t at = (size_t)(m0 + r) * p.N + n;
+        float v[C];
         if constexpr (MODE == kPlain) {
-            float v[C];
 #pragma unroll
             for (int c = 0; c < C; ++c) v[c] = acc[i][c >> 2][c & 3] + add[c];
-            store_run<C>(p.y, p.y_type, m * p.N + n, n, p.N, v);
         } else {
-            constexpr int UP = C / 4;                    // fragments of gate
             float least = 0.f;
 #pragma unroll
-            for (int c = 0; c < C; ++c) least = __builtin_fminf(least, acc[i][c >> 2][c & 3]);
-            if constexpr (MODE == kGated) {
-                float v[C];
-#pragma unroll
-                for (int c = 0; c < C; ++c) v[c] = silu(acc[i][c >> 2][c & 3]) * acc[i][UP + (c >> 2)][c & 3];
-                if (__builtin_expect(least < kFar, 0)) {         // rare, and then of no account
-#pragma unroll
-                    for (int c = 0; c < C; ++c) {
-                        const float g = acc[i][c >> 2][c & 3];
-                        if (g < kFar) v[c] = far_silu(g, acc[i][UP + (c >> 2)][c & 3]);
-                    }
-                }
-                store_run<C>(p.y, p.y_type, m * p.N + n, n, p.N, v);
-            } else {
-                float dg[C], du[C];
-                load_run<C>(p.dh, p.dh_type, m * p.N + n, n, p.N, dg);
+            for (int c = 0; c < C; ++c) {
+                v[c] = silu(acc[i][c >> 2][c & 3]) * acc[i][UP + (c >> 2)][c & 3];
+                least = __builtin_fminf(least, acc[i][c >> 2][c & 3]);
+            }
+            if (__builtin_expect(least < kFar, 0)) {             // rare, and then of no account
 #pragma unroll
                 for (int c = 0; c < C; ++c) {
-                    const float dh = dg[c], g = acc[i][c >> 2][c & 3], u = acc[i][UP + (c >> 2)][c & 3];
-                    gated_gradient(dh, g, u, dg[c], du[c]);
-                    if (__builtin_expect(least < kFar, 0) && g < kFar) far_gated_gradient(dh, g, u, dg[c], du[c]);
+                    const float g = acc[i][c >> 2][c & 3];
+                    if (g < kFar) v[c] = far_silu(g, acc[i][UP + (c >> 2)][c & 3]);
                 }
-                store_run<C>(p.y, p.y_type, m * 2 * p.N + n, n, p.N, dg);
-                store_run<C>(p.y, p.y_type, m * 2 * p.N + p.N + n, n, p.N, du);
             }
         }
+        store_run<C>(p.y, p.y_type, at, n, p.N, v);
     }
+}
+
+// The same for the backward pass.  All rows of dh are on their way before the
+// first is used.
+template <int FM, int C, bool WIDE>
+__device__ __forceinline__ void finish_backward(const Args &p, const f32x4_t (&acc)[FM][C / 2], int m0, int rows,
+                                                int row0, int n, int lane) {
+    constexpr int UP = C / 4;
+    if (n >= p.N) return;
+    uint32_t raw[FM][WIDE ? C : C / 2];
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+        const int r = min(row0 + i * 16 + (lane & 15), rows - 1);
+        load_run<C, WIDE>(p.dh, (size_t)(m0 + r) * p.N + n, n, p.N, raw[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+        const int r = row0 + i * 16 + (lane & 15);
+        if (r >= rows) continue;
+        float dg[C], du[C], least = 0.f;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const float dh = value_of<WIDE>(raw[i], p.dh_type, c), g = acc[i][c >> 2][c & 3];
+            gated_gradient(dh, g, acc[i][UP + (c >> 2)][c & 3], dg[c], du[c]);
+            least = __builtin_fminf(least, g);
+        }
+        if (__builtin_expect(least < kFar, 0)) {
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const float dh = value_of<WIDE>(raw[i], p.dh_type, c), g = acc[i][c >> 2][c & 3];
+                if (g < kFar) far_gated_gradient(dh, g, acc[i][UP + (c >> 2)][c & 3], dg[c], du[c]);
+            }
+        }
+        const size_t at = (size_t)(m0 + r) * 2 * p.N + n;
+        store_run<C>(p.y, p.y_type, at, n, p.N, dg);
+        store_run<C>(p.y, p.y_type, at + p.N, n, p.N, du);
+    }
+}
+
+template <int FM, int C, Mode MODE>
+__device__ __forceinline__ void write_out(const Args &p, const f32x4_t (&acc)[FM][MODE == kPlain ? C / 4 : C / 2],
+                                          int m0, int rows, const float *bias, int row0, int n, int lane) {
+    if constexpr (MODE != kBackward) finish<FM, C, MODE>(p, acc, m0, rows, bias, row0, n, lane);
+    else if (p.dh_type == I8_F32) finish_backward<FM, C, true>(p, acc, m0, rows, row0, n, lane);
+    else finish_backward<FM, C, false>(p, acc, m0, rows, row0, n, lane);
 }
 
 // Loads of the scales of 64 rows for a block: from row `row` on of the tile at
@@ -570,7 +606,7 @@ __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_f8_block(Args p) {
         const int col = wn * (4 * C) + (lane >> 4) * C;
         const float *bias = !TWO && p.bias ? biases + side * BN + col : nullptr;
         if constexpr (G == 1) {
-            finish<FM, C, MODE>(p, acc, cur.m0, cur.rows, bias, wm * (16 * FM), cur.n0 + col, lane);
+            write_out<FM, C, MODE>(p, acc, cur.m0, cur.rows, bias, wm * (16 * FM), cur.n0 + col, lane);
         } else {
             // The groups' sums meet in the ring's place, and group g finishes
             // rows g, g + G, .. of the fragments.
@@ -589,7 +625,7 @@ __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_f8_block(Args p) {
                 for (int g = 0; g < G; ++g)
 #pragma unroll
                     for (int j = 0; j < FW; ++j) sum[0][j] += part[(g * W * FM * FW + i * FW + j) * 64];
-                finish<1, C, MODE>(p, sum, cur.m0, cur.rows, bias, wm * (16 * FM) + i * 16, cur.n0 + col, lane);
+                write_out<1, C, MODE>(p, sum, cur.m0, cur.rows, bias, wm * (16 * FM) + i * 16, cur.n0 + col, lane);
             }
             return;
         }
@@ -745,7 +781,7 @@ __global__ __launch_bounds__(W * 64) void gemm_f8_few(Args p, int ks_log2) {
 #pragma unroll
                 for (int j = 0; j < FW; ++j) acc[i][j] += part[((wave + k) * FM * FW + i * FW + j) * 64];
     }
-    finish<FM, C, MODE>(p, acc, m0, rows, bias, 0, n, lane);
+    write_out<FM, C, MODE>(p, acc, m0, rows, bias, 0, n, lane);
 }
 
 constexpr int kMaxRows = 1 << 24;
