@@ -299,6 +299,7 @@ __device__ __forceinline__ void load_scale(__amdgpu_buffer_rsrc_t r, char *to, u
 // two matrices) those of the columns, a lane 16 of them.  They pass through LDS
 // as well: read through the scalar cache they would make every wait for an LDS
 // read a wait for all.
+
 // Orders what stands between two scheduling barriers: behind each of the
 // products an LDS read and five vector instructions.
 template <int PRODUCTS>
@@ -450,7 +451,8 @@ __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_f8_block(Args p) {
             for (int i = 0; i < LX; ++i)
                 *reinterpret_cast<i32x4_t *>(to + (wave * LX + i) * 1024 + lane * 16) = i32x4_t{0, 0, 0, 0};
         }
-        if (used >= 8 && !of_columns) *reinterpret_cast<float *>(to + scales_at + lane * 4) = 0.f;
+        // A block that the group has not: no scale of it may be infinite either.
+        if (used >= 8) *reinterpret_cast<float *>(to + scales_at + lane * 4) = 0.f;
     };
     auto barrier = [&]() {       // and this wavefront's LDS reads are done
         __builtin_amdgcn_sched_barrier(0);

@@ -459,6 +459,68 @@ def test_rows_do_not_mix(M, t):
     assert np.isfinite(y[:M - 1]).all()
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 300, 400), (9, 300, 400), (40, 300, 656), (141, 5177, 800), (130, 300, 912),
+                                   (600, 515, 400), (3083, 5219, 272)])
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+def test_infinite_scales(M, N, K, t):
+    """A block's sum times an infinite scale, whichever operand has it: infinite, or NaN where the sum is zero."""
+    (a, sa), [w] = short_problem(M, N, K)
+    a, sa, (w, sw) = dev(a), by_block(sa).clone(), pair(w)
+    sw[0, 1] = sw[-1, -1] = np.inf
+    sa[M // 2, 0] = -np.inf
+    y = q4.gemm_f8(a, sa, w, sw, dtype=TYPES[t])
+    want = torch.zeros(M, N, dtype=torch.float64, device=DEV)
+    for b in range(sa.shape[1]):
+        k = slice(128 * b, 128 * b + 128)
+        by = sa[:, b, None].double() * sw[:, b].double().repeat_interleave(128)[:N]
+        want += (a[:, k].double() @ w[:, k].double().t()) * by
+    assert torch.equal(y.isnan(), want.isnan())
+    same(torch.where(y.isnan(), 0, y), torch.where(want.isnan(), 0, want), f"{M} {N} {K}")
+
+
+# ---------------------------------------------------------------- past 32 bits
+
+def test_arrays_past_32_bits():
+    """Operands, scales' blocks and outputs whose last parts lie beyond 4 GiB."""
+    K, N = 131056, 33_000                                  # 4.3 GB of weights
+    w = torch.zeros(N, K, dtype=torch.uint8, device=DEV)
+    w[:] = dev(short_codes(2, K)).view(torch.uint8)
+    w[:, 5] = dev(short_codes(3, N)).view(torch.uint8)
+    w = w.view(F8)
+    sw = dev(short_scales(4, f8.blocks(N), K, unit(K)))
+    at = slice(N - 300, N)
+    for M in (3, 70):
+        a, sa = dev(short_codes(1, M, K)), by_block(short_scales(5, M, K, unit(K)))
+        nb = f8.blocks(N - 300) - 1
+        first = N - 300 - 128 * nb
+        want = exact_on_gpu(a, sa, w[128 * nb:], sw[nb:])[:, first:]
+        same(q4.gemm_f8(a, sa, w, sw)[:, at], want, f"{M} rows")
+        same(q4.gemm_f8_swiglu(a, sa, (w, sw), (w, sw))[:, at].float().isfinite(), torch.ones(M, 300, device=DEV), "gated")
+    del w
+    M, N, K = 70_000, 32_768, 272                          # 4.6 GB of outputs, twice that of gradients
+    (a, sa), [g, u] = short_problem(M, N, K, mats=2)
+    args = dev(a), by_block(sa), *pair(g)
+    rows = [0, M // 2 + 1, M - 1]
+    y = q4.gemm_f8(*args, dtype=torch.bfloat16)
+    same(y[rows], exact_on_gpu(args[0][rows], args[1][rows], *pair(g)), "y")
+    dh = y.clamp_(-4, 4)
+    d = q4.gemm_f8_swiglu_backward(dh, args[0], args[1], pair(g), pair(u), dtype=torch.bfloat16)
+    gate, up = (exact_on_gpu(args[0][rows], args[1][rows], *pair(m)).cpu().numpy() for m in (g, u))
+    check(d[rows], *f8.gradient(dh[rows].double().cpu().numpy(), gate, 0, up, 0), "bf16", "d")
+    del d, y, dh
+    g = torch.Generator(device=DEV).manual_seed(3)
+    x = torch.randn(70_000, 32_768, device=DEV, dtype=torch.float16, generator=g)
+    c, s, ct, st = q4.quant_f8_block(x, layout="both")
+    cr, sr = q4.quant_f8(x)
+    last = x[-(70_000 % 128):].double().cpu().numpy()      # the last blocks' rows
+    cw, sw = f8.quant(last[:, -256:], 128)
+    n = last.shape[0]
+    assert np.array_equal(f8.decode(bits(c[-n:, -256:])), f8.decode(cw)) and np.array_equal(bits(s[-1:, -2:]), sw)
+    assert np.array_equal(f8.decode(bits(ct[-256:, -n:])), f8.decode(cw.T)) and np.array_equal(bits(st[-2:, -1:]), sw.T)
+    cw, sw = f8.quant(last[:, -256:])
+    assert np.array_equal(f8.decode(bits(cr[-n:, -256:])), f8.decode(cw)) and np.array_equal(bits(sr[-n:, -2:]), sw)
+
+
 # ---------------------------------------------------------------- a layer's step
 
 def step(x, dy, gate, up, down):
