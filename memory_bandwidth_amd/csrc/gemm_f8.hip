@@ -324,7 +324,11 @@ __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_f8_block(Args p) {
     constexpr int SLICE = slice_bytes<BM, BW, TWO>(), STAGE = G * SLICE;
     constexpr bool SX = FM >= FW;                                        // the rows' fragments stream
     constexpr int S = SX ? FM : FW, H = SX ? FW : FM;
-    constexpr int T = S == 8 ? 3 : 1, R = T + 1;                         // of the stream: the last ones, places
+    // Of the stream: the last ones, and places.  Three at the end against one, 4 x 4
+    // fragments of one matrix: 72 against 78 us (4096 x 4096 x 4096, 128 x 256), 74
+    // against 79 (128 x 128, four wavefronts); of two matrices 104 against 100
+    // (600 x 14336 x 4096, 128 x 128).  Eight by four: 420 against 443.
+    constexpr int T = S == 8 || (H == 4 && !TWO) ? 3 : 1, R = T + 1;
     static_assert(S % R == 0, "the next step's first fragment takes a place that is free");
     static_assert(S >= 2 && BM % 64 == 0 && BM / 64 + MATS <= W, "one instruction a wavefront brings all scales");
     extern __shared__ __align__(16) char lds[];
@@ -512,7 +516,9 @@ __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_f8_block(Args p) {
             factor[n % 4] = by[SX ? at : h][TWO && j >= FW / 2 ? 1 : 0];
             add(n - 2);
         };
-        // Reads of the stream's fragments run up to R - 1 ahead, at most two a fragment.
+        // Reads of the stream's fragments run up to R - 1 ahead.
+        constexpr int EACH = T == 1 ? H : S - T > 1 ? H / 2 : 1;
+        static_assert(S - T > 1 || T <= H, "all are read");
         int ahead = 1;
 #pragma unroll
         for (int q = 0; q < S - T; ++q) {
@@ -521,9 +527,7 @@ __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_f8_block(Args p) {
 #pragma unroll
             for (int h = 0; h < H; ++h) {
                 product(q * H + h, passing[0], 0);
-                if (h == 0 || h == H / 2) {
-                    if (ahead < min(q + R, S) && (h == 0 || T > 1)) read_stream(slot, ahead++);
-                }
+                if (h % EACH == 0 && ahead < min(q + R, S)) read_stream(slot, ahead++);
             }
             if constexpr (!F16) spread<H>();
             __builtin_amdgcn_sched_barrier(0);
