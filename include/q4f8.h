@@ -17,10 +17,9 @@
  *     P[m, n] = sum_b a_scales[m, b] * w_scales[b(n), b] * sum_{k in block b} a[m, k] w[n, k]
  *
  * How far P may be off.  S is the sum of |each product| with its scales.
- *  - float32 outputs: products are exact, and the sums of a
- *    block are of fp32's accuracy (within 2^-20 of the sum of their
- *    magnitudes); scales are multiplied and blocks added in fp32.  P is within
- *    (2^-20 + (KB + 3) 2^-24) S.
+ *  - float32 outputs: products are exact, and the sums of a block are of fp32's
+ *    accuracy (within 2^-20 of the sum of their magnitudes); scales are
+ *    multiplied and blocks added in fp32.  P is within (2^-20 + (KB + 3) 2^-24) S.
  *  - float16 and bfloat16 outputs: the products of eight consecutive k are
  *    brought to the exponent of the largest of them, and what is below 2^-13
  *    of that power of two is dropped; the sums are fp32.  That adds at most
@@ -28,9 +27,10 @@
  *    the result for values of a normal distribution), where the output's own
  *    rounding is 2^-11 or 2^-8.
  * The order of the sums goes with the sizes, so the last digits of a row may
- * depend on how many others there are.  Scales of Inf or NaN and codes of NaN make what they enter Inf or NaN as fp32
- * arithmetic does.  Products of two scales should be in the normal range of
- * fp32: below it their last bits are lost, above it they are Inf.
+ * depend on how many others there are.  Scales of Inf or NaN and codes of NaN
+ * make what they enter Inf or NaN as fp32 arithmetic does.  Products of two
+ * scales should be in the normal range of fp32: below it their last bits are
+ * lost, above it they are Inf.
  *
  * Conventions are those of q4gemv.h and q4i8.h: device pointers owned by the
  * caller, asynchronous on `stream`, may be captured into a HIP graph, no
@@ -68,7 +68,9 @@ extern "C" {
  * that of the real quotient.  A block holding an Inf or a NaN gets zero codes
  * and the scale NaN.
  *   x [M, K] of x_type, 16-byte aligned; codes 16-byte aligned; scales with
- *   the strides above, 1 <= strides where there are several; M < 2^22. */
+ *   the strides above, each at a place of its own: 1 <= strides where there are
+ *   several, and then stride_k > (M - 1) stride_m or stride_m > (KB - 1) stride_k;
+ *   M < 2^22. */
 int quant_f8(const void *x, int x_type, uint8_t *codes, float *scales, int64_t stride_m, int64_t stride_k,
              int M, int K, void *stream);
 

@@ -685,7 +685,8 @@ def quant_f8(x: torch.Tensor, out: tuple | None = None) -> tuple[torch.Tensor, t
     2^22.  A block with an Inf or a NaN gets the scale NaN and zero codes.
 
     New scales lie block by block (their .t() is contiguous), as the products read
-    them best; scales given with out may have any strides."""
+    them best; scales given with out may have any strides that give each of them
+    a place of its own."""
     codes, scales = (None, None) if out is None else out
     got = (_bind or _load_bind()).quant_f8(x, codes, scales)
     if type(got) is tuple:

@@ -129,7 +129,7 @@ __device__ __forceinline__ u32x2_t codes8(const Eight<T> &x, const Scale &c) {
 // TB/s in and out; with two blocks a team 49.2, with four 52.5: more of them are
 // on their way to memory with more, smaller wavefronts.
 constexpr int kTeams = 16;
-constexpr int64_t kMaxGroups = 0xFFFFFFFFll / 512;      // of one launch
+constexpr int64_t kMaxThreads = 0xFFFFFFFFll;      // of one launch
 
 template <typename T>
 __global__ __launch_bounds__(256) void quant_rows(const char *__restrict__ x, uint8_t *__restrict__ codes,
@@ -155,7 +155,7 @@ int launch_rows(const char *x, uint8_t *codes, float *scales, int64_t sm, int64_
     while (rows_log2 < 4 && (1 << rows_log2) < M) ++rows_log2;
     const int blocks = kTeams >> rows_log2, strips = ((K + 127) / 128 + blocks - 1) / blocks;
     const int64_t grid = (int64_t)((M + (1 << rows_log2) - 1) >> rows_log2) * strips;
-    if (grid > kMaxGroups) return Q4_EINVAL;
+    if (grid * 256 > kMaxThreads) return Q4_EINVAL;
     quant_rows<T><<<(unsigned)grid, 256, 0, s>>>(x, codes, scales, sm, sk, M, K, rows_log2, strips);
     return q4::launch_status();
 }
@@ -245,7 +245,13 @@ bool type_ok(int t) { return t == I8_F32 || t == I8_F16 || t == I8_BF16; }
 extern "C" int quant_f8(const void *x, int x_type, uint8_t *codes, float *scales, int64_t stride_m, int64_t stride_k,
                         int M, int K, void *stream) {
     if (M < 0 || M >= (1 << 22) || K < 16 || K % 16 || K > 131056 || !type_ok(x_type)) return Q4_EINVAL;
-    if (stride_m < (M > 1) || stride_m > (1 << 20) || stride_k < (K > 128) || stride_k > (1ll << 31)) return Q4_EINVAL;
+    if (stride_m < 0 || stride_m > (1 << 20) || stride_k < 0 || stride_k > (1ll << 31)) return Q4_EINVAL;
+    // Each scale has a place of its own: runs along one dimension end before the next begins.
+    const int64_t end_m = M > 0 ? (M - 1) * stride_m : 0, end_k = ((K + 127) / 128 - 1) * stride_k;
+    const bool several_m = M > 1, several_k = K > 128;
+    if ((several_m && stride_m < 1) || (several_k && stride_k < 1) ||
+        (several_m && several_k && stride_k <= end_m && stride_m <= end_k))
+        return Q4_EINVAL;
     if (M == 0) return Q4_OK;
     if (!x || !codes || !scales) return Q4_ENULL;
     if (!q4::aligned(x, 16) || !q4::aligned(codes, 16) || !q4::aligned(scales, 4)) return Q4_EALIGN;
@@ -269,7 +275,7 @@ extern "C" int quant_f8_block(const void *x, int x_type, uint8_t *codes, float *
     const auto *xb = static_cast<const char *>(x);
     const hipStream_t s = static_cast<hipStream_t>(stream);
     const int RB = (R + 127) / 128, CB = (C + 127) / 128, grid = RB * CB;
-    if (grid > kMaxGroups) return Q4_EINVAL;
+    if ((int64_t)grid * 512 > kMaxThreads) return Q4_EINVAL;
     if (x_type == I8_F32) quant_blocks<F32><<<grid, 512, 0, s>>>(xb, codes, scales, codes_t, scales_t, R, C, RB, CB);
     else if (x_type == I8_F16) quant_blocks<F16><<<grid, 512, 0, s>>>(xb, codes, scales, codes_t, scales_t, R, C, RB, CB);
     else quant_blocks<BF16><<<grid, 512, 0, s>>>(xb, codes, scales, codes_t, scales_t, R, C, RB, CB);

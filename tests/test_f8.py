@@ -94,6 +94,15 @@ def test_quant_strides(L):
     assert call(L, "quant_f8", 0, 8, 256) == q4.Q4_OK
 
 
+@pytest.mark.parametrize("M,K,sm,sk,fine", [
+    (4, 256, 1, 4, True), (4, 256, 1, 3, False), (4, 256, 1, 1, False), (4, 256, 2, 1, True), (4, 256, 2, 2, False),
+    (4, 384, 3, 1, True), (4, 384, 2, 1, False), (1, 256, 0, 1, True), (1, 256, 0, 0, False), (4, 128, 1, 0, True),
+    (4, 128, 0, 1, False), (1, 128, 0, 0, True), (0, 256, 0, 1, True)])
+def test_quant_scales_have_places_of_their_own(L, M, K, sm, sk, fine):
+    want = q4.Q4_EINVAL if not fine else q4.Q4_OK if M == 0 else q4.Q4_ENULL
+    assert call(L, "quant_f8", M, 8, K, sm=sm, sk=sk, at=[(0, None)]) == want
+
+
 @pytest.mark.parametrize("fn", CALLS)
 def test_pointers(L, fn):
     for i in range(POINTERS[fn]):
