@@ -53,7 +53,7 @@ struct Args {
     int tiles_m, tiles_n;      // kHalves, kQuarters: of the tiles that are divided
     Part part;
     int whole;                 // kWhole: tiles that are taken; else: tiles before those that are divided
-    bool once;                 // the weights' stream is more than a cache would keep
+    bool once;                 // the weights are read past the caches
     bool share;                // several row tiles read the same weights
 };
 
@@ -809,7 +809,10 @@ int planned(const Target &to, int rows, int cols, int64_t grid, int block) {
 
 // Wavefronts on one strip's K (log2) and in a workgroup of a few-rows kernel
 // of bm rows: as many share K as it takes for 1536 wavefronts, 6 for each CU,
-// while each has a block.
+// while each has a block.  16 x 4096 x 14336 takes 13.9 us so and 21.3 with 1024,
+// 32 x 14336 x 4096 15.5 and, with 2048, 18.7.  Workgroups of four wavefronts
+// rather than eight where those would leave CUs idle or fill them unevenly:
+// 1 x 896 x 896 2.57 against 2.82 us, 8 x 28672 x 8192 45.5 against 47.1.
 struct Split { int64_t tiles, strips; int log2, waves; };
 Split split_of(const Args &p, int bm, int cols, int most) {
     Split s = {tiles_of(p.M, bm), tiles_of(p.N, cols), 0, most};
@@ -823,8 +826,15 @@ Split split_of(const Args &p, int bm, int cols, int most) {
 template <int NX, int FN, Mode MODE, bool F16, int W>
 int launch_few(Args p, const Split &s, const Target &to) {
     constexpr int FM = (NX + 1) / 2, FW = MODE == kPlain ? FN : 2 * FN, kLds = W * kFewDepth * ((2 * FW + 2 * FM) * 1024 + 256);
+    // 128 x 8192 x 8192, tiles of 64 x 32: 32.6 us with, 36.9 without.
     p.share = s.tiles > 1;
-    p.once = p.K % 64 == 0 && !p.share && (int64_t)(MODE == kPlain ? 1 : 2) * p.N * p.K > (int64_t)64 << 20;
+    // Weights that one row tile reads pass the caches by: the next layers'
+    // would put them out.  With 20 sets of operands in turn a row of 14336 x
+    // 4096 takes 12.1 us so and 13.7 through the caches, 4096 x 4096 5.7 and 6.4; with
+    // three sets, which the last cache holds, 11.2 and 10.5, 4.8 and 5.3.  Rows that
+    // begin within a line share it with the one before, which a cache has to
+    // keep: 14336 x 4112 takes 15.0 and 14.4.
+    p.once = p.K % 64 == 0 && !p.share;
     p.tiles_m = (int)s.tiles;
     p.tiles_n = (int)tiles_of(s.strips, W >> s.log2);
     const int64_t grid = s.tiles * p.tiles_n;
@@ -855,9 +865,10 @@ int launch_block(Args p, const Target &to) {
     if (p.part == kWhole) grid = p.whole;
     if (p.part >= kHalves) grid = (grid - p.whole) << (p.part - kHalves + 1);
     // Workgroups that stay and go through the tiles, each loading its next one
-    // while it finishes the last.
+    // while it finishes the last: 8192 x 14336 x 4096 in 256 x 256 takes 422 us so
+    // and 431 with a workgroup a tile, 4096 x 8192 x 512 gated 51.8 and 56.7.
     const int64_t steps = tiles_of(p.K, BK);
-    if (G == 1 && p.part < kHalves && steps >= D && steps <= 64)
+    if (G == 1 && p.part < kHalves && steps >= D)
         grid = std::min<int64_t>(grid, kCUs * (160 * 1024 / kLds));
     else if (grid * kThreads > kMaxThreads) return Q4_EINVAL;
     if (to.report) return planned(to, BM, kBN, grid, kThreads);
@@ -969,11 +980,14 @@ void split_rounds(Args &p, int64_t all, int slots) {
 template <Mode MODE, bool F16>
 int launch(const Args &p, Kernel k, const Target &to) {
     constexpr bool TWO = MODE != kPlain;
-    // Where there is only one workgroup for each CU, its ring has more stages.
+    // Where there is only one workgroup for each CU, its ring has more stages:
+    // 512 x 4096 x 14336 gated takes 84 us with four, 117 with two.
     auto alone = [&](int bm, int bw) { return tiles_of(p.M, bm) * tiles_of(p.N, TWO ? bw / 2 : bw) <= kCUs; };
     // Two matrices halve the columns of a lane's run: four rows of wavefronts
-    // then store whole lines.
-    constexpr int kM = TWO ? 4 : 2, kN = TWO ? 2 : 4;
+    // then store whole lines of 16 bits (1999 x 14336 x 4096 gated, 128 x 256: 253 us
+    // against 258).  To float32 they do in either order, and two rows convert fewer
+    // operands (4096 x 8192 x 512 gated: 84 us against 92).
+    constexpr int kM = TWO && !F16 ? 4 : 2, kN = TWO && !F16 ? 2 : 4;
     switch (k) {
     case kFew8: return launch_few<1, 1, MODE, F16>(p, to);
     case kFew16: return launch_few<2, 1, MODE, F16>(p, to);
