@@ -406,7 +406,8 @@ __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_f8_block(Args p) {
     auto source = [&](int slot, int t, bool wanted) {
         const int kb = min(t * G + group, KB - 1);
         return Source{rsrc_of(a_base, wanted ? a_bytes : 0u), rsrc_of(w_base, wanted ? w_bytes : 0u),
-                      rsrc_of(scale_base + kb * scale_step, wanted ? 0xFFFFFFFFu : 0u), lds + slot * STAGE + group * SLICE,
+                      rsrc_of(scale_base + kb * scale_step, wanted ? 0xFFFFFFFFu : 0u),
+                      lds + slot * STAGE + group * SLICE,
                       min((t * G + group) * BK, p.K - BK)};
     };
     auto load = [&](const Source &from, int k) {
@@ -825,7 +826,8 @@ Split split_of(const Args &p, int bm, int cols, int most) {
 
 template <int NX, int FN, Mode MODE, bool F16, int W>
 int launch_few(Args p, const Split &s, const Target &to) {
-    constexpr int FM = (NX + 1) / 2, FW = MODE == kPlain ? FN : 2 * FN, kLds = W * kFewDepth * ((2 * FW + 2 * FM) * 1024 + 256);
+    constexpr int FM = (NX + 1) / 2, FW = MODE == kPlain ? FN : 2 * FN;
+    constexpr int kLds = W * kFewDepth * ((2 * FW + 2 * FM) * 1024 + 256);
     // 128 x 8192 x 8192, tiles of 64 x 32: 32.6 us with, 36.9 without.
     p.share = s.tiles > 1;
     // Weights that one row tile reads pass the caches by: the next layers'
@@ -895,30 +897,30 @@ struct Costs {
     double stretch;            // of 64 x 128 tiles, by tiles a CU
     Linear tile64, tile128, tile128_many, wide, tile256;
 };
-// Fitted to 1000 calls (9 to 8192 rows, N 64 to 14336, K 128 to 14336, one matrix and
-// two; up to six sets of operands in turn, in a graph), in which the choice is on
-// average 0.6% behind the best kernel for 16-bit outputs and 1.2% for float32,
-// 5% and 7% or more in one of twenty.  Where they decide: 64 x 4096 x 14336
-// takes 21.2 us in tiles of 32 x 32, 26.6 in 32 x 16, 28.8 in 64 x 32 and 39.5 in
-// 64 x 64; at 128 rows these are 32.3, 42.1, 27.3 and 38.1.  1024 x 4096 x 4096
-// takes 25.6 us in 128 x 128, 29.1 in 64 x 128 and 34.3 in 128 x 256, 8192 x
-// 14336 x 4096 413 in 256 x 256, 508 in 128 x 256 and 536 in 128 x 128.
+// Fitted to 1370 calls (9 to 8192 rows, N 64 to 14336, K 128 to 14336, one matrix and
+// two; up to six sets of operands in turn, in a graph).  Of 370 of them, timed again,
+// the choice was on average 1.8% behind the best time of any kernel for 16-bit
+// outputs and 2.9% for float32, 11% and 13% or more in one of twenty.  Where they
+// decide: 64 x 4096 x 14336 takes 21.1 us in tiles of 32 x 32, 26.5 in 32 x 16, 28.5
+// in 64 x 32 and 39.3 in 64 x 64; at 128 rows these are 32.2, 42.1, 27.3 and 38.1.
+// 1024 x 4096 x 4096 takes 26.7 us in 128 x 128, 29.0 in 64 x 128 and 31.8 in 128 x
+// 256, 8192 x 14336 x 4096 417 in 256 x 256, 488 in 128 x 256 and 553 in 128 x 128.
 constexpr Costs kCosts16 = {{-0.344, 0.353, 0.045, 0.057, 0.963},
-                            {-0.680, 0.451, 0.058, 0.084, 0.407},
-                            {-0.502, 0.668, 0.078, 0.133, 0.682},
-                            {-0.231, 0.192, 0.128, 0.128, 1.067},
-                            {0.357, 0.616, 0.181, 0.635, 1.769},
-                            0.184, 0.519, 0.55,
-                            {1.457, 0.380},
-                            1.076, {2.484, 0.498}, {2.699, 0.540}, {0.435, 0.537}, {7.803, 0.552}, {2.800, 1.215}};
+                            {-0.617, 0.596, 0.066, 0.086, 1.336},
+                            {-0.221, 0.908, 0.105, 0.153, 1.345},
+                            {0.806, 0.721, 0.117, 0., 2.430},
+                            {-0.055, 0.895, 0.219, 0., 3.842},
+                            0.129, 0.837, -1.496,
+                            {4.659, 0.327},
+                            1.105, {2.935, 0.521}, {3.929, 0.608}, {0.979, 0.855}, {7.065, 0.968}, {9.123, 1.712}};
 constexpr Costs kCosts32 = {{-0.615, 0.142, 0.036, 0.046, 0.912},
-                            {-0.567, 0.240, 0.046, 0.051, 0.395},
-                            {-0.536, 0.306, 0.073, 0.100, 0.373},
-                            {-0.262, 0.316, 0.115, 0.115, 0.348},
-                            {0.757, 0.668, 0.197, 1.015, 2.179},
-                            0.134, 0.651, 1.153,
-                            {0.635, 0.406},
-                            0.999, {0.810, 0.558}, {0.878, 0.558}, {2.080, 0.780}, {4.298, 1.488}, {0., 0.}};
+                            {1.107, 0.547, 0.057, 0.086, 1.943},
+                            {0.361, 0.782, 0.087, 0.131, 2.548},
+                            {0.904, 0.849, 0.131, 0., 1.810},
+                            {-0.338, 1.006, 0.236, 0., 3.920},
+                            0.192, 0.565, -2.228,
+                            {4.348, 0.437},
+                            1.315, {4.539, 0.663}, {4.837, 0.996}, {5.928, 1.025}, {12.344, 1.549}, {0., 0.}};
 
 // The kernel for a call's sizes: up to 8 rows the weights' stream decides; above,
 // the least estimated time.
@@ -937,7 +939,8 @@ Kernel choose(const Args &p, int mats) {
     auto few = [&](int bm, int cols, int most, const FewCost &f) {
         const Split s = split_of(p, bm, cols, most);
         const int64_t tm = tiles_of(p.M, bm), wgs = tm * tiles_of(s.strips, s.waves >> s.log2);
-        const double block = std::max(f.block, (two ? f.shared_two : f.shared) * (double)(tiles_of(wgs, kCUs) * s.waves));
+        const double waves = (double)(tiles_of(wgs, kCUs) * s.waves);                   // of a CU
+        const double block = std::max(f.block, (two ? f.shared_two : f.shared) * waves);
         const double mb = (double)mats * p.N * p.K * 1e-6;
         return std::max(f.start + block * (f.first + (double)tiles_of(steps, 1 << s.log2)),
                         c.mb * mb * (1. + c.again * (double)(tm - 1)) - c.off);
@@ -951,11 +954,7 @@ Kernel choose(const Args &p, int mats) {
     cost[kFew64] = two ? kNever : few(64, 32, 4, c.few64);
     cost[kTileDeep] = tiles(64, 64) <= kCUs ? c.deep.at(steps) : kNever;
     cost[kTile64] = std::max(1.0, (double)tiles(64, 128) / kCUs * c.stretch) * c.tile64.at(steps);
-    const int64_t t128 = tiles(128, 128), left128 = t128 % (2 * kCUs);
-    cost[kTile128] = t128 >= 2 * kCUs && left128 && left128 <= kRestMost
-                         ? (double)(t128 - left128) / kCUs * c.tile128_many.at(steps) +
-                               rounds(4 * left128) * c.deep.at(steps)
-                         : each(t128, c.tile128, c.tile128_many);
+    cost[kTile128] = each(tiles(128, 128), c.tile128, c.tile128_many);
     cost[kTileWide] = rounds(tiles(128, 256)) * c.wide.at(steps);
     const int64_t t256 = tiles(256, 256), left = t256 % kCUs;
     const double divided = left > kQuartersMost ? c.wide.at(steps) : left ? c.tile128.at(steps) : 0.;
@@ -966,15 +965,6 @@ Kernel choose(const Args &p, int mats) {
     for (Kernel k : {kFew16, kFew32, kFew32x32, kFew64, kTileDeep, kTile64, kTile128, kTileWide, kTile256})
         if (cost[k] < cost[best]) best = k;
     return best;
-}
-
-// Tiles come in rounds of `slots`, as many as the chip holds at a time.  Where
-// the last round would have few, it goes to a launch of smaller tiles.
-void split_rounds(Args &p, int64_t all, int slots) {
-    const int64_t left = all % slots;
-    if (all < slots || !left || left > kRestMost) return;
-    p.part = kWhole;
-    p.whole = (int)(all - left);
 }
 
 template <Mode MODE, bool F16>
@@ -998,24 +988,26 @@ int launch(const Args &p, Kernel k, const Target &to) {
         else return k == kFew64 ? launch_few<8, 2, MODE, F16, 4>(p, to) : launch_few<4, 2, MODE, F16>(p, to);
     case kTile64: return launch_block<64, 128, 2, 4, 1, 3, MODE, F16>(p, to);
     case kTileDeep: return launch_block<64, 64, 2, 2, 2, 4, MODE, F16>(p, to);
-    case kTile128: {
+    case kTile128:
         if (alone(128, 128)) return launch_block<128, 128, kM, kN, 1, 4, MODE, F16>(p, to);
         // Four wavefronts, of 64 x 64: two workgroups a CU, neither of which
-        // waits at the other's barriers.
-        Args q = p;
-        split_rounds(q, tiles_of(p.M, 128) * tiles_of(p.N, TWO ? 64 : 128), 2 * kCUs);
-        if (int st = launch_block<128, 128, 2, 2, 1, 2, MODE, F16>(q, to)) return st;
-        if (q.part == kAll) return Q4_OK;
-        q.part = kQuarters;
-        return launch_block<64, 64, 2, 2, 2, 4, MODE, F16>(q, to);
-    }
+        // waits at the other's barriers, and a last round that is not full has
+        // the CUs to itself.
+        return launch_block<128, 128, 2, 2, 1, 2, MODE, F16>(p, to);
     case kTileWide: return launch_block<128, 256, kM, kN, 1, 3, MODE, F16>(p, to);
     default:
         if constexpr (F16) return Q4_EINVAL;         // not chosen
         else {
             Args q = p;
+            // One tile a CU, in rounds.  Where the last would have few, it goes to a
+            // launch of smaller tiles: 4600 x 4096 x 14336 (32 tiles left) takes 281 us so
+            // and 369 without, 5376 rows (80 left) 321 and 360, 1999 x 14336 x 4096
+            // gated (128 left) 227 and 238.
             const int64_t all = tiles_of(p.M, 256) * tiles_of(p.N, TWO ? 128 : 256), left = all % kCUs;
-            split_rounds(q, all, kCUs);
+            if (all > kCUs && left && left <= kRestMost) {
+                q.part = kWhole;
+                q.whole = (int)(all - left);
+            }
             if (int st = launch_block<256, 256, kM, kN, 1, 2, MODE, false>(q, to)) return st;
             if (q.part == kAll) return Q4_OK;
             if (left > kQuartersMost) {

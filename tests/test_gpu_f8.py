@@ -233,7 +233,9 @@ LARGE = [(64, 4100, 2064), (500, 2050, 2064), (3984, 3781, 656), (64, 3999, 4112
          (36, 8174, 1472), (38, 6292, 9520), (141, 5177, 800), (3065, 116, 1440), (4868, 387, 656), (5390, 659, 288),
          (7439, 1399, 272), (3692, 4667, 144), (4715, 1794, 304), (8655, 930, 272), (4771, 5846, 272),
          (5331, 4596, 656), (3083, 5219, 272), (4378, 345, 288), (7290, 193, 272), (6343, 103, 688),
-         (1804, 4310, 1680), (2910, 2761, 400), (2755, 5834, 400)]
+         (1804, 4310, 1680), (2910, 2761, 400), (2755, 5834, 400), (789, 5441, 272), (198, 3608, 6208),
+         (3630, 4229, 800), (5997, 33, 6976), (7171, 4233, 464), (1915, 8541, 912), (10, 1693, 976),
+         (33, 7794, 4496)]
 
 
 @pytest.mark.parametrize("M,N,K", GEMM + LARGE)
@@ -286,19 +288,17 @@ def launches(mats, M, N, K, t):
     tiles = -(-M // r) * -(-N // g["tile_cols"])
     if r <= 32 or (r, wide) == (64, 32):
         return r, g["block"]
-    slots = 512 if r <= 128 and wide <= 128 else 256
-    left = tiles % slots
+    left = tiles % 256
     name = "one each"
-    if wide <= 256 and r in (128, 256) and wide != 2 * r:
-        whole = tiles >= slots and 0 < left <= 128 and tiles > 256
-        name = ("halves" if r == 256 and left > 64 else "quarters") if whole else name
+    if r == wide == 256 and tiles > 256 and 0 < left <= 128:
+        name = "halves" if left > 64 else "quarters"
     return r, wide, "several" if name == "one each" and g["grid"] < tiles else name
 
 
 def test_sizes_take_every_launch():
     common = {(8, 256), (8, 512), (16, 256), (16, 512), (32, 256), (32, 512), (64, 64, "one each"), (64, 128, "one each"),
-              (128, 128, "one each"), (128, 128, "several"), (128, 128, "quarters"), (128, 256, "one each")}
-    f32 = common | {(64, 128, "several"), (128, 256, "several")}
+              (128, 128, "one each"), (128, 128, "several"), (128, 256, "one each")}
+    f32 = common | {(128, 256, "several")}
     f16 = common | {(256, 256, "one each"), (256, 256, "several"), (256, 256, "halves"), (256, 256, "quarters")}
     for mats, shapes, more in ((1, GEMM + LARGE, {(64, 256)}), (2, GATED, set())):
         for t, want in ((torch.float32, f32), (torch.bfloat16, f16)):
@@ -328,7 +328,9 @@ GATED = [(1, 1, 16), (1, 896, 896), (4, 300, 4096), (16, 65, 144), (30, 1000, 10
          (40, 1373, 48), (100, 1789, 6160), (4300, 2050, 2064), (9, 10, 16), (9, 9, 1056), (17, 9, 16), (4189, 9, 16),
          (19, 2724, 1040), (33, 6864, 1104), (35, 8135, 5824), (8550, 92, 784), (5390, 330, 288), (7439, 700, 272),
          (7056, 1172, 144), (4715, 897, 304), (8655, 465, 272), (4771, 2923, 272), (5331, 2298, 656), (3083, 2610, 272),
-         (5470, 151, 320), (1804, 2155, 1680), (2910, 1381, 400), (2755, 2917, 400)]
+         (5470, 151, 320), (1804, 2155, 1680), (2910, 1381, 400), (2755, 2917, 400),
+         (1033, 2083, 288), (44, 7211, 7504), (1968, 4020, 784), (3992, 4079, 480), (806, 8365, 1440),
+         (9, 4168, 400), (4186, 174, 192)]
 
 
 def gated_problem(M, N, K, size=4.0):
