@@ -653,13 +653,21 @@ __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_f8_block(Args p) {
 // the rows' scales behind them, the next block issued as soon as a slot has
 // been read: no barrier, and D - 1 blocks in flight while one is multiplied.
 // Blocks past K repeat the row's last 16 bytes against activations of zero.
-constexpr int kFewDepth = 2;
+//
+// Eight rows take as many slots as fit, up to four: 1 x 28672 x 8192 in 41.2 us (43.7
+// with two), 4 x 14336 x 4096 gated 21.5 (22.7).  With more rows the operands come from
+// the L2, and workgroups side by side on a CU count for more: 333 x 896 x 4864 in
+// 32 x 16 10.7 with two, 17.3 with four.
+constexpr int few_slot(int FM, int FW) { return (2 * FW + 2 * FM) * 1024 + 256; }  // whole fragments, and the scales
+constexpr int few_depth(int W, int NX, int FW) {
+    return NX == 1 ? std::min(4, 160 * 1024 / (W * few_slot(1, FW))) : 2;
+}
 
 template <int NX, int FN, Mode MODE, bool F16, int W>
 __global__ __launch_bounds__(W * 64) void gemm_f8_few(Args p, int ks_log2) {
     constexpr int FM = (NX + 1) / 2, BM = 8 * NX, MATS = MODE == kPlain ? 1 : 2, FW = FN * MATS;
-    constexpr int D = kFewDepth, LOADS = 2 * FW + NX + 1;               // load instructions of a block
-    constexpr int SLOT = (2 * FW + 2 * FM) * 1024 + 256;                // whole fragments, the last may be half loaded
+    constexpr int D = few_depth(W, NX, FW), LOADS = 2 * FW + NX + 1;    // load instructions of a block
+    constexpr int SLOT = few_slot(FM, FW);                              // the last fragment may be half loaded
     extern __shared__ __align__(16) char lds[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int KS = 1 << ks_log2, ks = wave & (KS - 1);
@@ -760,8 +768,7 @@ __global__ __launch_bounds__(W * 64) void gemm_f8_few(Args p, int ks_log2) {
             if (d < left) load(d, ks + d * KS);
         for (; left > 0; --left, u += KS) {
             load_sw(sw_next, u + KS);
-            if (left >= D) wait_loads<(D - 1) * LOADS>();
-            else wait_loads<0>();
+            wait_batches<LOADS, D - 1>(min(left, D) - 1);
             products(slot, u, sw);
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");      // the slot has been read
             if (left > D) load(slot, u + D * KS);
@@ -827,7 +834,8 @@ Split split_of(const Args &p, int bm, int cols, int most) {
 template <int NX, int FN, Mode MODE, bool F16, int W>
 int launch_few(Args p, const Split &s, const Target &to) {
     constexpr int FM = (NX + 1) / 2, FW = MODE == kPlain ? FN : 2 * FN;
-    constexpr int kLds = W * kFewDepth * ((2 * FW + 2 * FM) * 1024 + 256);
+    constexpr int kLds = W * few_depth(W, NX, FW) * few_slot(FM, FW);
+    static_assert(kLds <= 160 * 1024 && few_depth(W, NX, FW) >= 2, "the rings fit, with a block on its way");
     // 128 x 8192 x 8192, tiles of 64 x 32: 32.6 us with, 36.9 without.
     p.share = s.tiles > 1;
     // Weights that one row tile reads pass the caches by: the next layers'
