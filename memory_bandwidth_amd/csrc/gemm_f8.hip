@@ -603,6 +603,9 @@ __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_f8_block(Args p) {
             more = G == 1 && steps >= D && place(id + (int)gridDim.x, nxt);
             if (more) {
                 aim(nxt);
+                // The place is that of the tile before this one: a barrier since then says that
+                // every wavefront has read it.  With D steps there has been none.
+                if (!TWO && p.bias && steps == D) barrier();
                 load_bias(nxt, biases + (side ^ 1) * BN);
             }
         }

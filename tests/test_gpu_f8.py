@@ -321,6 +321,30 @@ def test_gemm_out_in_a_larger_buffer(t, M, N, skew):
     assert (buf[:8 + skew] == 7).all() and (buf[8 + skew + M * N:] == 7).all()
 
 
+def bias_of(N, seed=5):
+    """Whole sixteenths, other ones in every column tile."""
+    return (np.random.default_rng(seed).integers(-64, 65, N) / 16).astype(np.float32)
+
+
+# Stages that a workgroup keeps on their way, by tile, where it goes through several tiles.
+STAGES = {(128, 128): 2, (128, 256): 3}
+
+
+@pytest.mark.parametrize("t,M,N,K", [("bf16", 8192, 4096, 256), ("f16", 8192, 4096, 256), ("bf16", 32, 132383, 208),
+                                     ("f32", 8192, 8192, 272), ("f32", 4096, 8192, 384), ("f32", 99, 134948, 192)])
+def test_gemm_bias_of_tiles_in_turn(t, M, N, K):
+    """Three tiles or more a workgroup, and as many blocks of K as stages: the loads of a tile's first step are then
+    followed by the next one's bias, in the place of the one before."""
+    g = q4.gemm_f8_geometry(1, M, N, K, dtype=TYPES[t])
+    tile = g["tile_rows"], g["tile_cols"]
+    assert -(-M // tile[0]) * -(-N // tile[1]) > 2 * g["grid"] and f8.blocks(K) == STAGES[tile]
+    (a, sa), [w] = short_problem(M, N, K)
+    args, b = (dev(a), by_block(sa), *pair(w)), dev(bias_of(N))
+    want = (exact_on_gpu(*args) + b.double()).to(TYPES[t])
+    for i in range(5):
+        same(q4.gemm_f8(*args, bias=b, dtype=TYPES[t]), want, f"{M} {N} {K}, call {i}")
+
+
 # ---------------------------------------------------------------- gates, on exact products
 
 GATED = [(1, 1, 16), (1, 896, 896), (4, 300, 4096), (16, 65, 144), (30, 1000, 1040), (64, 32, 128), (100, 130, 2816),
