@@ -345,6 +345,34 @@ def test_gemm_bias_of_tiles_in_turn(t, M, N, K):
         same(q4.gemm_f8(*args, bias=b, dtype=TYPES[t]), want, f"{M} {N} {K}, call {i}")
 
 
+# A bias in every kind of launch, whose tiles each bring it in a way of their own: few rows from memory (8, 16, 32
+# and 64 rows, four and eight wavefronts), tiles through LDS (64 x 64, 64 x 128, 128 x 128, 128 x 256 and 256 x 256,
+# one and several a workgroup, in halves and in quarters).  Columns end inside a tile in all of them.
+BIASED = [(1, 300, 4096), (3, 129, 144), (10, 1693, 976), (65, 127, 256), (16, 45, 64), (40, 70, 32), (100, 890, 4864),
+          (141, 5177, 800), (33, 7794, 4496), (198, 3608, 6208), (333, 4864, 896), (500, 2050, 2064), (4868, 387, 656),
+          (5390, 659, 288), (8655, 930, 272), (2910, 2761, 400), (1804, 4310, 1680), (2755, 5834, 400),
+          (1915, 8541, 912), (7171, 4233, 464), (5331, 4596, 656), (4300, 4100, 2064)]
+
+
+def test_biased_sizes_take_every_launch():
+    both = {(8, 256), (8, 512), (16, 256), (16, 512), (32, 256), (32, 512), (64, 256), (64, 64, "one each"),
+            (64, 128, "one each"), (128, 128, "one each"), (128, 128, "several"), (128, 256, "one each"),
+            (128, 256, "several")}
+    largest = {(256, 256, k) for k in ("one each", "several", "halves", "quarters")}
+    for t, want in (("f32", both), ("f16", both | largest), ("bf16", both | largest)):
+        seen = {launches(1, *s, TYPES[t]) for s in BIASED}
+        assert want <= seen, (t, want - seen)
+
+
+@pytest.mark.parametrize("M,N,K", BIASED)
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("tall", [1, 128])
+def test_gemm_bias(M, N, K, t, tall):
+    (a, sa), [w] = short_problem(M, N, K, tall=tall)
+    args, b = (dev(a), by_block(sa) if tall == 1 else dev(sa), *pair(w)), dev(bias_of(N))
+    same(q4.gemm_f8(*args, bias=b, dtype=TYPES[t]), exact_on_gpu(*args) + b.double(), f"{M} {N} {K}")
+
+
 # ---------------------------------------------------------------- gates, on exact products
 
 GATED = [(1, 1, 16), (1, 896, 896), (4, 300, 4096), (16, 65, 144), (30, 1000, 1040), (64, 32, 128), (100, 130, 2816),
