@@ -23,9 +23,10 @@
  *  - float16 and bfloat16 outputs: the products of eight consecutive k are
  *    brought to the exponent of the largest of them, and what is below 2^-13
  *    of that power of two is dropped; the sums are fp32.  That adds at most
- *    7 * 2^-13 times the largest product of each eight (in practice 2^-16 of
- *    the result for values of a normal distribution), where the output's own
- *    rounding is 2^-11 or 2^-8.
+ *    7 * 2^-13 times the largest product of each eight: some 2^-16 of the
+ *    result for values of a normal distribution; where one product is far
+ *    above its neighbours, more than the 2^-11 of float16's own rounding (that
+ *    of bfloat16 is 2^-8); where products cancel, any part of the result.
  * The order of the sums goes with the sizes, so the last digits of a row may
  * depend on how many others there are.  Scales of Inf or NaN and codes of NaN
  * make what they enter Inf or NaN as fp32 arithmetic does.  Products of two

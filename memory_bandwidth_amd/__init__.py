@@ -736,10 +736,15 @@ def gemm_f8(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scales: 
     a and w float8_e4m3fn; a_scales float32 [M, ceil(K / 128)], of any strides, or
     one for each block of 128 rows too, [ceil(M / 128), ceil(K / 128)]; w_scales
     float32 [ceil(N / 128), ceil(K / 128)]; bias float32.  y is of `dtype`
-    (float32, float16 or bfloat16).  K is a multiple of 16.  For float32 the
-    products are exact and their sums of fp32's accuracy; for 16 bits the matrix
-    cores' 8-bit products are used, which are twice as fast and whose rounding
-    (include/q4f8.h) is below that of the output."""
+    (float32, float16 or bfloat16), and dtype chooses how exact the sums are.  K is
+    a multiple of 16.
+
+    float32: products are exact and their sums of fp32's accuracy.  float16 and
+    bfloat16: the matrix cores' 8-bit products, twice as fast, which lose of every
+    eight consecutive k up to 7 * 2^-13 of the largest product: some 2^-16 of the
+    result for normally distributed values, more than float16's own rounding
+    where one product is far above its neighbours, and any part of a result whose
+    products cancel.  Ask for float32 there."""
     y = (_bind or _load_bind()).gemm_f8(a, a_scales, w, w_scales, bias, dtype, out)
     if y is None:
         _f8_refuse_product(a, a_scales, w, w_scales, bias, dtype, out)
@@ -750,7 +755,8 @@ def gemm_f8(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scales: 
 
 def gemm_f8_swiglu(a: torch.Tensor, a_scales: torch.Tensor, gate: tuple, up: tuple,
                    dtype=torch.float32, out: torch.Tensor | None = None) -> torch.Tensor:
-    """y = silu(g) * u with g, u the gemm_f8 of a with gate and up, each (w, w_scales); neither is stored."""
+    """y = silu(g) * u with g, u the gemm_f8 of a with gate and up, each (w, w_scales), as
+    exact as gemm_f8's of that dtype; neither is stored."""
     (wg, sg), (wu, su) = gate, up
     y = (_bind or _load_bind()).swiglu_f8(a, a_scales, wg, sg, wu, su, dtype, out)
     if y is None:
@@ -765,10 +771,10 @@ def gemm_f8_swiglu_backward(dh: torch.Tensor, a: torch.Tensor, a_scales: torch.T
     """The gradients of gemm_f8_swiglu's g and u, side by side: d [M, 2 N] for dh [M, N],
     the gradient of y (float32, float16 or bfloat16).
 
-    g and u are computed again.  The gradient of the activations is d . [Wg; Wu] and
-    that of [Wg; Wu] is d^T . x, both gemm_f8 of d's codes: of quant_f8(d) with the
-    weights' quant_f8_block(.., "columns"), and of quant_f8_block(d, "columns") with
-    quant_f8_block(x, "columns")."""
+    g and u are computed again, as exact as gemm_f8's of that dtype.  The gradient of
+    the activations is d . [Wg; Wu] and that of [Wg; Wu] is d^T . x, both gemm_f8 of d's
+    codes: of quant_f8(d) with the weights' quant_f8_block(.., "columns"), and of
+    quant_f8_block(d, "columns") with quant_f8_block(x, "columns")."""
     (wg, sg), (wu, su) = gate, up
     d = None if dh is None else \
         (_bind or _load_bind()).swiglu_backward_f8(dh, a, a_scales, wg, sg, wu, su, dtype, out)

@@ -473,6 +473,22 @@ def test_gemm_of_quantised_values(M, N, K, t):
     assert rms < 0.5 * torch.finfo(TYPES[t]).eps + (2.0 ** -20 if t == "f32" else 2.0 ** -14)
 
 
+@pytest.mark.parametrize("M,N", [(1, 17), (40, 70), (300, 264), (700, 777)])
+@pytest.mark.parametrize("t", TYPES)
+def test_small_products_beside_large_ones(M, N, t):
+    """One product of 1 among seven of 1.875 * 2^-14, which the 8-bit unit may drop and float32 outputs may not."""
+    K = 272
+    a, w = np.full((M, K), 0x0F, dtype=np.uint8), np.full((N, K), 0x02, dtype=np.uint8)        # 1.875 * 2^-6, 2^-8
+    a[:, 3::8] = w[:, 3::8] = 0x38                                                              # 1
+    sa, sw = (np.ones((n, 3), dtype=np.float32) for n in (M, f8.blocks(N)))
+    want, bound = f8.product(a, sa, w, sw, t == "f32")
+    assert want[0, 0] == 34 * (1 + 7 * 1.875 * 2.0 ** -14)
+    y = q4.gemm_f8(dev(a), by_block(sa), dev(w), dev(sw), dtype=TYPES[t])
+    check(y, want, bound, t, f"{M} {N}")
+    if t == "f32":
+        same(y, torch.full((M, N), want[0, 0], dtype=torch.float64, device=DEV), f"{M} {N}")
+
+
 @pytest.mark.parametrize("M,N,K", REAL)
 @pytest.mark.parametrize("t", TYPES)
 def test_gates_of_quantised_values(M, N, K, t):
