@@ -657,10 +657,10 @@ __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_f8_block(Args p) {
 // been read: no barrier, and D - 1 blocks in flight while one is multiplied.
 // Blocks past K repeat the row's last 16 bytes against activations of zero.
 //
-// Eight rows take as many slots as fit, up to four: 1 x 28672 x 8192 in 41.2 us (43.7
-// with two), 4 x 14336 x 4096 gated 21.5 (22.7).  With more rows the operands come from
-// the L2, and workgroups side by side on a CU count for more: 333 x 896 x 4864 in
-// 32 x 16 10.7 with two, 17.3 with four.
+// Eight rows take as many slots as fit, up to four: 1 x 28672 x 8192 in 41.3 us (44.7
+// with two), 4 x 14336 x 4096 gated to bf16 21.4 (22.6), to float32 22.2 (23.1).  With
+// more rows the operands come from the L2, and workgroups side by side on a CU count
+// for more: 333 x 896 x 4864 in 32 x 16 10.7 with two, 17.3 with four.
 constexpr int few_slot(int FM, int FW) { return (2 * FW + 2 * FM) * 1024 + 256; }  // whole fragments, and the scales
 constexpr int few_depth(int W, int NX, int FW) {
     return NX == 1 ? std::min(4, 160 * 1024 / (W * few_slot(1, FW))) : 2;
@@ -1011,13 +1011,15 @@ int launch(const Args &p, Kernel k, const Target &to) {
         else {
             Args q = p;
             // One tile a CU, in rounds.  Where the last would have few, it goes to a
-            // launch of smaller tiles: 4600 x 4096 x 14336 (32 tiles left) takes 281 us so
-            // and 369 without, 5376 rows (80 left) 321 and 360, 1999 x 14336 x 4096
-            // gated (128 left) 227 and 238.
-            const int64_t all = tiles_of(p.M, 256) * tiles_of(p.N, TWO ? 128 : 256), left = all % kCUs;
-            if (all > kCUs && left && left <= kRestMost) {
+            // launch of smaller tiles.  With six sets of operands in turn 4600 x 4096 x
+            // 14336 (32 tiles left) takes 280 us so and 368 without, 5376 rows (80 left)
+            // 311 and 358, 1999 x 14336 x 4096 gated (128 left) 227 and 235 (222 with
+            // three sets, which the last cache holds in part).
+            const int64_t all = tiles_of(p.M, 256) * tiles_of(p.N, TWO ? 128 : 256);
+            const int whole = whole_rounds((int)all), left = (int)all - whole;
+            if (all > kCUs && left) {
                 q.part = kWhole;
-                q.whole = (int)(all - left);
+                q.whole = whole;
             }
             if (int st = launch_block<256, 256, kM, kN, 1, 2, MODE, false>(q, to)) return st;
             if (q.part == kAll) return Q4_OK;

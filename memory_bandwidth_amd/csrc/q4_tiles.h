@@ -17,11 +17,8 @@ constexpr int kCUs = 256;
 // Tiles of 256 x 256 come in rounds of one for each CU.  Where the last round
 // would have up to 128, they go to a launch of their own (kHalves, 128 rows
 // each, where there are more than 64; kQuarters, 128 x 128, else), which takes
-// one round of two thirds or a third of the time: 4600 x 4096 x 14336 (32 tiles
-// left) takes 223 us so and 315 without, 5376 rows (80 left) 251 and 316 (287
-// as quarters, in two rounds), 9000 x 8192 x 8192 (128 left) 461 and 481.
-// With groups the count is the GPU's to know: both are launched, and one has
-// no work.
+// one round of two thirds or a third of the time.  What it measured stands at
+// each kernel's choice.
 enum Part { kAll, kWhole, kHalves, kQuarters };
 constexpr int kRestMost = 128, kQuartersMost = 64;
 
