@@ -621,7 +621,9 @@ def gemm_i8_geometry(matrices: int, M: int, N: int, K: int, groups: int = 0) -> 
 # ---------------------------------------------------------------- 8-bit floating point
 #
 # Codes are torch.float8_e4m3fn; a scale stands for 128 values of a row, or for a
-# block of 128 x 128.
+# block of 128 x 128.  autograd does not see these calls: their results never
+# require grad, whatever the arguments do, and a training step makes the calls of
+# its backward pass itself, or from a torch.autograd.Function of its own.
 
 _F8 = torch.float8_e4m3fn
 
@@ -685,8 +687,10 @@ def quant_f8(x: torch.Tensor, out: tuple | None = None) -> tuple[torch.Tensor, t
     2^22.  A block with an Inf or a NaN gets the scale NaN and zero codes.
 
     New scales lie block by block (their .t() is contiguous), as the products read
-    them best; scales given with out may have any strides that give each of them
-    a place of its own."""
+    them best; scales given with out may have any strides, of up to 2^20 from row to
+    row and 2^31 from block to block, that give each of them a place of its own.
+
+    The results do not require grad, also where x does: no gradient passes through."""
     codes, scales = (None, None) if out is None else out
     got = (_bind or _load_bind()).quant_f8(x, codes, scales)
     if type(got) is tuple:
@@ -699,15 +703,15 @@ def quant_f8(x: torch.Tensor, out: tuple | None = None) -> tuple[torch.Tensor, t
 
 
 def quant_f8_block(x: torch.Tensor, layout: str = "rows", out: tuple | None = None) -> tuple:
-    """x [R, C] (float32, float16 or bfloat16, C a multiple of 16) to codes with
-    a scale for each 128 x 128 block, by quant_f8's rule.  By layout:
+    """x [R, C] (float32, float16 or bfloat16, C a multiple of 16, R below 2^22) to
+    codes with a scale for each 128 x 128 block, by quant_f8's rule.  By layout:
 
       "rows"     (codes [R, C], scales [ceil(R / 128), ceil(C / 128)])
       "columns"  (codes [C, R16], scales [ceil(C / 128), ceil(R / 128)]) of the transpose, R16 = R
                  rounded up to a multiple of 16 and the codes behind R zero
       "both"     all four, from one pass
 
-    The codes of a value are the same in both."""
+    The codes of a value are the same in both.  No gradient passes through, as in quant_f8."""
     if layout not in ("rows", "columns", "both"):
         raise ValueError(f"layout must be 'rows', 'columns' or 'both', got {layout!r}")
     as_is, turned = layout != "columns", layout != "rows"
@@ -733,9 +737,10 @@ def gemm_f8(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scales: 
             out: torch.Tensor | None = None) -> torch.Tensor:
     """y[M, N] = dequant(a)[M, K] . dequant(w)[N, K]^T (+ bias[N]).
 
-    a and w float8_e4m3fn; a_scales float32 [M, ceil(K / 128)], of any strides, or
-    one for each block of 128 rows too, [ceil(M / 128), ceil(K / 128)]; w_scales
-    float32 [ceil(N / 128), ceil(K / 128)]; bias float32.  y is of `dtype`
+    a and w float8_e4m3fn; a_scales float32 [M, ceil(K / 128)], of any strides up to
+    2^20 from row to row and 2^31 from block to block, or one for each block of 128
+    rows too, [ceil(M / 128), ceil(K / 128)]; w_scales float32
+    [ceil(N / 128), ceil(K / 128)]; bias float32.  y is of `dtype`
     (float32, float16 or bfloat16), and dtype chooses how exact the sums are.  K is
     a multiple of 16.
 
@@ -744,7 +749,10 @@ def gemm_f8(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scales: 
     eight consecutive k up to 7 * 2^-13 of the largest product: some 2^-16 of the
     result for normally distributed values, more than float16's own rounding
     where one product is far above its neighbours, and any part of a result whose
-    products cancel.  Ask for float32 there."""
+    products cancel.  Ask for float32 there.
+
+    y does not require grad, whatever a, the scales or bias do: the gradients are
+    products of their own (see gemm_f8_swiglu_backward)."""
     y = (_bind or _load_bind()).gemm_f8(a, a_scales, w, w_scales, bias, dtype, out)
     if y is None:
         _f8_refuse_product(a, a_scales, w, w_scales, bias, dtype, out)
@@ -756,7 +764,8 @@ def gemm_f8(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scales: 
 def gemm_f8_swiglu(a: torch.Tensor, a_scales: torch.Tensor, gate: tuple, up: tuple,
                    dtype=torch.float32, out: torch.Tensor | None = None) -> torch.Tensor:
     """y = silu(g) * u with g, u the gemm_f8 of a with gate and up, each (w, w_scales), as
-    exact as gemm_f8's of that dtype; neither is stored."""
+    exact as gemm_f8's of that dtype; neither is stored.  y does not require grad:
+    gemm_f8_swiglu_backward has the gradients of g and u."""
     (wg, sg), (wu, su) = gate, up
     y = (_bind or _load_bind()).swiglu_f8(a, a_scales, wg, sg, wu, su, dtype, out)
     if y is None:

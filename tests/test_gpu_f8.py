@@ -659,6 +659,33 @@ def test_gradient_against_differences():
         assert (np.abs(slope - d[:, N * i:N * i + N] * v) <= tol).all()
 
 
+def test_results_do_not_require_grad():
+    """As the docstrings say: autograd does not see the calls, and a Function of a program's own makes a step of them."""
+    x = torch.randn(40, 256, device=DEV, requires_grad=True)
+    w = torch.randn(384, 256, device=DEV, requires_grad=True)
+    codes, scales, codes_t, scales_t = q4.quant_f8_block(w, layout="both")
+    a, sa = q4.quant_f8(x)
+    y = q4.gemm_f8(a, sa.requires_grad_(), codes, scales)
+    assert not any(t.requires_grad for t in (a, codes, scales, codes_t, scales_t, y))
+    sa = sa.detach()
+
+    class Product(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, v):
+            return q4.gemm_f8(*q4.quant_f8(v), codes, scales)
+
+        @staticmethod
+        def backward(ctx, dy):
+            return q4.gemm_f8(*q4.quant_f8(dy), codes_t, scales_t)
+
+    got = Product.apply(x)
+    assert got.requires_grad and torch.equal(got, y)
+    dy = torch.randn(40, 384, device=DEV)
+    got.backward(dy)
+    want = q4.gemm_f8(*q4.quant_f8(dy), codes_t, scales_t)
+    assert torch.equal(x.grad, want) and w.grad is None
+
+
 # ---------------------------------------------------------------- streams, graphs, threads
 
 @pytest.mark.parametrize("T", [1, 20, 300])
