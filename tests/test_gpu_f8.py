@@ -591,6 +591,29 @@ def test_arrays_past_32_bits():
     assert np.array_equal(f8.decode(bits(cr[-n:, -256:])), f8.decode(cw)) and np.array_equal(bits(sr[-n:, -2:]), sw)
 
 
+@pytest.mark.parametrize("M,N", [(3, 40), (40, 200), (300, 264), (700, 777)])
+@pytest.mark.parametrize("strides", [(2 ** 20, 1), (1, 2 ** 31), (2 ** 20, 3)])
+@pytest.mark.parametrize("tall", [1, 128])
+def test_scales_as_far_apart_as_may_be(M, N, strides, tall):
+    """Scales of the largest strides, as quant_f8 writes them and as the products read them."""
+    K = 272
+    rows, KB = M if tall == 1 else f8.blocks(M), f8.blocks(K)
+    place = torch.zeros((rows - 1) * strides[0] + (KB - 1) * strides[1] + 1, device=DEV)
+    apart = place.as_strided((rows, KB), strides)
+    if tall == 1:
+        x = values_of(M, M, K, "bf16")
+        codes = torch.empty(M, K, dtype=F8, device=DEV)
+        q4.quant_f8(x.to(DEV), out=(codes, apart))
+        cw, sw = f8.quant(x.double().numpy())
+        assert np.array_equal(bits(apart), sw) and np.array_equal(f8.decode(bits(codes)), f8.decode(cw))
+        assert int((place != 0).sum()) == rows * KB
+    (a, sa), [w] = short_problem(M, N, K, tall=tall)
+    apart.copy_(dev(sa))
+    want = exact_on_gpu(dev(a), dev(sa), *pair(w))
+    for t in (torch.float32, torch.bfloat16):
+        same(q4.gemm_f8(dev(a), apart, *pair(w), dtype=t), want, f"{M} {N} {strides}")
+
+
 # ---------------------------------------------------------------- a layer's step
 
 def step(x, dy, gate, up, down):
