@@ -657,19 +657,19 @@ __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_f8_block(Args p) {
 // been read: no barrier, and D - 1 blocks in flight while one is multiplied.
 // Blocks past K repeat the row's last 16 bytes against activations of zero.
 //
-// Eight rows take as many slots as fit, up to four: 1 x 28672 x 8192 in 41.3 us (44.7
-// with two), 4 x 14336 x 4096 gated to bf16 21.4 (22.6), to float32 22.2 (23.1).  With
-// more rows the operands come from the L2, and workgroups side by side on a CU count
-// for more: 333 x 896 x 4864 in 32 x 16 10.7 with two, 17.3 with four.
+// Up to eight rows take as many slots as fit, up to four: 1 x 28672 x 8192 in 41.3 us
+// (44.7 with two), 4 x 14336 x 4096 gated to bf16 21.4 (22.6), to float32 22.2 (23.1).
+// With more rows the operands come from the L2, and workgroups side by side on a CU
+// count for more, whatever the tile: 333 x 896 x 4864 in 32 x 16 10.7 with two, 17.3
+// with four; to float32 in 8 x 16 329 x 933 x 288 gated 5.5 and 9.2, 200 x 333 x 2064
+// 5.3 and 7.1, and 12 x 4864 x 896 3.9 both.
 constexpr int few_slot(int FM, int FW) { return (2 * FW + 2 * FM) * 1024 + 256; }  // whole fragments, and the scales
-constexpr int few_depth(int W, int NX, int FW) {
-    return NX == 1 ? std::min(4, 160 * 1024 / (W * few_slot(1, FW))) : 2;
-}
+constexpr int few_most(int W, int FW) { return std::min(4, 160 * 1024 / (W * few_slot(1, FW))); }
 
-template <int NX, int FN, Mode MODE, bool F16, int W>
+template <int NX, int FN, Mode MODE, bool F16, int W, int D>
 __global__ __launch_bounds__(W * 64) void gemm_f8_few(Args p, int ks_log2) {
     constexpr int FM = (NX + 1) / 2, BM = 8 * NX, MATS = MODE == kPlain ? 1 : 2, FW = FN * MATS;
-    constexpr int D = few_depth(W, NX, FW), LOADS = 2 * FW + NX + 1;    // load instructions of a block
+    constexpr int LOADS = 2 * FW + NX + 1;                              // load instructions of a block
     constexpr int SLOT = few_slot(FM, FW);                              // the last fragment may be half loaded
     extern __shared__ __align__(16) char lds[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -834,11 +834,11 @@ Split split_of(const Args &p, int bm, int cols, int most) {
     return s;
 }
 
-template <int NX, int FN, Mode MODE, bool F16, int W>
+template <int NX, int FN, Mode MODE, bool F16, int W, int D>
 int launch_few(Args p, const Split &s, const Target &to) {
     constexpr int FM = (NX + 1) / 2, FW = MODE == kPlain ? FN : 2 * FN;
-    constexpr int kLds = W * few_depth(W, NX, FW) * few_slot(FM, FW);
-    static_assert(kLds <= 160 * 1024 && few_depth(W, NX, FW) >= 2, "the rings fit, with a block on its way");
+    constexpr int kLds = W * D * few_slot(FM, FW);
+    static_assert(kLds <= 160 * 1024 && D >= 2, "the rings fit, with a block on its way");
     // 128 x 8192 x 8192, tiles of 64 x 32: 32.6 us with, 36.9 without.
     p.share = s.tiles > 1;
     // Weights that one row tile reads pass the caches by: the next layers'
@@ -853,8 +853,16 @@ int launch_few(Args p, const Split &s, const Target &to) {
     const int64_t grid = s.tiles * p.tiles_n;
     if (grid * (W * 64) > kMaxThreads) return Q4_EINVAL;
     if (to.report) return planned(to, 8 * NX, (W >> s.log2) * 16 * FN, grid, W * 64);
-    gemm_f8_few<NX, FN, MODE, F16, W><<<(unsigned)grid, W * 64, kLds, to.stream>>>(p, s.log2);
+    gemm_f8_few<NX, FN, MODE, F16, W, D><<<(unsigned)grid, W * 64, kLds, to.stream>>>(p, s.log2);
     return q4::launch_status();
+}
+
+template <int NX, int FN, Mode MODE, bool F16, int W>
+int launch_few(const Args &p, const Split &s, const Target &to) {
+    if constexpr (NX == 1)
+        if (s.tiles == 1)
+            return launch_few<NX, FN, MODE, F16, W, few_most(W, MODE == kPlain ? FN : 2 * FN)>(p, s, to);
+    return launch_few<NX, FN, MODE, F16, W, 2>(p, s, to);
 }
 
 template <int NX, int FN, Mode MODE, bool F16, int MOST = 8>
