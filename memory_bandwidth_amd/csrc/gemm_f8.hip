@@ -899,14 +899,15 @@ int launch_block(Args p, const Target &to) {
 
 enum Kernel { kFew8, kFew16, kFew32, kFew32x32, kFew64, kTile64, kTile128, kTileWide, kTile256, kTileDeep, kKernels };
 
-// Estimated times, in us.  Tiles: for one, and for a step of it (`many`: where a
-// CU has several, each of them); tiles that have a CU to themselves come in
-// whole rounds.  Few rows: the start, a block of a wavefront alone and for each of
-// the CU's (of two matrices), the blocks that the ring's first wait stands for; and,
-// as the weights are read past the L2 again for every row tile, a MB of them,
-// what each more row tile adds of that, and what the cache takes off.  64 x 64
-// tiles are for where there is one for each CU at most; 32 x 32 and 64 x 32 for one
-// matrix.
+// Estimates that order the kernels by their times, in us.  Tiles: for one, and for
+// a step of it (`many`: where a CU has several, each of them); tiles that have a CU
+// to themselves come in whole rounds.  Few rows: the start, a block of a wavefront
+// alone and for each of the CU's (of two matrices), the blocks that the ring's first
+// wait stands for; and, as the weights are read past the L2 again for every row
+// tile, a MB of them, what each more row tile adds of that, and what is taken off.
+// 64 x 64 tiles are for where there is one for each CU at most; 32 x 32 and 64 x 32
+// for one matrix.  The constants are the fit's: one by itself is no time that was
+// measured (starts below zero are none), and all are of the kernels as they were then.
 struct Linear { double start, step; double at(int64_t steps) const { return start + step * (double)steps; } };
 struct FewCost { double start, block, shared, shared_two, first; };
 struct Costs {
@@ -917,9 +918,11 @@ struct Costs {
     Linear tile64, tile128, tile128_many, wide, tile256;
 };
 // Fitted to 1370 calls (9 to 8192 rows, N 64 to 14336, K 128 to 14336, one matrix and
-// two; up to six sets of operands in turn, in a graph).  Of 370 of them, timed again,
-// the choice was on average 1.8% behind the best time of any kernel for 16-bit
-// outputs and 2.9% for float32, 11% and 13% or more in one of twenty.  Where they
+// two; up to six sets of operands in turn, in a graph), those of eight rows to fewer
+// and before.  Of 2400 others (perf/fit_gemm_f8.py, which fits them anew) the choice
+// was on average 1.6% behind the best kernel for 16-bit outputs, 10% or more in one of
+// twenty; for float32 4.1% and 18%, mostly where eight-row tiles are taken for more
+// rows: they are estimated too low (50 x 588 x 2160 gated 7.2 us, 4.4 in 16 x 16).  Where they
 // decide: 64 x 4096 x 14336 takes 21.1 us in tiles of 32 x 32, 26.5 in 32 x 16, 28.5
 // in 64 x 32 and 39.3 in 64 x 64; at 128 rows these are 32.2, 42.1, 27.3 and 38.1.
 // 1024 x 4096 x 4096 takes 26.7 us in 128 x 128, 29.0 in 64 x 128 and 31.8 in 128 x

@@ -3,7 +3,9 @@ library exports what include/q4f8.h declares, refuses bad arguments before it
 touches the device, and the oracle agrees with worked values, with exact
 arithmetic and, for gradients, with differences."""
 
+import importlib.util
 import os
+import random
 import re
 import subprocess
 from fractions import Fraction
@@ -195,6 +197,22 @@ def test_geometry_refusals(L):
         with pytest.raises(q4.Q4Error):
             q4.gemm_f8_geometry(*shape)
     assert q4.gemm_f8_geometry(1, 0, 8, 64)["grid"] == 0
+
+
+@pytest.mark.parametrize("t", ["bf16", "f32"])
+def test_fit_script_has_the_librarys_choice(L, t):
+    """perf/fit_gemm_f8.py, which fits the constants of the choice, estimates as the library does."""
+    spec = importlib.util.spec_from_file_location("fit_gemm_f8", os.path.join(ROOT, "perf", "fit_gemm_f8.py"))
+    fit = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(fit)
+    rng = random.Random(3)
+    shapes = [fit.draw(rng)[:4] for _ in range(1000)]
+    shapes += [[rng.randint(1, 200), rng.randint(1, 5000), 16 * rng.randint(1, 20), rng.choice([1, 2])]
+               for _ in range(500)]
+    calls = fit.Calls(t, shapes)
+    for i, ((M, N, K, mats), kernel) in enumerate(zip(shapes, calls.choose(fit.constants(t)))):
+        g = q4.gemm_f8_geometry(mats, M, N, K, torch.float32 if t == "f32" else torch.bfloat16)
+        assert (g["tile_rows"], g["tile_cols"]) == calls.tile(i, kernel), (M, N, K, mats)
 
 
 # ---------------------------------------------------------------- the oracle
