@@ -918,11 +918,12 @@ struct Costs {
     Linear tile64, tile128, tile128_many, wide, tile256;
 };
 // Fitted to 1370 calls (9 to 8192 rows, N 64 to 14336, K 128 to 14336, one matrix and
-// two; up to six sets of operands in turn, in a graph), those of eight rows to fewer
-// and before.  Of 2400 others (perf/fit_gemm_f8.py, which fits them anew) the choice
-// was on average 1.6% behind the best kernel for 16-bit outputs, 10% or more in one of
-// twenty; for float32 4.1% and 18%, mostly where eight-row tiles are taken for more
-// rows: they are estimated too low (50 x 588 x 2160 gated 7.2 us, 4.4 in 16 x 16).  Where they
+// two; up to six sets of operands in turn, in a graph), the eight-row kernel's to
+// fewer and earlier ones.  Of 2400 others (perf/fit_gemm_f8.py, which fits them anew)
+// the choice was on average 1.6% behind the best kernel for 16-bit outputs, 10% or
+// more in one of twenty; for float32 4.1% and 18%, mostly where eight-row tiles are
+// taken for more rows: they are estimated too low (50 x 588 x 2160 gated 7.2 us, 4.4
+// in 16 x 16).  Where they
 // decide: 64 x 4096 x 14336 takes 21.1 us in tiles of 32 x 32, 26.5 in 32 x 16, 28.5
 // in 64 x 32 and 39.3 in 64 x 64; at 128 rows these are 32.2, 42.1, 27.3 and 38.1.
 // 1024 x 4096 x 4096 takes 26.7 us in 128 x 128, 29.0 in 64 x 128 and 31.8 in 128 x
