@@ -6,7 +6,9 @@ int4 group-128 matrices K=4096 x N=14336 (976,224,256 B of codes, scales and
 zero points, more than L2 + Infinity Cache) cycled at M=1.  One step is one
 pass over the 32 matrices (32 gemv_q4 calls, replayed from one HIP graph).
 W warm-up steps, then exactly K timed steps between two device syncs, timed
-with HIP events on the stream the graph runs on.  Prints ONE JSON line.
+with HIP events on the stream the graph runs on.  Prints ONE JSON line, short
+enough for a log that keeps some thousand characters of a run: of the tables
+below it has the rates (brief()); --details FILE writes all of each.
 
 Alongside, in the same process and in ABBA order (forward, then reversed), the
 measurement method of cera 0.5.0 wgpu_gemv_bench.rs is applied to three
@@ -475,7 +477,40 @@ def run_default(args):
     if not args.no_cpu:
         log("timing the CPU oracle on a bounded sample ...")
         line["cpu_baseline"] = cpu_baseline(args.cpu_seconds)
-    print(json.dumps(line), flush=True)
+    if args.details:
+        with open(args.details, "w") as f:
+            json.dump(line, f, indent=1)
+    print(json.dumps(brief(line)), flush=True)
+
+
+def brief(line: dict) -> dict:
+    """The record of a run with its tables down to rates in GB/s (of the two-point
+    cells: the median us a launch too; of the sweep, one list for the sizes in
+    KiB).  What is no table stays as it is."""
+    out = dict(line)
+    whole = lambda v: v if v is None else round(v)                            # noqa: E731
+    if out.get("two_point"):
+        out["two_point"] = {k: {"us": r["per_launch_us"]["median"] and round(r["per_launch_us"]["median"], 3),
+                                "GBps": r["GBps_median"] and round(r["GBps_median"], 1), "noise_cells": r["noise_cells"]}
+                            for k, r in out["two_point"].items()}
+    if "configs" in out:
+        c = out["configs"]
+        out["configs"] = {"GBps": {r["name"]: r["GBps_median"]
+                                   for r in c["cells_cache_resident"] + c["cells_hbm_streaming"]}}
+        if "cpu_oracle" in c:
+            out["configs"]["cpu_oracle_GBps"] = {k: [r["one_thread"]["GBps"], r["all_threads"]["GBps"]]
+                                                 for k, r in c["cpu_oracle"].items()}
+    if "block_formats" in out:
+        out["block_formats"] = {f: {shape: r["GBps"] for shape, r in t.items()}
+                                for f, t in out["block_formats"].items()}
+    if "ffn_rows" in out:
+        out["ffn_rows"] = {shape: {str(r["M"]): r["GBps"] for r in t["cells"]} for shape, t in out["ffn_rows"].items()}
+    if "bandwidth_sweep" in out:
+        b = out["bandwidth_sweep"]
+        out["bandwidth_sweep"] = {"KiB": [n >> 10 for n in b["sizes"]],
+                                  **{k: {"GBps": [whole(r["GBps_median"]) for r in b[k]["best"]], "cliffs": b[k]["cliffs"]}
+                                     for k in ("read_reduce", "copy")}}
+    return out
 
 
 # ---------------------------------------------------------------- the per-config table
@@ -1581,6 +1616,7 @@ def main(argv=None):
     ap.add_argument("--config-cpu-seconds", type=float, default=3.0,
                     help="CPU oracle seconds per config of the table (half on one thread, half on all)")
     ap.add_argument("--no-sweep", action="store_true", help="skip the 16 KiB - 2 GiB bandwidth sweep")
+    ap.add_argument("--details", default="", metavar="FILE", help="write the whole record, every cell of its tables, to FILE")
     ap.add_argument("--blocks-only", action="store_true", help="only the block-format cells")
     ap.add_argument("--block-shapes", default="",
                     help="with --blocks-only: comma list of shape labels (stream, 'lm head', ..., scan, layer, ffn, sweep)")

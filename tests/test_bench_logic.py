@@ -193,3 +193,53 @@ def test_with_floor_records_the_fraction():
     out = bench.with_floor(rec, {"stats": {"median": 8e-6}})
     assert out["single_launch_floor_us"] == 8.0 and out["frac_of_single_launch_floor"] == 0.8
     assert "single_launch_floor_us" not in rec
+
+
+def record():
+    """A run's record with tables of the default run's sizes."""
+    stat = {"median": 7.801587227731942, "min": 7.7, "p10": 7.7, "p90": 7.9}
+    cell = lambda name: {"kernel": "gemv_q4", "bytes_per_launch": 464128, "us_per_launch": stat, "runs": 5,  # noqa: E731
+                         "GBps_median": 4176.1, "frac_of_spec": 0.022, "config": "c", "name": name}
+    two = {"per_launch_us": stat, "GBps_median": 3910.35, "GBps_best": 3948.3, "noise_cells": 0, "resolvable_cells": 9}
+    best = [{"grid": 4, "passes": 4096, "GBps_median": 126.6}] * 18
+    shapes = ("stream", "ffn gate/up", "ffn down", "attn qkv/out", "lm head")
+    oracle = {"one_thread": {"GBps": 0.1}, "all_threads": {"GBps": 0.4}}
+    line = {"metric": "m", "value": 3808.55, "unit": "GB/s", "n_gpus": 1, "steps": 20, "warmup": 5, "ms_per_step": 0.25632,
+            "higher_is_better": True, "scaling": "weak", "vs_baseline": None, "dtype": "i32+f32", "data": "synthetic",
+            "config": {"workload": "w" * 100, "arithmetic": "a" * 260}, "roofline": {"frac": 0.4761},
+            "two_point": {k: dict(two) for k in ("gemv_q4", "gemv_f32", "read_reduce", "gemv_q4_swiglu")},
+            "configs": {"cells_cache_resident": [cell(f"ffn up 4096->14336 g128 M={i}, one matrix looped") for i in range(12)],
+                        "cells_hbm_streaming": [cell(f"read_reduce over {i} distinct 78.7 MB buffers (one launch each)")
+                                                for i in range(12)],
+                        "cpu_oracle": {k: oracle for k in ("gemv-896", "decoder-layer", "lm-head", "ffn-8b")}},
+            "block_formats": {f: {s: {"N": 1, "us_per_launch": 2.5, "GBps": 651.8} for s in shapes}
+                              for f in ("q4_0", "q8_0", "q4_k", "q5_k", "q6_k")},
+            "ffn_rows": {s: {"cells": [{"M": m, "GBps": 3932.5} for m in (1, 2, 4, 8)]} for s in ("up", "down")},
+            "bandwidth_sweep": {"sizes": [16384 << i for i in range(18)], "read_reduce": {"best": best, "cliffs": [67108864]},
+                                "copy": {"best": best, "cliffs": [33554432]}},
+            "cpu_baseline": {"value": 1.83, "unit": "GB/s", "kind": "oracle"}}
+    return line
+
+
+def test_the_line_is_short_and_whole():
+    """A log that keeps the last 16,000 characters of a run, 9,000 of them of what goes to stderr, holds the line."""
+    line = record()
+    before = json.dumps(line)
+    out = bench.brief(line)
+    assert json.dumps(line) == before and len(json.dumps(out)) < 5500 and "\n" not in json.dumps(out)
+    tables = {"two_point", "configs", "block_formats", "ffn_rows", "bandwidth_sweep"}
+    assert list(out) == list(line)
+    assert all(out[k] == line[k] for k in line if k not in tables)
+    assert out["two_point"]["gemv_q4"] == {"us": 7.802, "GBps": round(3910.35, 1), "noise_cells": 0}
+    assert len(out["configs"]["GBps"]) == 24 and out["configs"]["cpu_oracle_GBps"]["lm-head"] == [0.1, 0.4]
+    assert out["block_formats"]["q6_k"]["lm head"] == 651.8 and out["ffn_rows"]["up"]["8"] == 3932.5
+    sweep = out["bandwidth_sweep"]
+    assert len(sweep["KiB"]) == len(sweep["copy"]["GBps"]) == 18 and sweep["KiB"][0] == 16
+
+
+def test_the_line_without_its_tables():
+    line = {k: v for k, v in record().items() if k not in ("configs", "block_formats", "ffn_rows", "bandwidth_sweep")}
+    line["two_point"] = None
+    assert bench.brief(line) == line
+    line["two_point"] = {"gemv_q4": {"per_launch_us": {"median": None}, "GBps_median": None, "noise_cells": 9}}
+    assert bench.brief(line)["two_point"]["gemv_q4"] == {"us": None, "GBps": None, "noise_cells": 9}
