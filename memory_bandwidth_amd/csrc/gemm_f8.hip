@@ -604,7 +604,9 @@ __global__ __launch_bounds__(WM * WN * G * 64, 2) void gemm_f8_block(Args p) {
             if (more) {
                 aim(nxt);
                 // The place is that of the tile before this one: a barrier since then says that
-                // every wavefront has read it.  With D steps there has been none.
+                // every wavefront has read it.  With D steps there has been none.  (Fetched
+                // behind the next step's barrier instead, it has the largest tiles spill;
+                // bf16 8192 x 4096 x 256 takes 25.2 us so, 26.0 without a bias.)
                 if (!TWO && p.bias && steps == D) barrier();
                 load_bias(nxt, biases + (side ^ 1) * BN);
             }
